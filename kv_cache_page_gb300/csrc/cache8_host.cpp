@@ -105,7 +105,7 @@ uint32_t page_units(const C8Params& p) {
 }
 
 struct Split {
-  uint32_t units, splits, chunk;
+  uint32_t units, splits, chunk, warps;
   uint64_t ticket_bytes, bytes;
 };
 
@@ -122,10 +122,19 @@ Split step_split(const C8Params& p, const kv_cache8_batch* b, uint32_t window) {
   if (window) keys = std::min<uint64_t>(keys, (uint64_t)window + kvc::kStepRows + 15u);
   keys = std::max<uint64_t>(keys, 16u);
   const uint64_t jobs = std::max<uint64_t>((uint64_t)s.units * p.H, 1u);
-  const uint64_t slots = (uint64_t)kvc::kC8Sms * (p.D == 256 ? 2 : 3) * (b->n_seqs == 1 ? 1 : 8);
-  uint64_t chunk = (keys * jobs + slots - 1) / slots;
-  chunk = (std::max<uint64_t>(chunk, 128u) + 15u) & ~15ull;
-  s.splits = (uint32_t)std::min<uint64_t>((keys + chunk - 1) / chunk, 4096u);
+  const uint32_t big = p.D == 256 ? 8u : 12u;
+  uint64_t chunk;
+  if (b->n_seqs == 1 || jobs * ((keys + 32 * big - 1) / (32 * big)) <= kvc::kC8Sms) {
+    // one sequence, or so little work that every CTA has an SM of its own: CTAs of as many warps as an
+    // SM holds, which join their warps in shared memory and leave few ranges to join through memory
+    s.warps = big;
+    chunk = std::max<uint64_t>((keys * jobs + kvc::kC8Sms - 1) / kvc::kC8Sms, 32u * big);
+  } else {
+    s.warps = 4;
+    chunk = std::max<uint64_t>((keys * jobs + 24u * kvc::kC8Sms - 1) / (24u * kvc::kC8Sms), 128u);
+  }
+  chunk = (chunk + 31u) & ~31ull;
+  s.splits = (uint32_t)std::min<uint64_t>((keys + chunk - 1) / chunk, kvc::kMaxSplits);
   s.chunk = (uint32_t)chunk;
   s.ticket_bytes = s.splits > 1 ? (jobs * 4u + 255u) & ~255ull : 0u;
   s.bytes = s.splits > 1 ? s.ticket_bytes + jobs * s.splits * (kvc::kStepRows * (p.D + 2ull) * 4u) : 0u;
@@ -264,6 +273,7 @@ int kv_cache8_attend(kv_cache8_t h, const kv_cache8_layer* layer, const kv_cache
   p.n_units = sp.units;
   p.splits = sp.splits;
   p.chunk = sp.chunk;
+  p.step_warps = sp.warps;
   p.min_rows = 1;
   p.max_rows = 0xffffffffu;
   p.tickets = static_cast<uint32_t*>(workspace);

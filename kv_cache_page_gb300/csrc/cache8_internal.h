@@ -12,6 +12,7 @@ constexpr uint32_t kC8Sms = 152;  // SMs of a GB300: what the split rules count 
 // Row tiles of the attention: consecutive (token, query head of the group)
 // pairs r = i * G + g of one sequence and KV head.
 constexpr uint32_t kStepRows = 16;
+constexpr uint32_t kMaxSplits = 256;  // ranges of a row tile's keys (the joining CTA holds 8 bytes a range and row)
 constexpr uint32_t kPromptRows = 128;
 
 struct C8Params {
@@ -42,6 +43,7 @@ struct C8Params {
   uint32_t window;              // 0: none
   uint32_t causal;
   uint32_t splits;              // ranges a row tile's keys are split into, at most
+  uint32_t step_warps;          // warps of a step CTA: 4, or as many as an SM holds (12; 8 for D = 256)
   uint32_t chunk;               // keys of a range (more where splits ranges of it do not reach)
   uint32_t min_rows, max_rows;  // sequences this launch serves: G * new within [min_rows, max_rows]
   uint32_t n_units;             // row tiles (step, prompt) or page units (write, read), an upper bound

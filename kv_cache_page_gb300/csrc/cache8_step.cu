@@ -6,28 +6,33 @@
 // Bound by reading the codes once (2 D bytes a token and KV head).  A CTA takes
 // a row tile of one sequence and KV head (16 rows: the G query heads that share
 // the KV head, times the new tokens) over one range of its keys; its warps walk
-// the range 16 tokens at a time, each on its own, and join at the end.  Ranges
-// of one row tile are joined by the CTA that finishes last, in range order, so
-// the result does not depend on timing.
+// the range 32 tokens at a time (16 for D = 256), each on its own, and join at the
+// end.  Ranges of one row tile are joined by the CTA that finishes last, in range
+// order, so the result does not depend on timing.
 //
-// Tiles go from global memory to the lane that needs them: the order in which
-// dims and tokens are fed to the 16x8x16 matrix products is free as long as both
+// A warp copies its tiles asynchronously into shared memory slots of its own
+// (cp.async), a stage or more ahead; no barrier is needed in the walk.  The order
+// in which dims are fed to the 16x8x16 score product is free as long as both
 // operands agree, and is chosen such that a lane's K fragment is 16 contiguous
-// codes of a token and its V fragment 16 contiguous codes of four tokens.  Each
-// lane copies these asynchronously into shared memory slots of its own
-// (cp.async), several tiles ahead: no lane reads another's slot, so the walk
-// needs no barrier.  Codes become FP16 exactly; K's scale multiplies the scores,
+// codes of a token, read from slots that the lane itself copied.  V's fragments
+// need runs of tokens at one dim: 16 x 16 byte tiles transposed by ldmatrix, rows
+// swizzled over the banks.  The tokens of a 16-token tile are dealt to the score
+// product's columns such that its result is the second product's operand as it
+// stands (see tok_of).  Codes become FP16 exactly; K's scale multiplies the scores,
 // V's scale the weights.
+//
+// What the walk costs besides bytes is instructions: 64 conversions and 32
+// products per 16 tokens and D = 128 are the floor.
 #include "cache8_common.cuh"
 
 namespace kvc {
 namespace {
 
-constexpr int kStepWarps = 4;
 constexpr float kNegInf = -INFINITY;
-// Weights are held as 2^(z - m) * 2^11 (in the factor that carries V's scale): FP16 then keeps 11 bits down to 2^-25
-// of the row's largest weight, below that 2^-36 of it.  m may lag the true maximum
-// by kLag (fewer rescalings of the sums): 2^(11 + kLag) = 2^15 < 65504.
+// Weights are held as 2^(z - m) * 2^11 (in the factor that carries V's scale):
+// FP16 then keeps 11 bits down to 2^-25 of the row's largest weight, below that
+// 2^-36 of it.  m may lag the true maximum by kLag (fewer rescalings of the sums):
+// 2^(11 + kLag) = 2^15 < 65504.
 constexpr float kLift = 2048.0f, kLag = 4.0f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -63,29 +68,52 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Two 16 x 16 byte tiles, transposed: lanes 0-15 give the rows' addresses of the
+// first, lanes 16-31 of the second; r0, r1 (second: r2, r3) hold rows 4 (lane & 3)
+// .. + 3 of column lane >> 2 and of column (lane >> 2) + 8.
+__device__ __forceinline__ void ldsm_t16x2(uint32_t (&r)[4], uint32_t smem) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem));
+}
+
 template <int D>
 struct StepShape {
+  static constexpr int TS = D == 256 ? 16 : 32;        // tokens of a warp's step
+  static constexpr int HT = TS / 16;                   // 16-token tiles of a step
   static constexpr int CH = D >= 64 ? 16 : 8;          // bytes of a K copy
   static constexpr int KC = D / 4 / CH;                // K copies of a lane and token
-  static constexpr int VB = D / 8 >= 16 ? 16 : D / 8;  // bytes of a V copy
-  static constexpr int VC = D / 8 / VB;                // V copies of a lane and token
   static constexpr int KS = D / 16;                    // k-steps of the score product
   static constexpr int NT = D / 8;                     // 8-wide column tiles of the output
-  static constexpr int kTile = 32 * (2 * KC * CH + 4 * VC * VB);  // bytes of K and V of 16 tokens
-};
-
-// Shared memory of a warp's slots: [stage][K copies, V copies, scales][lane].
-template <int D, bool PAGED16>
-struct StepSmem {
-  using S = StepShape<D>;
-  static constexpr int kScales = PAGED16 ? 2 : 8;      // FP32 words of a lane: K and V scales
-  static constexpr int kStage = S::kTile + 32 * 4 * kScales;
-  static constexpr int kStages = D == 256 ? 3 : D == 128 ? 4 : D == 64 ? 6 : 8;
+  static constexpr int VR = 512 / D;                   // token rows that a warp's 16-byte V copies cover
+  static constexpr int kK = TS * D;                    // bytes of a stage's K and of its V
+  static constexpr int kStage = 2 * kK + 8 * TS;       // and FP32 scales of K and V per token
+  static constexpr int kStages = D == 256 ? 3 : D == 128 ? 2 : D == 64 ? 3 : 4;
   static constexpr int kQ = 16 * D * 2;
-  static constexpr int kJoin = kStepWarps * 16 * (D + 4) * 4;  // the warps' sums, over the slots
-  static constexpr int kSlots = kStepWarps * kStages * kStage;
-  static constexpr int kBytes = kQ + 512 + (kSlots > kJoin ? kSlots : kJoin);
+  static constexpr int kSmall = 2048;                  // rows' factors, maxima, sums
 };
+template <int D, int W>
+constexpr int step_smem() {
+  using S = StepShape<D>;
+  constexpr int slots = W * S::kStages * S::kStage, join = W * 16 * (D + 4) * 4;
+  constexpr int ranges = (int)kMaxSplits * 16 * 8;
+  return S::kQ + S::kSmall + (slots > join ? (slots > ranges ? slots : ranges) : (join > ranges ? join : ranges));
+}
+
+// Column c of score tile h (8 wide) of a 16-token tile is token
+// 4 (c >> 1) + (c & 1) + 2 h: the lane that holds columns 2 q, 2 q + 1 of both score
+// tiles then holds tokens 4 q .. 4 q + 3, as ldmatrix deals V's rows.
+__device__ __forceinline__ uint32_t tok_of(uint32_t c, uint32_t h) { return 4u * (c >> 1) + (c & 1u) + 2u * h; }
+
+// Byte offset of 16-byte chunk c of token row t in a V tile: 8 consecutive rows
+// of one chunk lie in 8 different bank groups.
+template <int D>
+__device__ __forceinline__ uint32_t v_at(uint32_t t, uint32_t c) {
+  constexpr uint32_t R = D / 16;  // chunks of a row
+  if (R >= 8) return t * D + ((c ^ (t & 7u)) << 4);
+  if (R == 4) return t * D + ((c ^ ((t >> 1) & 3u)) << 4);
+  return t * D + ((c ^ ((t >> 2) & 1u)) << 4);
+}
 
 // loads of what other CTAs of this launch have stored (L2)
 __device__ __forceinline__ float2 ld_join2(const float* ptr) {
@@ -97,29 +125,18 @@ __device__ __forceinline__ float4 ld_join4(const float* ptr) {
   return __ldcg(reinterpret_cast<const float4*>(ptr));
 }
 
-// One bit per byte of w that is an E4M3 NaN.
+// The high bit of each byte of w that is an E4M3 NaN.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
-// 4 tokens x 4 dims: word t holds token t's codes of dims 0..3; out word d the
-// codes of tokens 0..3 at dim d.
-__device__ __forceinline__ void transpose4(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, uint32_t (&o)[4]) {
-  const uint32_t a = __byte_perm(w0, w1, 0x5140), b = __byte_perm(w2, w3, 0x5140);  // (0,0')(1,1')
-  const uint32_t c = __byte_perm(w0, w1, 0x7362), d = __byte_perm(w2, w3, 0x7362);
-  o[0] = __byte_perm(a, b, 0x5410);
-  o[1] = __byte_perm(a, b, 0x7632);
-  o[2] = __byte_perm(c, d, 0x5410);
-  o[3] = __byte_perm(c, d, 0x7632);
-}
-
-// PAGED16: pages are whole 16-token tiles, so a tile has one page and one pair
-// of scales; otherwise each lane looks its tokens' pages up by itself.
-template <int DT, int D, bool PAGED16>
-__global__ void __launch_bounds__(kStepWarps * 32) c8_step_kernel(const __grid_constant__ C8Params p) {
+// PAGED16: pages are whole 16-token tiles, so a tile lies in one page; otherwise
+// every token's page is looked up by itself.
+template <int DT, int D, bool PAGED16, int W>
+__global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
+    c8_step_kernel(const __grid_constant__ C8Params p) {
   using S = StepShape<D>;
-  using M = StepSmem<D, PAGED16>;
-  constexpr int NS = M::kStages;
+  constexpr int NS = S::kStages, TS = S::TS, HT = S::HT;
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
   const uint32_t g = lane >> 2, qd = lane & 3u;
@@ -134,26 +151,107 @@ __global__ void __launch_bounds__(kStepWarps * 32) c8_step_kernel(const __grid_c
 
   // the keys that some row of the tile sees
   const int32_t first_pos = q.start + (int32_t)(r0 / p.G), last_pos = q.start + (int32_t)((r0 + n_rows - 1u) / p.G);
-  int32_t hi = p.causal ? min(q.len, last_pos + 1) : q.len;
-  int32_t lo = p.window ? max(0, first_pos - (int32_t)min(p.window, 0x7fffffffu) + 1) : 0;
-  hi = max(hi, 0);
-  if (first_pos < 0) lo = 0;
+  const int32_t hi = max(p.causal ? min(q.len, last_pos + 1) : q.len, 0);
+  int32_t lo = p.window && first_pos >= 0 ? max(0, first_pos - (int32_t)min(p.window, 0x7fffffffu) + 1) : 0;
   lo &= ~15;  // tiles start at multiples of 16
   const uint32_t keys = hi > lo ? (uint32_t)(hi - lo) : 0u;
   // ranges: p.chunk keys each, longer where p.splits of them would not reach
   uint32_t chunk = p.chunk;
-  if ((uint64_t)chunk * p.splits < keys) chunk = ((keys + p.splits - 1) / p.splits + 15u) & ~15u;
+  if ((uint64_t)chunk * p.splits < keys) chunk = ((keys + p.splits - 1) / p.splits + 31u) & ~31u;
   const uint32_t n_split = keys ? (keys + chunk - 1) / chunk : 1u;
   if (split >= n_split) return;
   const int32_t c_lo = lo + (int32_t)(split * chunk);
   const int32_t c_hi = (int32_t)min((int64_t)hi, (int64_t)c_lo + chunk);
+  const int32_t n_steps = (c_hi - c_lo + TS - 1) / TS;
+
+  uint8_t* my_slots = smem + S::kQ + S::kSmall + warp * (NS * S::kStage);
+  const uint32_t slots = (uint32_t)__cvta_generic_to_shared(my_slots);
+  bool bad = false;
+  uint32_t holes = 0;  // bit s: a token of stage s has no page
+
+  // this lane's copies: K tokens (h, t) at dims of its quad; V rows lane / (D / 16) + VR i
+  const uint8_t* k_src = p.k + (int64_t)head * p.sh + qd * S::CH;
+  const uint8_t* v_src = p.v + (int64_t)head * p.sh + (lane % (D / 16)) * 16;
+  const uint32_t v_row = lane / (D / 16);
+
+  // raw table entry of this lane's token of step t, one step ahead of its use
+  auto entry_of = [&](int32_t t) -> int32_t {
+    const int32_t tok = c_lo + TS * t + (int32_t)(lane % TS);
+    if (tok >= c_hi) return -2;
+    const uint32_t i = c8_div_t(p, (uint32_t)tok);
+    return i < p.table_width ? ldg_i32(p.tables + (int64_t)q.s * p.table_stride + i) : -1;
+  };
+  auto issue = [&](int32_t t, int stage, int32_t entry) {
+    const uint32_t at = slots + stage * S::kStage;
+    const int32_t tok0 = c_lo + TS * t, tok = tok0 + (int32_t)(lane % TS);
+    const bool ok = (uint32_t)entry < p.num_blocks;
+    const uint32_t hole = __ballot_sync(0xffffffffu, !ok && entry != -2);
+    holes = (holes & ~(1u << stage)) | (hole ? 1u << stage : 0u);
+    bad |= hole != 0u;
+    const uint32_t in_page = (uint32_t)tok - c8_div_t(p, (uint32_t)tok) * p.T;
+    const int64_t off = ok ? (int64_t)entry * p.sb + (int64_t)in_page * p.st : -1;
+    const int64_t si = ok ? (int64_t)entry * p.H + head : 0;
+    if (lane < TS) {
+      cp_async<4>(at + 2 * S::kK + lane * 4, p.k_scale + si, ok);
+      cp_async<4>(at + 2 * S::kK + 4 * TS + lane * 4, p.v_scale + si, ok);
+    }
+#pragma unroll
+    for (int t16 = 0; t16 < HT; ++t16) {
+      if (PAGED16) {
+        // a tile's tokens all lie in its first token's page (those past the length hold anything)
+        const int64_t base = __shfl_sync(0xffffffffu, off, 16 * t16);
+        const bool has = base >= 0;
+        const int64_t b = has ? base : 0;
+        const uint8_t* ks = k_src + b + (int64_t)tok_of(g, 0) * p.st;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int c = 0; c < S::KC; ++c)
+            cp_async<S::CH>(at + (((t16 * 2 + h) * S::KC + c) * 32 + lane) * S::CH,
+                            (has ? ks + h * 2 * p.st : k_src) + c * 4 * S::CH, has);
+        const uint8_t* vs = v_src + b;
+#pragma unroll
+        for (int i = 0; i < 16 / S::VR; ++i) {
+          const uint32_t r = v_row + i * S::VR;
+          cp_async<16>(at + S::kK + v_at<D>(16 * t16 + r, lane % (D / 16)), has ? vs + (int64_t)r * p.st : v_src, has);
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int64_t b = __shfl_sync(0xffffffffu, off, 16 * t16 + tok_of(g, h));
+#pragma unroll
+          for (int c = 0; c < S::KC; ++c)
+            cp_async<S::CH>(at + (((t16 * 2 + h) * S::KC + c) * 32 + lane) * S::CH, k_src + (b >= 0 ? b : 0) + c * 4 * S::CH,
+                            b >= 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 16 / S::VR; ++i) {
+          const uint32_t r = v_row + i * S::VR;
+          const int64_t b = __shfl_sync(0xffffffffu, off, 16 * t16 + r);
+          cp_async<16>(at + S::kK + v_at<D>(16 * t16 + r, lane % (D / 16)), v_src + (b >= 0 ? b : 0), b >= 0);
+        }
+      }
+    }
+  };
+
+  int32_t entry = entry_of((int32_t)warp);
+#pragma unroll
+  for (int s = 0; s < NS - 1; ++s) {
+    const int32_t t = (int32_t)warp + s * W;
+    if (t < n_steps) {
+      const int32_t e = entry;
+      entry = entry_of(t + W);
+      issue(t, s, e);
+    }
+    cp_commit();
+  }
 
   // Q as FP16 fragments, rows scaled by a power of two into FP16's range (bf16;
   // exact but for values 2^-39 of the row's largest): lane (g, qd) of k-step
   // 4 c + i holds dims 64 c + 16 qd + 4 i .. + 3 (D = 32: 8 qd + 4 i) of rows g, g + 8.
   uint32_t* s_q = reinterpret_cast<uint32_t*>(smem);
-  float* s_row = reinterpret_cast<float*>(smem + M::kQ);  // per row: scale * log2(e) / row scaling
-  {
+  float* s_row = reinterpret_cast<float*>(smem + S::kQ);  // per row: scale * log2(e) / row scaling
+  if (W == 4 || tid < 128u) {
     // 8 threads to a row; each converts D / 8 dims
     const uint32_t r = tid >> 3, part = tid & 7u;
     constexpr int PER = D / 8;
@@ -198,7 +296,7 @@ __global__ void __launch_bounds__(kStepWarps * 32) c8_step_kernel(const __grid_c
 #pragma unroll
     for (int k = 0; k < PER / 2; ++k) {
       const uint32_t dim = part * PER + 2 * k;
-      uint32_t ks, l4, pair;
+      uint32_t ks, l4;
       if (D >= 64) {
         ks = (dim >> 6) * 4 + ((dim >> 2) & 3u);
         l4 = (dim >> 4) & 3u;
@@ -206,11 +304,9 @@ __global__ void __launch_bounds__(kStepWarps * 32) c8_step_kernel(const __grid_c
         ks = (dim >> 2) & 1u;
         l4 = (dim >> 3) & 3u;
       }
-      pair = (dim >> 1) & 1u;
       // fragment registers: a0 (row g, k lo), a1 (row g + 8, k lo), a2 (row g, k hi), a3 (row g + 8, k hi)
-      s_q[(ks * 32 + (r & 7u) * 4 + l4) * 4 + pair * 2 + (r >> 3)] = w[k];
+      s_q[(ks * 32 + (r & 7u) * 4 + l4) * 4 + ((dim >> 1) & 1u) * 2 + (r >> 3)] = w[k];
     }
-    // two factors so that neither under- nor overflows alone
     if (part == 0) s_row[r] = p.scale_log2 * __uint_as_float((uint32_t)(127 - ex) << 23);
   }
   __syncthreads();
@@ -227,8 +323,8 @@ __global__ void __launch_bounds__(kStepWarps * 32) c8_step_kernel(const __grid_c
     if (r >= n_rows || pos < 0) vis_hi[h] = 0;
     rf[h] = s_row[r];
   }
-  // tiles between these need no mask
-  const int32_t full_hi = first_pos < 0 ? 0 : p.causal ? min(q.len, first_pos + 1) : q.len;
+  // steps between these need no mask
+  const int32_t full_hi = min(c_hi, first_pos < 0 ? 0 : p.causal ? min(q.len, first_pos + 1) : q.len);
   const int32_t full_lo = p.window ? (int32_t)max((int64_t)0, (int64_t)last_pos - p.window + 1) : 0;
 
   float o[S::NT][4];
@@ -237,116 +333,36 @@ __global__ void __launch_bounds__(kStepWarps * 32) c8_step_kernel(const __grid_c
   float m[2] = {kNegInf, kNegInf}, l[2] = {0.0f, 0.0f};
   float vref = 1.17549435e-38f, vinv = 0.0f;  // V scales are held relative to the largest so far
 
-  const uint32_t slots = (uint32_t)__cvta_generic_to_shared(smem + M::kQ + 512) + warp * (NS * M::kStage);
-  const int32_t n_tiles = (c_hi - c_lo + 15) / 16;
-  const uint8_t* kbase = p.k + (int64_t)head * p.sh;
-  const uint8_t* vbase = p.v + (int64_t)head * p.sh;
-  bool bad = false;
-
-  // page of tile t's tokens (PAGED16), one tile ahead of its use
-  auto page_of = [&](int32_t t) -> int32_t {
-    const int32_t tok = c_lo + 16 * t;
-    return tok < c_hi ? c8_page(p, q.s, c8_div_t(p, (uint32_t)tok)) : -2;
-  };
-  auto issue = [&](int32_t t, int stage, int32_t id) {
-    const uint32_t at = slots + stage * M::kStage;
-    const int32_t tok0 = c_lo + 16 * t;
-    if (PAGED16) {
-      const uint32_t in_page = (uint32_t)tok0 - c8_div_t(p, (uint32_t)tok0) * p.T;
-      const bool page_ok = id >= 0;
-      if (id == -1) bad = true;
-      const int64_t off = page_ok ? (int64_t)id * p.sb + (int64_t)in_page * p.st : 0;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t tt = g + 8 * h;
-        const bool ok = page_ok && tok0 + (int32_t)tt < c_hi;
-        const uint8_t* src = kbase + (ok ? off + (int64_t)tt * p.st : 0);
-#pragma unroll
-        for (int c = 0; c < S::KC; ++c)
-          cp_async<S::CH>(at + ((h * S::KC + c) * 32 + lane) * S::CH, src + c * 4 * S::CH + qd * S::CH, ok);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t tt = 2 * qd + (i & 1) + 8 * (i >> 1);
-        const bool ok = page_ok && tok0 + (int32_t)tt < c_hi;
-        const uint8_t* src = vbase + (ok ? off + (int64_t)tt * p.st : 0);
-#pragma unroll
-        for (int c = 0; c < S::VC; ++c)
-          cp_async<S::VB>(at + 2 * S::KC * 32 * S::CH + ((i * S::VC + c) * 32 + lane) * S::VB,
-                          src + c * 8 * S::VB + g * S::VB, ok);
-      }
-      const int64_t si = page_ok ? (int64_t)id * p.H + head : 0;
-      cp_async<4>(at + S::kTile + lane * 4, p.k_scale + si, page_ok);
-      cp_async<4>(at + S::kTile + 128 + lane * 4, p.v_scale + si, page_ok);
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int32_t tok = tok0 + (int32_t)(g + 8 * h);
-        bool ok = tok < c_hi;
-        const uint32_t pi = c8_div_t(p, (uint32_t)tok);
-        const int32_t pid = ok ? c8_page(p, q.s, pi) : -1;
-        if (ok && pid < 0) bad = true;
-        ok = ok && pid >= 0;
-        const uint8_t* src = kbase + (ok ? (int64_t)pid * p.sb + (int64_t)((uint32_t)tok - pi * p.T) * p.st : 0);
-#pragma unroll
-        for (int c = 0; c < S::KC; ++c)
-          cp_async<S::CH>(at + ((h * S::KC + c) * 32 + lane) * S::CH, src + c * 4 * S::CH + qd * S::CH, ok);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int32_t tok = tok0 + (int32_t)(2 * qd + (i & 1) + 8 * (i >> 1));
-        bool ok = tok < c_hi;
-        const uint32_t pi = c8_div_t(p, (uint32_t)tok);
-        const int32_t pid = ok ? c8_page(p, q.s, pi) : -1;
-        ok = ok && pid >= 0;
-        const uint8_t* src = vbase + (ok ? (int64_t)pid * p.sb + (int64_t)((uint32_t)tok - pi * p.T) * p.st : 0);
-#pragma unroll
-        for (int c = 0; c < S::VC; ++c)
-          cp_async<S::VB>(at + 2 * S::KC * 32 * S::CH + ((i * S::VC + c) * 32 + lane) * S::VB,
-                          src + c * 8 * S::VB + g * S::VB, ok);
-        // a scale of 0 marks a token without a page
-        const int64_t si = ok ? (int64_t)pid * p.H + head : 0;
-        cp_async<4>(at + S::kTile + (i * 32 + lane) * 4, p.k_scale + si, ok);
-        cp_async<4>(at + S::kTile + ((4 + i) * 32 + lane) * 4, p.v_scale + si, ok);
-      }
-    }
-  };
-
-  int32_t next_id = PAGED16 ? page_of((int32_t)warp) : 0;
-#pragma unroll
-  for (int s = 0; s < NS - 1; ++s) {
-    const int32_t t = (int32_t)warp + s * kStepWarps;
-    const int32_t id = next_id;
-    if (t < n_tiles) {
-      if (PAGED16) next_id = page_of(t + kStepWarps);
-      issue(t, s, id);
-    }
-    cp_commit();
-  }
   int stage = 0;
-  for (int32_t t = (int32_t)warp; t < n_tiles; t += kStepWarps) {
+  for (int32_t t = (int32_t)warp; t < n_steps; t += W) {
     {
-      const int32_t tn = t + (NS - 1) * kStepWarps;
+      const int32_t tn = t + (NS - 1) * W;
       const int sn = stage == 0 ? NS - 1 : stage - 1;
-      if (tn < n_tiles) {
-        const int32_t id = next_id;
-        if (PAGED16) next_id = page_of(tn + kStepWarps);
-        issue(tn, sn, id);
+      __syncwarp();  // every lane is done with the stage that is refilled
+      if (tn < n_steps) {
+        const int32_t e = entry;
+        entry = entry_of(tn + W);
+        issue(tn, sn, e);
       }
       cp_commit();
       cp_wait<NS - 1>();
+      __syncwarp();  // V and the scales were copied by other lanes
     }
-    const uint8_t* sp = smem + M::kQ + 512 + warp * (NS * M::kStage) + stage * M::kStage;
+    const uint8_t* sp = my_slots + stage * S::kStage;
+    const uint32_t sv = slots + stage * S::kStage + S::kK;
+    const bool hole = (holes >> stage) & 1u;
     stage = stage == NS - 1 ? 0 : stage + 1;
-    const int32_t tok0 = c_lo + 16 * t;
+    const int32_t tok0 = c_lo + TS * t;
 
-    // scores of 16 tokens: s[h][.] for tokens 8 h + 2 qd, + 1
-    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    // scores: s[2 t16 + h][.] of columns 2 qd, + 1 of rows g, g + 8
+    float s[2 * HT][4];
+#pragma unroll
+    for (int h = 0; h < 2 * HT; ++h) s[h][0] = s[h][1] = s[h][2] = s[h][3] = 0.0f;
 #pragma unroll
     for (int c = 0; c < S::KC; ++c) {
-      uint32_t kw[2][4];
+      uint32_t kw[2 * HT][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < 2 * HT; ++h) {
         const uint8_t* at = sp + ((h * S::KC + c) * 32 + lane) * S::CH;
         if (S::CH == 16) {
           const uint4 x = *reinterpret_cast<const uint4*>(at);
@@ -360,39 +376,50 @@ __global__ void __launch_bounds__(kStepWarps * 32) c8_step_kernel(const __grid_c
       for (int i = 0; i < S::CH / 4; ++i) {
         const uint4 a = *reinterpret_cast<const uint4*>(s_q + ((c * (S::CH / 4) + i) * 32 + lane) * 4);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2 * HT; ++h) {
           uint32_t b0, b1;
           c8_dec4(kw[h][i], b0, b1);
           mma16816(s[h], a.x, a.y, a.z, a.w, b0, b1);
         }
       }
     }
-    float ks[4], vs[4];
-    if (PAGED16) {
-      ks[0] = ks[1] = ks[2] = ks[3] = *reinterpret_cast<const float*>(sp + S::kTile + lane * 4);
-      vs[0] = vs[1] = vs[2] = vs[3] = *reinterpret_cast<const float*>(sp + S::kTile + 128 + lane * 4);
-    } else {
+    // scales of tokens 16 t16 + 4 qd .. + 3; column (h, e) of a tile is token 2 h + e of these
+    float vt = 0.0f;
+    float4 vs[HT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        ks[i] = *reinterpret_cast<const float*>(sp + S::kTile + (i * 32 + lane) * 4);
-        vs[i] = *reinterpret_cast<const float*>(sp + S::kTile + ((4 + i) * 32 + lane) * 4);
+    for (int t16 = 0; t16 < HT; ++t16) {
+      const uint32_t i = PAGED16 ? 16 * t16 : 16 * t16 + 4 * qd;
+      const float4 k4 = *reinterpret_cast<const float4*>(sp + 2 * S::kK + i * 4);
+      vs[t16] = *reinterpret_cast<const float4*>(sp + 2 * S::kK + 4 * TS + i * 4);
+      if (PAGED16) {
+        const float f0 = k4.x * rf[0], f1 = k4.x * rf[1];
+#pragma unroll
+        for (int h = 2 * t16; h < 2 * t16 + 2; ++h) {
+          s[h][0] *= f0; s[h][1] *= f0;
+          s[h][2] *= f1; s[h][3] *= f1;
+        }
+        vt = fmaxf(vt, vs[t16].x);
+      } else {
+        s[2 * t16][0] *= k4.x * rf[0]; s[2 * t16][1] *= k4.y * rf[0];
+        s[2 * t16][2] *= k4.x * rf[1]; s[2 * t16][3] *= k4.y * rf[1];
+        s[2 * t16 + 1][0] *= k4.z * rf[0]; s[2 * t16 + 1][1] *= k4.w * rf[0];
+        s[2 * t16 + 1][2] *= k4.z * rf[1]; s[2 * t16 + 1][3] *= k4.w * rf[1];
+        vt = fmaxf(vt, fmaxf(fmaxf(vs[t16].x, vs[t16].y), fmaxf(vs[t16].z, vs[t16].w)));
       }
     }
-    // tokens without a page have the scale 0 of a skipped copy
-    const bool no_page = PAGED16 ? ks[0] == 0.0f : __any_sync(0xffffffffu, ks[0] == 0.0f || ks[1] == 0.0f || ks[2] == 0.0f || ks[3] == 0.0f);
-    const bool masked = no_page || tok0 + 16 > full_hi || tok0 < full_lo;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[h][e] = (s[h][e] * ks[2 * h + (e & 1)]) * rf[e >> 1];
+    const bool masked = hole || tok0 + TS > full_hi || tok0 < full_lo;
     if (masked) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2 * HT; ++h)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int32_t tok = tok0 + (int32_t)(8 * h + 2 * qd + (e & 1));
+          const uint32_t i = 16 * (h >> 1) + 4 * qd + 2 * (h & 1) + (e & 1);
+          const int32_t tok = tok0 + (int32_t)i;
           const int r = e >> 1;
-          if (tok >= vis_hi[r] || tok < vis_lo[r] || ks[2 * h + (e & 1)] == 0.0f) s[h][e] = kNegInf;
+          // a token without a page has the scale 0 of a skipped copy
+          if (tok >= min(vis_hi[r], c_hi) || tok < vis_lo[r] ||
+              (hole && *reinterpret_cast<const float*>(sp + 2 * S::kK + i * 4) == 0.0f))
+            s[h][e] = kNegInf;
         }
     }
     // running maxima; the sums are rescaled only where a maximum grew by more than kLag
@@ -400,13 +427,14 @@ __global__ void __launch_bounds__(kStepWarps * 32) c8_step_kernel(const __grid_c
     float mt[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      float x = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+      float x = fmaxf(s[0][2 * r], s[0][2 * r + 1]);
+#pragma unroll
+      for (int h = 1; h < 2 * HT; ++h) x = fmaxf(x, fmaxf(s[h][2 * r], s[h][2 * r + 1]));
       x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
       x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
       mt[r] = x;
       grow |= x > m[r] + kLag;  // -inf + kLag = -inf: any finite score of a fresh row
     }
-    float vt = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
     if (!PAGED16) {
       vt = fmaxf(vt, __shfl_xor_sync(0xffffffffu, vt, 1));
       vt = fmaxf(vt, __shfl_xor_sync(0xffffffffu, vt, 2));
@@ -430,101 +458,86 @@ __global__ void __launch_bounds__(kStepWarps * 32) c8_step_kernel(const __grid_c
         }
       }
     }
-    float vr[4];
+    const float b0 = m[0] == kNegInf ? 0.0f : m[0], b1 = m[1] == kNegInf ? 0.0f : m[1];
+    uint32_t pa[HT][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) vr[i] = PAGED16 && i ? vr[0] : vs[i] * vinv;
-    uint32_t pa[4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float base = m[r] == kNegInf ? 0.0f : m[r];
-        const float p0 = ex2(s[h][2 * r] - base), p1 = ex2(s[h][2 * r + 1] - base);
-        l[r] += p0 + p1;
-        // a weight of 0 stays 0 whatever the scale (a masked token of a page that holds infinities)
-        const float w0 = p0 == 0.0f ? 0.0f : p0 * vr[2 * h], w1 = p1 == 0.0f ? 0.0f : p1 * vr[2 * h + 1];
-        pa[2 * h + r] = pack2<0>(w0, w1);
-      }
-    // V: the lane's four tokens, transposed to pairs of tokens per dim
-    uint32_t any_nan = 0;
-#pragma unroll
-    for (int c = 0; c < S::VC; ++c) {
-      uint32_t vw[4][S::VB / 4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint8_t* at = sp + 2 * S::KC * 32 * S::CH + ((i * S::VC + c) * 32 + lane) * S::VB;
-        if (S::VB == 16) {
-          const uint4 x = *reinterpret_cast<const uint4*>(at);
-          vw[i][0] = x.x;
-          vw[i][1 % (S::VB / 4)] = x.y;
-          vw[i][2 % (S::VB / 4)] = x.z;
-          vw[i][3 % (S::VB / 4)] = x.w;
-        } else if (S::VB == 8) {
-          const uint2 x = *reinterpret_cast<const uint2*>(at);
-          vw[i][0] = x.x;
-          vw[i][1 % (S::VB / 4)] = x.y;
-        } else {
-          vw[i][0] = *reinterpret_cast<const uint32_t*>(at);
-        }
-      }
-      if (masked) {
-        // a NaN that some row does not see must not reach it through 0 * NaN:
-        // NaN codes become 0 here and are put back below where they are seen
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int k = 0; k < S::VB / 4; ++k) {
-            const uint32_t nb = nan_bytes(vw[i][k]);
-            any_nan |= nb;
-            vw[i][k] &= ~((nb >> 7) * 0xffu);
-          }
-      }
-#pragma unroll
-      for (int k = 0; k < S::VB / 4; ++k) {
-        uint32_t tr[4];
-        transpose4(vw[0][k], vw[1][k], vw[2][k], vw[3][k], tr);
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          uint32_t b0, b1;
-          c8_dec4(tr[d], b0, b1);
-          mma16816(o[c * S::VB + 4 * k + d], pa[0], pa[1], pa[2], pa[3], b0, b1);
-        }
-      }
-    }
-    if (masked && __any_sync(0xffffffffu, any_nan != 0u)) {
-      // rows x dims where a visible token's value is NaN: count them with the same product
-      uint32_t seen[4];
+    for (int t16 = 0; t16 < HT; ++t16) {
+      const float w4[4] = {vs[t16].x * vinv, (PAGED16 ? vs[t16].x : vs[t16].y) * vinv,
+                           (PAGED16 ? vs[t16].x : vs[t16].z) * vinv, (PAGED16 ? vs[t16].x : vs[t16].w) * vinv};
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-          seen[2 * h + r] = (s[h][2 * r] == kNegInf ? 0u : 0x3c00u) | (s[h][2 * r + 1] == kNegInf ? 0u : 0x3c000000u);
+        for (int r = 0; r < 2; ++r) {
+          const float z0 = s[2 * t16 + h][2 * r], z1 = s[2 * t16 + h][2 * r + 1];
+          const float p0 = ex2(z0 - (r ? b1 : b0)), p1 = ex2(z1 - (r ? b1 : b0));
+          l[r] += p0 + p1;
+          float x0 = p0 * w4[2 * h], x1 = p1 * w4[2 * h + 1];
+          if (masked) {  // 0 whatever the scale of the page that holds a token the row does not see
+            x0 = z0 == kNegInf ? 0.0f : x0;
+            x1 = z1 == kNegInf ? 0.0f : x1;
+          }
+          pa[t16][2 * h + r] = pack2<0>(x0, x1);
+        }
+    }
+    // V: words of four tokens (4 qd .. + 3) at dims 8 n + g
+    uint32_t any_nan = 0;
 #pragma unroll
-      for (int c = 0; c < S::VC; ++c)
+    for (int t16 = 0; t16 < HT; ++t16)
 #pragma unroll
-        for (int k = 0; k < S::VB / 4; ++k) {
-          uint32_t w[4], tr[4];
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t vw[4];
+        ldsm_t16x2(vw, sv + v_at<D>(16 * t16 + (lane & 15u), 2 * c + (lane >> 4)));
+        if (masked) {
+          // a NaN that some row does not see must not reach it through 0 * NaN:
+          // NaN codes become 0 here and are put back below where they are seen
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            w[i] = *reinterpret_cast<const uint32_t*>(
-                       sp + 2 * S::KC * 32 * S::CH + ((i * S::VC + c) * 32 + lane) * S::VB + 4 * k);
-          transpose4(nan_bytes(w[0]), nan_bytes(w[1]), nan_bytes(w[2]), nan_bytes(w[3]), tr);
-#pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            // 0x80 bytes -> 1.0 halves
-            const uint32_t b0 = (tr[d] & 0x80u ? 0x3c00u : 0u) | (tr[d] & 0x8000u ? 0x3c000000u : 0u);
-            const uint32_t b1 = (tr[d] & 0x800000u ? 0x3c00u : 0u) | (tr[d] & 0x80000000u ? 0x3c000000u : 0u);
-            float cnt[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816(cnt, seen[0], seen[1], seen[2], seen[3], b0, b1);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (cnt[e] > 0.0f) o[c * S::VB + 4 * k + d][e] = __int_as_float(0x7fffffff);
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t nb = nan_bytes(vw[k]);
+            any_nan |= nb;
+            vw[k] &= ~((nb >> 7) * 0xffu);
           }
         }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t v0, v1;
+          c8_dec4(vw[k], v0, v1);
+          mma16816(o[4 * c + k], pa[t16][0], pa[t16][1], pa[t16][2], pa[t16][3], v0, v1);
+        }
+      }
+    if (masked && __any_sync(0xffffffffu, any_nan != 0u)) {
+      // rows x dims where a visible token's value is NaN: count them with the same product
+#pragma unroll 1
+      for (int t16 = 0; t16 < HT; ++t16) {
+        uint32_t seen[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float z0 = t16 ? s[2 * (HT - 1) + h][2 * r] : s[h][2 * r];
+            const float z1 = t16 ? s[2 * (HT - 1) + h][2 * r + 1] : s[h][2 * r + 1];
+            seen[2 * h + r] = (z0 == kNegInf ? 0u : 0x3c00u) | (z1 == kNegInf ? 0u : 0x3c000000u);
+          }
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t vw[4];
+          ldsm_t16x2(vw, sv + v_at<D>(16 * t16 + (lane & 15u), 2 * c + (lane >> 4)));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t nb = nan_bytes(vw[k]);  // 0x80 bytes -> 1.0 halves
+            const uint32_t v0 = (nb & 0x80u ? 0x3c00u : 0u) | (nb & 0x8000u ? 0x3c000000u : 0u);
+            const uint32_t v1 = (nb & 0x800000u ? 0x3c00u : 0u) | (nb & 0x80000000u ? 0x3c000000u : 0u);
+            float cnt[4] = {0.f, 0.f, 0.f, 0.f};
+            mma16816(cnt, seen[0], seen[1], seen[2], seen[3], v0, v1);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (cnt[e] > 0.0f) o[4 * c + k][e] = __int_as_float(0x7fffffff);
+          }
+        }
+      }
     }
   }
   cp_wait<0>();
-  if (PAGED16 ? (bad && lane == 0u) : bad) c8_error(p, q.s, KV_CACHE8_BAD_PAGE);
+  if (bad && lane == 0u) c8_error(p, q.s, KV_CACHE8_BAD_PAGE);
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
@@ -532,14 +545,15 @@ __global__ void __launch_bounds__(kStepWarps * 32) c8_step_kernel(const __grid_c
   }
 
   // ---- join the warps: every row to the largest maximum among them
-  __syncthreads();
-  float* s_m = reinterpret_cast<float*>(smem + M::kQ);  // [row][warp] maxima, then the tile's
-  float* s_o = reinterpret_cast<float*>(smem + M::kQ + 512);  // [warp][16][D + 4]
-  float* s_l = reinterpret_cast<float*>(smem);          // [row][warp]
+  float* s_m = s_row + 16;               // [row][warp] maxima
+  float* s_l = s_m + 16 * W;             // [row][warp] sums, at the row's maximum
+  float2* s_fin = reinterpret_cast<float2*>(smem);  // row: maximum and 1 / sum, over Q once no warp needs that
+  float* s_o = reinterpret_cast<float*>(smem + S::kQ + S::kSmall);  // [warp][16][D + 4], over the slots
+  static_assert((16 + 32 * W) * 4 + 128 <= S::kSmall, "");
   constexpr int OS = D + 4;
   if (qd == 0) {
-    s_m[g * kStepWarps + warp] = m[0];
-    s_m[(g + 8) * kStepWarps + warp] = m[1];
+    s_m[g * W + warp] = m[0];
+    s_m[(g + 8) * W + warp] = m[1];
   }
   __syncthreads();
 #pragma unroll
@@ -547,115 +561,139 @@ __global__ void __launch_bounds__(kStepWarps * 32) c8_step_kernel(const __grid_c
     const uint32_t row = g + 8 * r;
     float mx = kNegInf;
 #pragma unroll
-    for (int w = 0; w < kStepWarps; ++w) mx = fmaxf(mx, s_m[row * kStepWarps + w]);
+    for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_m[row * W + w]);
     const float f = m[r] == kNegInf ? 0.0f : ex2(m[r] - mx);
     const float fo = m[r] == kNegInf ? 0.0f : f * (vref * (1.0f / kLift));
-    if (qd == 0) s_l[row * kStepWarps + warp] = l[r] * f;
-    // column 2 qd + e of tile n is dim (2 qd + e) * VB + (n mod VB) of its 8 VB dims
-    float* dst = s_o + (warp * 16 + row) * OS;
+    if (qd == 0) s_l[row * W + warp] = l[r] * f;
+    // column 2 qd + e of tile n is dim 8 n + 2 qd + e
+    float* dst = s_o + (warp * 16 + row) * OS + 2 * qd;
 #pragma unroll
-    for (int c = 0; c < S::VC; ++c)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int k = 0; k < S::VB; k += 4) {
-          const int n = c * S::VB + k;
-          *reinterpret_cast<float4*>(dst + c * 8 * S::VB + (2 * qd + e) * S::VB + k) =
-              make_float4(o[n][2 * r + e] * fo, o[n + 1][2 * r + e] * fo, o[n + 2][2 * r + e] * fo,
-                          o[n + 3][2 * r + e] * fo);
-        }
+    for (int n = 0; n < S::NT; ++n)
+      *reinterpret_cast<float2*>(dst + 8 * n) = make_float2(o[n][2 * r] * fo, o[n][2 * r + 1] * fo);
   }
   __syncthreads();
-  // 8 threads to a row, D / 8 dims each (4 at a time, 32 apart)
-  const uint32_t row = tid >> 3, part = tid & 7u;
-  float mx = kNegInf, ls = 0.0f;
+  const uint32_t job = u * p.H + head;
+  float* base = p.partials + (uint64_t)job * p.splits * (kStepRows * (D + 2));
+  float* mine = base + (uint64_t)split * (kStepRows * (D + 2));
+  // a row's maximum and sum: to the outputs, or to the range's record
+  auto finish_row = [&](uint32_t row, float mx, float ls) {
+    s_fin[row] = make_float2(mx, ls == 0.0f ? 0.0f : 1.0f / ls);
+    if (p.lse && row < n_rows) {
+      const uint32_t rr = r0 + row, tok = rr / p.G, hd = head * p.G + rr - tok * p.G;
+      st4(p.lse + ((int64_t)q.row + tok) * p.HQ + hd,
+          __float_as_uint(ls == 0.0f ? kNegInf : (mx + log2f(ls)) * 0.693147180559945309f));
+    }
+  };
+  auto finish_out = [&](uint32_t r, uint32_t d4, float4 x) {
+    const float inv = s_fin[r].y;
+    const uint32_t rr = r0 + r, tok = rr / p.G, hd = head * p.G + rr - tok * p.G;
+    st8(p.b + ((int64_t)q.row + tok) * p.b_row + (int64_t)hd * p.b_head + d4 * 4,
+        inv == 0.0f ? make_uint2(0, 0)
+                    : make_uint2(pack2<DT>(x.x * inv, x.y * inv), pack2<DT>(x.z * inv, x.w * inv)));
+  };
+  if (tid < n_rows) {
+    float mx = kNegInf, ls = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kStepWarps; ++w) {
-    mx = fmaxf(mx, s_m[row * kStepWarps + w]);
-    ls += s_l[row * kStepWarps + w];
+    for (int w = 0; w < W; ++w) {
+      mx = fmaxf(mx, s_m[tid * W + w]);
+      ls += s_l[tid * W + w];
+    }
+    if (n_split > 1u) st8(mine + kStepRows * D + 2 * tid, make_uint2(__float_as_uint(mx), __float_as_uint(ls)));
+    else finish_row(tid, mx, ls);
   }
-  float acc[D / 8];
-#pragma unroll
-  for (int c = 0; c < D / 32; ++c) {
+  if (n_split == 1u) __syncthreads();
+  for (uint32_t c4 = tid; c4 < n_rows * (D / 4); c4 += W * 32) {
+    const uint32_t r = c4 / (D / 4), d4 = c4 % (D / 4);
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < kStepWarps; ++w) {
-      const float4 y = *reinterpret_cast<const float4*>(s_o + (w * 16 + row) * OS + c * 32 + part * 4);
+    for (int w = 0; w < W; ++w) {
+      const float4 y = *reinterpret_cast<const float4*>(s_o + (w * 16 + r) * OS + d4 * 4);
       x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
     }
-    acc[4 * c] = x.x; acc[4 * c + 1] = x.y; acc[4 * c + 2] = x.z; acc[4 * c + 3] = x.w;
+    if (n_split > 1u)
+      st16(mine + r * D + d4 * 4, make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(x.z),
+                                             __float_as_uint(x.w)));
+    else finish_out(r, d4, x);
   }
-  const uint32_t job = u * p.H + head;
-  if (n_split > 1u) {
-    // ---- leave the range's sums; the last CTA of the job joins the ranges
-    float* base = p.partials + (uint64_t)job * p.splits * (kStepRows * (D + 2));
-    float* mine = base + (uint64_t)split * (kStepRows * (D + 2));
-    if (row < n_rows) {
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c)
-        st16(mine + row * D + c * 32 + part * 4,
-             make_uint4(__float_as_uint(acc[4 * c]), __float_as_uint(acc[4 * c + 1]), __float_as_uint(acc[4 * c + 2]),
-                        __float_as_uint(acc[4 * c + 3])));
-      if (part == 0) st8(mine + kStepRows * D + 2 * row, make_uint2(__float_as_uint(mx), __float_as_uint(ls)));
+  if (n_split == 1u) return;
+
+  // ---- the last CTA of the row tile joins the ranges
+  __syncthreads();
+  uint32_t* s_last = reinterpret_cast<uint32_t*>(s_m);
+  if (tid == 0) {
+    uint32_t last = 0;
+    KVC_GUARD(p.tickets + job, 4, last = 2);
+    if (last == 0) {
+      __threadfence();
+      last = atomicAdd(p.tickets + job, 1u) == n_split - 1u ? 1u : 0u;
+      if (last) p.tickets[job] = 0;  // as the next call finds it
+      __threadfence();
     }
-    __syncthreads();
-    uint32_t* s_last = reinterpret_cast<uint32_t*>(smem + M::kQ);
-    if (tid == 0) {
-      uint32_t last = 0;
-      KVC_GUARD(p.tickets + job, 4, last = 2);
-      if (last == 0) {
-        __threadfence();
-        last = atomicAdd(p.tickets + job, 1u) == n_split - 1u ? 1u : 0u;
-        if (last) p.tickets[job] = 0;  // as the next call finds it
-        __threadfence();
-      }
-      *s_last = last;
+    *s_last = last;
+  }
+  __syncthreads();
+  if (*s_last != 1u) return;
+  // maxima and sums of all ranges at once, then a range's factor in place of its maximum
+  float2* s_ml = reinterpret_cast<float2*>(smem + S::kQ + S::kSmall);  // [range][16 rows], over the slots
+  for (uint32_t k0 = tid; k0 < n_split * kStepRows; k0 += W * 32 * 4) {
+    float2 y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t k = k0 + i * W * 32;
+      if (k < n_split * kStepRows && k % kStepRows < n_rows)
+        y[i] = ld_join2(base + (uint64_t)(k / kStepRows) * (kStepRows * (D + 2)) + kStepRows * D + 2 * (k % kStepRows));
+      else y[i] = make_float2(kNegInf, 0.0f);
     }
-    __syncthreads();
-    if (*s_last != 1u) return;
-    // maxima first, then the sums, in range order
-    mx = kNegInf;
-    if (row < n_rows)
-      for (uint32_t k = 0; k < n_split; ++k)
-        mx = fmaxf(mx, ld_join2(base + (uint64_t)k * (kStepRows * (D + 2)) + kStepRows * D + 2 * row).x);
-    ls = 0.0f;
 #pragma unroll
-    for (int k = 0; k < D / 8; ++k) acc[k] = 0.0f;
-    if (row < n_rows)
-      for (uint32_t k = 0; k < n_split; ++k) {
-        const float* part_k = base + (uint64_t)k * (kStepRows * (D + 2));
-        const float2 ml = ld_join2(part_k + kStepRows * D + 2 * row);
-        const float f = ml.x == kNegInf ? 0.0f : ex2(ml.x - mx);
-        ls += ml.y * f;
+    for (int i = 0; i < 4; ++i)
+      if (k0 + i * W * 32 < n_split * kStepRows) s_ml[k0 + i * W * 32] = y[i];
+  }
+  __syncthreads();
+  if (W == 4 || tid < 128u) {
+    const uint32_t row = tid >> 3, part = tid & 7u;
+    float mx = kNegInf, ls = 0.0f;
+    for (uint32_t k = part; k < n_split; k += 8) mx = fmaxf(mx, s_ml[k * kStepRows + row].x);
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          const float4 y = ld_join4(part_k + row * D + c * 32 + part * 4);
-          acc[4 * c] += y.x * f;
-          acc[4 * c + 1] += y.y * f;
-          acc[4 * c + 2] += y.z * f;
-          acc[4 * c + 3] += y.w * f;
+    for (int d = 1; d < 8; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    for (uint32_t k = part; k < n_split; k += 8) {
+      const float2 ml = s_ml[k * kStepRows + row];
+      const float f = ml.x == kNegInf ? 0.0f : ex2(ml.x - mx);
+      ls += ml.y * f;
+      s_ml[k * kStepRows + row].x = f;
+    }
+#pragma unroll
+    for (int d = 1; d < 8; d *= 2) ls += __shfl_xor_sync(0xffffffffu, ls, d);
+    if (part == 0) finish_row(row, mx, ls);
+  }
+  __syncthreads();
+  // four dims a thread, all ranges in order, 16 loads in flight
+  for (uint32_t c4 = tid; c4 < n_rows * (D / 4); c4 += W * 32) {
+    const uint32_t r = c4 / (D / 4), d4 = c4 % (D / 4);
+    const float* src = base + r * D + d4 * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (uint32_t k0 = 0; k0 < n_split; k0 += 16) {
+      float4 y[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        if (k0 + k < n_split) y[k] = ld_join4(src + (uint64_t)(k0 + k) * (kStepRows * (D + 2)));
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        if (k0 + k < n_split) {
+          const float f = s_ml[(k0 + k) * kStepRows + r].x;
+          x.x += y[k].x * f;
+          x.y += y[k].y * f;
+          x.z += y[k].z * f;
+          x.w += y[k].w * f;
         }
-      }
+    }
+    finish_out(r, d4, x);
   }
-  if (row >= n_rows) return;
-  const uint32_t rr = r0 + row, tok = rr / p.G, hd = head * p.G + rr - tok * p.G;
-  const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
-  uint16_t* out = p.b + ((int64_t)q.row + tok) * p.b_row + (int64_t)hd * p.b_head;
-#pragma unroll
-  for (int c = 0; c < D / 32; ++c)
-    st8(out + c * 32 + part * 4,
-        ls == 0.0f ? make_uint2(0, 0)
-                   : make_uint2(pack2<DT>(acc[4 * c] * inv, acc[4 * c + 1] * inv),
-                                pack2<DT>(acc[4 * c + 2] * inv, acc[4 * c + 3] * inv)));
-  if (p.lse && part == 0)
-    st4(p.lse + ((int64_t)q.row + tok) * p.HQ + hd,
-        __float_as_uint(ls == 0.0f ? kNegInf : (mx + log2f(ls)) * 0.693147180559945309f));
 }
 
-template <int DT, int D, bool PAGED16>
+template <int DT, int D, bool PAGED16, int W>
 int step_launch(const C8Params& p, void* stream) {
-  constexpr int bytes = StepSmem<D, PAGED16>::kBytes;
-  const auto kernel = c8_step_kernel<DT, D, PAGED16>;
+  constexpr int bytes = step_smem<D, W>();
+  const auto kernel = c8_step_kernel<DT, D, PAGED16, W>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return KV_ERR_CUDA;
   const uint64_t gx = (uint64_t)p.n_units * p.splits;
@@ -663,7 +701,7 @@ int step_launch(const C8Params& p, void* stream) {
   return dbg_launch(
       stream,
       [&] {
-        kernel<<<dim3((unsigned)gx, p.H), kStepWarps * 32, bytes, (cudaStream_t)stream>>>(p);
+        kernel<<<dim3((unsigned)gx, p.H), W * 32, bytes, (cudaStream_t)stream>>>(p);
         return cudaGetLastError();
       },
       p);
@@ -671,7 +709,10 @@ int step_launch(const C8Params& p, void* stream) {
 
 template <int DT, int D>
 int step_d(const C8Params& p, void* stream) {
-  return p.T % 16 == 0 ? step_launch<DT, D, true>(p, stream) : step_launch<DT, D, false>(p, stream);
+  constexpr int BIG = D == 256 ? 8 : 12;
+  if (p.step_warps > 4)
+    return p.T % 16 == 0 ? step_launch<DT, D, true, BIG>(p, stream) : step_launch<DT, D, false, BIG>(p, stream);
+  return p.T % 16 == 0 ? step_launch<DT, D, true, 4>(p, stream) : step_launch<DT, D, false, 4>(p, stream);
 }
 
 }  // namespace
