@@ -109,10 +109,8 @@ struct Split {
   uint64_t ticket_bytes, bytes;
 };
 
-// Row tiles of the step kernel and the ranges their keys are split into.  A
-// range is chosen such that the tiles' ranges fill the GPU: one wave where all
-// lengths are the bound (a single sequence), several where they may differ, and
-// at least 128 keys (two rounds of a CTA's four warps).
+// Row tiles of the step kernel and the ranges their keys are split into, from the
+// batch's host fields alone.
 Split step_split(const C8Params& p, const kv_cache8_batch* b, uint32_t window) {
   Split s;
   const uint32_t tiles1 = (p.G + kvc::kStepRows - 1) / kvc::kStepRows;
@@ -130,8 +128,14 @@ Split step_split(const C8Params& p, const kv_cache8_batch* b, uint32_t window) {
     s.warps = big;
     chunk = std::max<uint64_t>((keys * jobs + kvc::kC8Sms - 1) / kvc::kC8Sms, 32u * big);
   } else {
+    // Smaller CTAs, whose starts and ends hide behind each other.  A range costs its CTA some 4 us besides
+    // its keys, so it has 384 keys at least; and the lengths may be far below the bound, so the more jobs there
+    // are the more ranges each resident CTA gets on average (64 sequences of 100 to 8192 tokens, 8 heads, D = 128:
+    // ranges of 1200 keys 72 us, 2300 75, 4096 84, 512 84).  Where there are jobs enough to fill the GPU twice
+    // these are balance enough (256 sequences of 1000 to 2000 tokens: whole 150 us, ranges of 1024 169).
     s.warps = 4;
-    chunk = std::max<uint64_t>((keys * jobs + 24u * kvc::kC8Sms - 1) / (24u * kvc::kC8Sms), 128u);
+    const uint64_t slots = (uint64_t)kvc::kC8Sms * (p.D == 256 ? 2 : 3);
+    chunk = jobs >= 2 * slots ? keys : std::max<uint64_t>(keys * jobs / (2 * slots + 5 * jobs), 384u);
   }
   chunk = (chunk + 31u) & ~31ull;
   s.splits = (uint32_t)std::min<uint64_t>((keys + chunk - 1) / chunk, kvc::kMaxSplits);
@@ -195,6 +199,8 @@ int kv_cache8_create(const kv_cache8_geometry* g, kv_cache8_t* out) {
   p.sb = g->stride_block;
   p.st = g->stride_token;
   p.sh = g->stride_head;
+  p.st2 = 2 * p.st;
+  p.stv = (int64_t)(512 / D) * p.st;
   // n / T for n < 2^31 by the round-up method (Granlund and Montgomery, PLDI 1994)
   while ((1u << p.t_shift) < p.T) ++p.t_shift;
   p.t_magic = (uint32_t)((((uint64_t(1) << p.t_shift) - p.T) << 32) / p.T + 1);

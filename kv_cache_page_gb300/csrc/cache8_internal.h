@@ -21,6 +21,7 @@ struct C8Params {
   uint32_t t_magic, t_shift;    // n / T = (umulhi(t_magic, n) + n) >> t_shift, n < 2^31
   uint32_t num_blocks;
   int64_t sb, st, sh;           // code strides, bytes
+  int64_t st2, stv;             // 2 tokens; the token rows that a warp's 16-byte copies cover (512 / D)
   // ---- layer ----
   uint8_t* k;
   uint8_t* v;

@@ -35,6 +35,11 @@ constexpr float kNegInf = -INFINITY;
 // 2^(11 + kLag) = 2^15 < 65504.
 constexpr float kLift = 2048.0f, kLag = 4.0f;
 
+// A barrier of the CTA that counts threads, whether or not their warp is
+// converged (__syncthreads() asks for converged warps, and the branches here on
+// one thread's bookkeeping and on loaded values do not promise that).
+__device__ __forceinline__ void cta_sync() { asm volatile("barrier.sync 0;" ::: "memory"); }
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -50,7 +55,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Copy N bytes to a shared slot, zeros when !ok.
+// Copy N bytes to a shared slot; zeros when !ok.
 template <int N>
 __device__ __forceinline__ void cp_async(uint32_t smem, const void* src, bool ok) {
 #ifdef KVC_BOUNDS_CHECK
@@ -61,6 +66,14 @@ __device__ __forceinline__ void cp_async(uint32_t smem, const void* src, bool ok
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(src), "r"(n) : "memory");
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem), "l"(src), "n"(N), "r"(n) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async(uint32_t smem, const void* src) {
+  KVC_GUARD(src, N, return);
+  if (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem), "l"(src), "n"(N) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -83,11 +96,12 @@ struct StepShape {
   static constexpr int HT = TS / 16;                   // 16-token tiles of a step
   static constexpr int CH = D >= 64 ? 16 : 8;          // bytes of a K copy
   static constexpr int KC = D / 4 / CH;                // K copies of a lane and token
-  static constexpr int KS = D / 16;                    // k-steps of the score product
   static constexpr int NT = D / 8;                     // 8-wide column tiles of the output
   static constexpr int VR = 512 / D;                   // token rows that a warp's 16-byte V copies cover
   static constexpr int kK = TS * D;                    // bytes of a stage's K and of its V
-  static constexpr int kStage = 2 * kK + 8 * TS;       // and FP32 scales of K and V per token
+  // and FP32 scales of K and V per token; V tiles start at multiples of a row (addressed by xor)
+  static constexpr int kStage = 2 * kK + (TS == 16 ? 256 : 8 * TS);
+  static_assert(kStage % 256 == 0, "");
   static constexpr int kStages = D == 256 ? 3 : D == 128 ? 2 : D == 64 ? 3 : 4;
   static constexpr int kQ = 16 * D * 2;
   static constexpr int kSmall = 2048;                  // rows' factors, maxima, sums
@@ -137,11 +151,12 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
     c8_step_kernel(const __grid_constant__ C8Params p) {
   using S = StepShape<D>;
   constexpr int NS = S::kStages, TS = S::TS, HT = S::HT;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
   const uint32_t g = lane >> 2, qd = lane & 3u;
-  const uint32_t head = blockIdx.y;
-  const uint32_t u = blockIdx.x / p.splits, split = blockIdx.x - u * p.splits;
+  // heads next to each other: their rows of a page lie side by side, and are read at about the same time
+  const uint32_t us = blockIdx.x / p.H, head = blockIdx.x - us * p.H;
+  const uint32_t u = us / p.splits, split = us - u * p.splits;
 
   const uint32_t tiles1 = (p.G + kStepRows - 1) / kStepRows;
   const C8Seq q = c8_find(p, u, p.G, kStepRows, 1u, tiles1);
@@ -167,68 +182,74 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
   uint8_t* my_slots = smem + S::kQ + S::kSmall + warp * (NS * S::kStage);
   const uint32_t slots = (uint32_t)__cvta_generic_to_shared(my_slots);
   bool bad = false;
-  uint32_t holes = 0;  // bit s: a token of stage s has no page
 
-  // this lane's copies: K tokens (h, t) at dims of its quad; V rows lane / (D / 16) + VR i
-  const uint8_t* k_src = p.k + (int64_t)head * p.sh + qd * S::CH;
-  const uint8_t* v_src = p.v + (int64_t)head * p.sh + (lane % (D / 16)) * 16;
-  const uint32_t v_row = lane / (D / 16);
+  // this lane's copies: K tokens tok_of(g, h) at dims of its quad; V chunk lane % (D / 16) of rows
+  // v_row + VR i, whose place in the V tile repeats every NV rows but for i VR D bytes.
+  const uint32_t v_row = lane / (D / 16), v_chunk = lane % (D / 16);
+  const uint8_t* k_src = p.k + (int64_t)head * p.sh + qd * S::CH + (PAGED16 ? (int64_t)tok_of(g, 0) * p.st : 0);
+  const uint8_t* v_src = p.v + (int64_t)head * p.sh + v_chunk * 16 + (PAGED16 ? (int64_t)v_row * p.st : 0);
+  const uint32_t k_dst = lane * S::CH;
+  constexpr int NV = D == 256 ? 4 : 2;
+  uint32_t v_dst[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) v_dst[i] = S::kK + v_at<D>(v_row + S::VR * i, v_chunk) - S::VR * D * i;
+  const int32_t* table = p.tables + (int64_t)q.s * p.table_stride;
 
   // raw table entry of this lane's token of step t, one step ahead of its use
   auto entry_of = [&](int32_t t) -> int32_t {
     const int32_t tok = c_lo + TS * t + (int32_t)(lane % TS);
     if (tok >= c_hi) return -2;
     const uint32_t i = c8_div_t(p, (uint32_t)tok);
-    return i < p.table_width ? ldg_i32(p.tables + (int64_t)q.s * p.table_stride + i) : -1;
+    return i < p.table_width ? ldg_i32(table + i) : -1;
   };
+  // Start the copies of step t.  Tokens without a page, and those past the range
+  // (entry -2), are not copied: their slots hold what they held, their scales 0.
   auto issue = [&](int32_t t, int stage, int32_t entry) {
     const uint32_t at = slots + stage * S::kStage;
-    const int32_t tok0 = c_lo + TS * t, tok = tok0 + (int32_t)(lane % TS);
+    const int32_t tok = c_lo + TS * t + (int32_t)(lane % TS);
     const bool ok = (uint32_t)entry < p.num_blocks;
-    const uint32_t hole = __ballot_sync(0xffffffffu, !ok && entry != -2);
-    holes = (holes & ~(1u << stage)) | (hole ? 1u << stage : 0u);
-    bad |= hole != 0u;
+    bad |= !ok && entry != -2;
     const uint32_t in_page = (uint32_t)tok - c8_div_t(p, (uint32_t)tok) * p.T;
     const int64_t off = ok ? (int64_t)entry * p.sb + (int64_t)in_page * p.st : -1;
-    const int64_t si = ok ? (int64_t)entry * p.H + head : 0;
-    if (lane < TS) {
-      cp_async<4>(at + 2 * S::kK + lane * 4, p.k_scale + si, ok);
-      cp_async<4>(at + 2 * S::kK + 4 * TS + lane * 4, p.v_scale + si, ok);
-    }
+    const uint32_t si = ok ? (uint32_t)entry : 0u;
+    // (steps of 16 tokens: lanes 16 .. 31 copy the same words once more)
+    cp_async<4>(at + 2 * S::kK + (lane % TS) * 4, p.k_scale + head + (uint64_t)si * p.H, ok);
+    cp_async<4>(at + 2 * S::kK + 4 * TS + (lane % TS) * 4, p.v_scale + head + (uint64_t)si * p.H, ok);
 #pragma unroll
     for (int t16 = 0; t16 < HT; ++t16) {
       if (PAGED16) {
         // a tile's tokens all lie in its first token's page (those past the length hold anything)
         const int64_t base = __shfl_sync(0xffffffffu, off, 16 * t16);
-        const bool has = base >= 0;
-        const int64_t b = has ? base : 0;
-        const uint8_t* ks = k_src + b + (int64_t)tok_of(g, 0) * p.st;
+        if (base >= 0) {
+          const uint8_t* ks = k_src + base;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int c = 0; c < S::KC; ++c)
-            cp_async<S::CH>(at + (((t16 * 2 + h) * S::KC + c) * 32 + lane) * S::CH,
-                            (has ? ks + h * 2 * p.st : k_src) + c * 4 * S::CH, has);
-        const uint8_t* vs = v_src + b;
+            for (int c = 0; c < S::KC; ++c)
+              cp_async<S::CH>(at + k_dst + ((t16 * 2 + h) * S::KC + c) * 32 * S::CH, ks + c * 4 * S::CH);
+            ks += p.st2;
+          }
+          const uint8_t* vs = v_src + base;
 #pragma unroll
-        for (int i = 0; i < 16 / S::VR; ++i) {
-          const uint32_t r = v_row + i * S::VR;
-          cp_async<16>(at + S::kK + v_at<D>(16 * t16 + r, lane % (D / 16)), has ? vs + (int64_t)r * p.st : v_src, has);
+          for (int i = 0; i < 16 / S::VR; ++i) {
+            cp_async<16>(at + v_dst[i % NV] + (16 * t16 + i * S::VR) * D, vs);
+            vs += p.stv;
+          }
         }
       } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int64_t b = __shfl_sync(0xffffffffu, off, 16 * t16 + tok_of(g, h));
+          if (b >= 0) {
 #pragma unroll
-          for (int c = 0; c < S::KC; ++c)
-            cp_async<S::CH>(at + (((t16 * 2 + h) * S::KC + c) * 32 + lane) * S::CH, k_src + (b >= 0 ? b : 0) + c * 4 * S::CH,
-                            b >= 0);
+            for (int c = 0; c < S::KC; ++c)
+              cp_async<S::CH>(at + k_dst + ((t16 * 2 + h) * S::KC + c) * 32 * S::CH, k_src + b + c * 4 * S::CH);
+          }
         }
 #pragma unroll
         for (int i = 0; i < 16 / S::VR; ++i) {
-          const uint32_t r = v_row + i * S::VR;
-          const int64_t b = __shfl_sync(0xffffffffu, off, 16 * t16 + r);
-          cp_async<16>(at + S::kK + v_at<D>(16 * t16 + r, lane % (D / 16)), v_src + (b >= 0 ? b : 0), b >= 0);
+          const int64_t b = __shfl_sync(0xffffffffu, off, 16 * t16 + v_row + i * S::VR);
+          if (b >= 0) cp_async<16>(at + v_dst[i % NV] + (16 * t16 + i * S::VR) * D, v_src + b);
         }
       }
     }
@@ -309,20 +330,9 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
     }
     if (part == 0) s_row[r] = p.scale_log2 * __uint_as_float((uint32_t)(127 - ex) << 23);
   }
-  __syncthreads();
+  cta_sync();
 
-  // visible keys of this lane's rows g and g + 8
-  int32_t vis_hi[2], vis_lo[2];
-  float rf[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t r = g + 8 * h;
-    const int32_t pos = q.start + (int32_t)((r0 + r) / p.G);
-    vis_hi[h] = p.causal ? min(q.len, pos + 1) : q.len;
-    vis_lo[h] = p.window ? (int32_t)max((int64_t)0, (int64_t)pos - p.window + 1) : 0;
-    if (r >= n_rows || pos < 0) vis_hi[h] = 0;
-    rf[h] = s_row[r];
-  }
+  const float rf[2] = {s_row[g], s_row[g + 8]};
   // steps between these need no mask
   const int32_t full_hi = min(c_hi, first_pos < 0 ? 0 : p.causal ? min(q.len, first_pos + 1) : q.len);
   const int32_t full_lo = p.window ? (int32_t)max((int64_t)0, (int64_t)last_pos - p.window + 1) : 0;
@@ -349,8 +359,8 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
       __syncwarp();  // V and the scales were copied by other lanes
     }
     const uint8_t* sp = my_slots + stage * S::kStage;
-    const uint32_t sv = slots + stage * S::kStage + S::kK;
-    const bool hole = (holes >> stage) & 1u;
+    // V row lane & 15, chunk lane >> 4; chunk 2 c + (lane >> 4) of a row lies at this ^ (c << 5)
+    const uint32_t sv = slots + stage * S::kStage + S::kK + v_at<D>(lane & 15u, lane >> 4);
     stage = stage == NS - 1 ? 0 : stage + 1;
     const int32_t tok0 = c_lo + TS * t;
 
@@ -385,6 +395,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
     }
     // scales of tokens 16 t16 + 4 qd .. + 3; column (h, e) of a tile is token 2 h + e of these
     float vt = 0.0f;
+    bool hole = false;  // a token has the scale 0 of one that was not copied
     float4 vs[HT];
 #pragma unroll
     for (int t16 = 0; t16 < HT; ++t16) {
@@ -393,6 +404,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
       vs[t16] = *reinterpret_cast<const float4*>(sp + 2 * S::kK + 4 * TS + i * 4);
       if (PAGED16) {
         const float f0 = k4.x * rf[0], f1 = k4.x * rf[1];
+        hole |= k4.x == 0.0f;
 #pragma unroll
         for (int h = 2 * t16; h < 2 * t16 + 2; ++h) {
           s[h][0] *= f0; s[h][1] *= f0;
@@ -400,6 +412,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
         }
         vt = fmaxf(vt, vs[t16].x);
       } else {
+        hole |= k4.x == 0.0f || k4.y == 0.0f || k4.z == 0.0f || k4.w == 0.0f;
         s[2 * t16][0] *= k4.x * rf[0]; s[2 * t16][1] *= k4.y * rf[0];
         s[2 * t16][2] *= k4.x * rf[1]; s[2 * t16][3] *= k4.y * rf[1];
         s[2 * t16 + 1][0] *= k4.z * rf[0]; s[2 * t16 + 1][1] *= k4.w * rf[0];
@@ -407,8 +420,19 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
         vt = fmaxf(vt, fmaxf(fmaxf(vs[t16].x, vs[t16].y), fmaxf(vs[t16].z, vs[t16].w)));
       }
     }
+    if (!PAGED16) hole = __any_sync(0xffffffffu, hole);
     const bool masked = hole || tok0 + TS > full_hi || tok0 < full_lo;
     if (masked) {
+      // visible keys of this lane's rows g and g + 8
+      int32_t vis_hi[2], vis_lo[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t r = g + 8 * h;
+        const int32_t pos = q.start + (int32_t)((r0 + r) / p.G);
+        vis_hi[h] = p.causal ? min(c_hi, pos + 1) : c_hi;  // c_hi: at most the length
+        vis_lo[h] = p.window ? (int32_t)max((int64_t)0, (int64_t)pos - p.window + 1) : 0;
+        if (r >= n_rows || pos < 0) vis_hi[h] = 0;
+      }
 #pragma unroll
       for (int h = 0; h < 2 * HT; ++h)
 #pragma unroll
@@ -416,8 +440,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
           const uint32_t i = 16 * (h >> 1) + 4 * qd + 2 * (h & 1) + (e & 1);
           const int32_t tok = tok0 + (int32_t)i;
           const int r = e >> 1;
-          // a token without a page has the scale 0 of a skipped copy
-          if (tok >= min(vis_hi[r], c_hi) || tok < vis_lo[r] ||
+          if (tok >= vis_hi[r] || tok < vis_lo[r] ||
               (hole && *reinterpret_cast<const float*>(sp + 2 * S::kK + i * 4) == 0.0f))
             s[h][e] = kNegInf;
         }
@@ -486,7 +509,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t vw[4];
-        ldsm_t16x2(vw, sv + v_at<D>(16 * t16 + (lane & 15u), 2 * c + (lane >> 4)));
+        ldsm_t16x2(vw, (sv ^ (c << 5)) + 16 * t16 * D);
         if (masked) {
           // a NaN that some row does not see must not reach it through 0 * NaN:
           // NaN codes become 0 here and are put back below where they are seen
@@ -520,7 +543,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t vw[4];
-          ldsm_t16x2(vw, sv + v_at<D>(16 * t16 + (lane & 15u), 2 * c + (lane >> 4)));
+          ldsm_t16x2(vw, (sv ^ (c << 5)) + 16 * t16 * D);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const uint32_t nb = nan_bytes(vw[k]);  // 0x80 bytes -> 1.0 halves
@@ -537,7 +560,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
     }
   }
   cp_wait<0>();
-  if (bad && lane == 0u) c8_error(p, q.s, KV_CACHE8_BAD_PAGE);
+  if (bad) c8_error(p, q.s, KV_CACHE8_BAD_PAGE);
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
@@ -555,7 +578,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
     s_m[g * W + warp] = m[0];
     s_m[(g + 8) * W + warp] = m[1];
   }
-  __syncthreads();
+  cta_sync();
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     const uint32_t row = g + 8 * r;
@@ -571,7 +594,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
     for (int n = 0; n < S::NT; ++n)
       *reinterpret_cast<float2*>(dst + 8 * n) = make_float2(o[n][2 * r] * fo, o[n][2 * r + 1] * fo);
   }
-  __syncthreads();
+  cta_sync();
   const uint32_t job = u * p.H + head;
   float* base = p.partials + (uint64_t)job * p.splits * (kStepRows * (D + 2));
   float* mine = base + (uint64_t)split * (kStepRows * (D + 2));
@@ -601,7 +624,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
     if (n_split > 1u) st8(mine + kStepRows * D + 2 * tid, make_uint2(__float_as_uint(mx), __float_as_uint(ls)));
     else finish_row(tid, mx, ls);
   }
-  if (n_split == 1u) __syncthreads();
+  if (n_split == 1u) cta_sync();
   for (uint32_t c4 = tid; c4 < n_rows * (D / 4); c4 += W * 32) {
     const uint32_t r = c4 / (D / 4), d4 = c4 % (D / 4);
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -618,7 +641,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
   if (n_split == 1u) return;
 
   // ---- the last CTA of the row tile joins the ranges
-  __syncthreads();
+  cta_sync();
   uint32_t* s_last = reinterpret_cast<uint32_t*>(s_m);
   if (tid == 0) {
     uint32_t last = 0;
@@ -631,7 +654,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
     }
     *s_last = last;
   }
-  __syncthreads();
+  cta_sync();
   if (*s_last != 1u) return;
   // maxima and sums of all ranges at once, then a range's factor in place of its maximum
   float2* s_ml = reinterpret_cast<float2*>(smem + S::kQ + S::kSmall);  // [range][16 rows], over the slots
@@ -648,7 +671,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
     for (int i = 0; i < 4; ++i)
       if (k0 + i * W * 32 < n_split * kStepRows) s_ml[k0 + i * W * 32] = y[i];
   }
-  __syncthreads();
+  cta_sync();
   if (W == 4 || tid < 128u) {
     const uint32_t row = tid >> 3, part = tid & 7u;
     float mx = kNegInf, ls = 0.0f;
@@ -665,7 +688,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
     for (int d = 1; d < 8; d *= 2) ls += __shfl_xor_sync(0xffffffffu, ls, d);
     if (part == 0) finish_row(row, mx, ls);
   }
-  __syncthreads();
+  cta_sync();
   // four dims a thread, all ranges in order, 16 loads in flight
   for (uint32_t c4 = tid; c4 < n_rows * (D / 4); c4 += W * 32) {
     const uint32_t r = c4 / (D / 4), d4 = c4 % (D / 4);
@@ -696,12 +719,12 @@ int step_launch(const C8Params& p, void* stream) {
   const auto kernel = c8_step_kernel<DT, D, PAGED16, W>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return KV_ERR_CUDA;
-  const uint64_t gx = (uint64_t)p.n_units * p.splits;
+  const uint64_t gx = (uint64_t)p.n_units * p.splits * p.H;
   if (gx > 0x7fffffffull) return KV_ERR_INVALID_ARG;
   return dbg_launch(
       stream,
       [&] {
-        kernel<<<dim3((unsigned)gx, p.H), W * 32, bytes, (cudaStream_t)stream>>>(p);
+        kernel<<<(unsigned)gx, W * 32, bytes, (cudaStream_t)stream>>>(p);
         return cudaGetLastError();
       },
       p);
