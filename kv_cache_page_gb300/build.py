@@ -19,7 +19,7 @@ SRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkvcodec.so")
 DEBUG_LIB = os.path.join(PKG, "libkvcodec_debug.so")
-UNITS = ["fp8.cu", "uniform.cu", "turboquant.cu", "int8.cu", "crc.cu", "cache8_rw.cu", "cache8_step.cu",
+UNITS = ["fp8.cu", "uniform.cu", "turboquant.cu", "int8.cu", "crc.cu", "cache8_rw.cu", "cache8_step.cu", "cache8_prompt.cu",
          "kv_codec_host.cpp", "cache8_host.cpp"]
 HEADERS = ["kv_internal.h", "device_common.cuh", "crc_common.cuh", "cache8_internal.h", "cache8_common.cuh"]
 

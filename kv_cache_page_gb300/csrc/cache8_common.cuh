@@ -54,18 +54,17 @@ __device__ __forceinline__ int32_t ldg_i32(const int32_t* p) {
 }
 
 // The sequence of unit u: the last s with base(s) <= u, found by the whole warp
-// 32 probes at a time.  Without cu_new, `per` units belong to each sequence.
+// 32 probes at a time.  With per > 0, `per` units belong to each sequence.
 __device__ __forceinline__ C8Seq c8_find(const C8Params& p, uint32_t u, uint32_t w, uint32_t d, uint32_t x,
                                          uint32_t per) {
   C8Seq q;
-  if (p.cu == nullptr) {
-    q.s = u / per;
-    q.unit = u - q.s * per;
-    q.row = q.s;
-    q.n_new = 1;
+  uint32_t lo = 0;
+  if (per) {
+    lo = u / per;
+    q.unit = u - lo * per;
   } else {
     const uint32_t lane = threadIdx.x & 31u;
-    uint32_t lo = 0, n = p.n_seqs;  // the answer is in [lo, lo + n)
+    uint32_t n = p.n_seqs;  // the answer is in [lo, lo + n)
     while (n > 1u) {
       const uint32_t step = (n + 31u) / 32u;
       const uint32_t s = lo + lane * step;
@@ -75,16 +74,19 @@ __device__ __forceinline__ C8Seq c8_find(const C8Params& p, uint32_t u, uint32_t
       lo += k * step;
       n = min(step, n - k * step);
     }
+    q.unit = u - c8_base((uint32_t)ldg_i32(p.cu + lo), lo, w, d, x);
+  }
+  q.s = lo;
+  q.row = lo;
+  q.n_new = 1;
+  if (p.cu) {
     const int32_t c0 = ldg_i32(p.cu + lo), c1 = ldg_i32(p.cu + lo + 1u);
-    q.s = lo;
-    q.unit = u - c8_base((uint32_t)c0, lo, w, d, x);
     q.row = (uint32_t)c0;
     // rows past n_new are no memory of the caller's
-    q.n_new = (c0 < 0 || (uint32_t)c0 > p.n_new) ? 0 : min(c1 - c0, (int32_t)(p.n_new - (uint32_t)c0));
-    q.n_new = max(q.n_new, 0);
+    q.n_new = c0 < 0 || (uint32_t)c0 > p.n_new || c1 < c0 ? 0 : min(c1 - c0, (int32_t)(p.n_new - (uint32_t)c0));
   }
   if (q.unit > 0x3fffffffu) q.n_new = 0;  // cu_new not ascending
-  q.len = min(max(0, ldg_i32(p.lens + q.s)), 0x7fff0000);  // positions + a tile stay in 32 bits
+  q.len = min(max(0, ldg_i32(p.lens + lo)), 0x7fff0000);  // positions + a tile stay in 32 bits
   q.start = q.len - q.n_new;
   return q;
 }

@@ -105,21 +105,38 @@ uint32_t page_units(const C8Params& p) {
 }
 
 struct Split {
-  uint32_t units, splits, chunk, warps;
+  uint32_t units, per_seq, splits, chunk, warps;
   uint64_t ticket_bytes, bytes;
 };
+
+// Sequences of more than kStepMost rows (new tokens x query heads of a group) go to
+// the prompt kernel, the others to the step kernel.
+constexpr uint32_t kStepMost = 64;
+
+bool has_prompts(const C8Params& p, const kv_cache8_batch* b) {
+  if (!b->cu_new || p.D > 128) return false;
+  const uint64_t most = b->max_new ? std::min(b->max_new, b->n_new) : b->n_new;
+  return most * p.G > kStepMost;
+}
+// A single sequence's count is the total.
+bool has_steps(const C8Params& p, const kv_cache8_batch* b) {
+  return !has_prompts(p, b) || b->n_seqs > 1 || (uint64_t)b->n_new * p.G <= kStepMost;
+}
 
 // Row tiles of the step kernel and the ranges their keys are split into, from the
 // batch's host fields alone.
 Split step_split(const C8Params& p, const kv_cache8_batch* b, uint32_t window) {
   Split s;
   const uint32_t tiles1 = (p.G + kvc::kStepRows - 1) / kvc::kStepRows;
-  s.units = b->cu_new ? (uint32_t)((uint64_t)b->n_new * p.G / kvc::kStepRows) + b->n_seqs : b->n_seqs * tiles1;
+  s.per_seq = !b->cu_new ? tiles1 : has_prompts(p, b) ? kStepMost / kvc::kStepRows : 0u;
+  s.units = s.per_seq ? b->n_seqs * s.per_seq : (uint32_t)((uint64_t)b->n_new * p.G / kvc::kStepRows) + b->n_seqs;
   const uint64_t reach = std::min<uint64_t>((uint64_t)b->table_width * p.T, 0x7fff0000u);
   uint64_t keys = b->max_len ? std::min<uint64_t>(b->max_len, reach) : reach;
   if (window) keys = std::min<uint64_t>(keys, (uint64_t)window + kvc::kStepRows + 15u);
   keys = std::max<uint64_t>(keys, 16u);
-  const uint64_t jobs = std::max<uint64_t>((uint64_t)s.units * p.H, 1u);
+  // (next to prompts: single tokens, most likely)
+  const uint64_t jobs = std::max<uint64_t>((uint64_t)(has_prompts(p, b) ? b->n_seqs * tiles1 : s.units) * p.H, 1u);
+  const uint64_t all = std::max<uint64_t>((uint64_t)s.units * p.H, 1u);
   const uint32_t big = p.D == 256 ? 8u : 12u;
   uint64_t chunk;
   if (b->n_seqs == 1 || jobs * ((keys + 32 * big - 1) / (32 * big)) <= kvc::kC8Sms) {
@@ -139,9 +156,10 @@ Split step_split(const C8Params& p, const kv_cache8_batch* b, uint32_t window) {
   }
   chunk = (chunk + 31u) & ~31ull;
   s.splits = (uint32_t)std::min<uint64_t>((keys + chunk - 1) / chunk, kvc::kMaxSplits);
+  if (window) s.splits = std::min(s.splits, step_split(p, b, 0).splits);  // the workspace is sized without one
   s.chunk = (uint32_t)chunk;
-  s.ticket_bytes = s.splits > 1 ? (jobs * 4u + 255u) & ~255ull : 0u;
-  s.bytes = s.splits > 1 ? s.ticket_bytes + jobs * s.splits * (kvc::kStepRows * (p.D + 2ull) * 4u) : 0u;
+  s.ticket_bytes = s.splits > 1 ? (all * 4u + 255u) & ~255ull : 0u;
+  s.bytes = s.splits > 1 ? s.ticket_bytes + all * s.splits * (kvc::kStepRows * (p.D + 2ull) * 4u) : 0u;
   return s;
 }
 
@@ -249,7 +267,7 @@ int kv_cache8_attend_workspace(kv_cache8_t h, const kv_cache8_batch* batch, uint
   const int rc = check_batch_fields(h->p, batch);
   if (rc != KV_OK) return rc;
   if (batch->n_new == 0) return KV_OK;
-  *bytes = step_split(h->p, batch, 0).bytes;  // a window never needs more
+  if (has_steps(h->p, batch)) *bytes = step_split(h->p, batch, 0).bytes;  // a window never needs more
   return KV_OK;
 }
 
@@ -274,14 +292,23 @@ int kv_cache8_attend(kv_cache8_t h, const kv_cache8_layer* layer, const kv_cache
   if (!(p.scale_log2 > 0.0f) || !std::isfinite(p.scale_log2)) return KV_ERR_INVALID_ARG;
   p.window = window;
   p.causal = flags & KV_CACHE8_CAUSAL;
-  const Split sp = step_split(p, batch, window);
+  const bool prompts = has_prompts(p, batch), steps = has_steps(p, batch);
+  Split sp = {};
+  if (steps) sp = step_split(p, batch, window);
   if (sp.bytes && (!workspace || workspace_bytes < sp.bytes)) return KV_ERR_INVALID_ARG;
+  if (prompts) {
+    p.n_units = (uint32_t)((uint64_t)p.n_new * p.G / kvc::kPromptRows) + p.n_seqs;
+    p.min_rows = kStepMost + 1;
+    p.max_rows = 0xffffffffu;
+    if ((rc = kvc::launch_c8_prompt(p, stream)) != KV_OK || !steps) return rc;
+  }
   p.n_units = sp.units;
+  p.per_seq = sp.per_seq;
   p.splits = sp.splits;
   p.chunk = sp.chunk;
   p.step_warps = sp.warps;
   p.min_rows = 1;
-  p.max_rows = 0xffffffffu;
+  p.max_rows = prompts ? kStepMost : 0xffffffffu;
   p.tickets = static_cast<uint32_t*>(workspace);
   p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.ticket_bytes);
   return kvc::launch_c8_step(p, stream);

@@ -13,7 +13,7 @@ constexpr uint32_t kC8Sms = 152;  // SMs of a GB300: what the split rules count 
 // pairs r = i * G + g of one sequence and KV head.
 constexpr uint32_t kStepRows = 16;
 constexpr uint32_t kMaxSplits = 256;  // ranges of a row tile's keys (the joining CTA holds 8 bytes a range and row)
-constexpr uint32_t kPromptRows = 128;
+constexpr uint32_t kPromptRows = 256;
 
 struct C8Params {
   // ---- registered geometry ----
@@ -47,6 +47,7 @@ struct C8Params {
   uint32_t step_warps;          // warps of a step CTA: 4, or as many as an SM holds (12; 8 for D = 256)
   uint32_t chunk;               // keys of a range (more where splits ranges of it do not reach)
   uint32_t min_rows, max_rows;  // sequences this launch serves: G * new within [min_rows, max_rows]
+  uint32_t per_seq;             // step: units of a sequence, 0: by cu_new
   uint32_t n_units;             // row tiles (step, prompt) or page units (write, read), an upper bound
   uint32_t* tickets;            // [n_units][H]
   float* partials;              // [n_units][H][splits][kStepRows][D + 2]
@@ -55,5 +56,6 @@ struct C8Params {
 int launch_c8_write(const C8Params& p, void* stream);
 int launch_c8_read(const C8Params& p, void* stream);
 int launch_c8_step(const C8Params& p, void* stream);
+int launch_c8_prompt(const C8Params& p, void* stream);
 
 }  // namespace kvc

@@ -1,0 +1,637 @@
+// cache8_prompt.cu -- attention of many query rows over the 8-bit cache: whole
+// prompts and chunks of them.
+//
+//   S = Q K^T,  P = 2^(scale s_k S - m),  O = sum over key tiles of (s_v P) V
+//
+// Bound by the matrix products (4 D operations per query-key pair) and, next to
+// them, by the exponentials.  A CTA takes 256 rows (two tiles of 128: the G query
+// heads that share a KV head, times 256 / G new tokens) of one sequence and KV
+// head, and walks the keys 128 at a time:
+//   warps 8-11  read the codes, make FP16 of them (exactly) and lay them out for the
+//               tensor cores, K and V two tiles deep;
+//   warp 12     issues the products: scores of both row tiles into TMEM, weights
+//               (from TMEM) times V into accumulators in TMEM;
+//   warps 0-3, 4-7  the softmax of row tile 0 and 1, a thread to a row: scores from
+//               TMEM, weights back over them as FP16, the running maximum and sum.
+// While one row tile's softmax runs, the tensor cores work on the other's products.
+// The accumulators are rescaled only where a row's maximum grew by more than kLag.
+//
+// K and V share one layout, rows of 64 dims (128 bytes, 128-byte swizzle) per
+// token: as the score product's B operand dims are its inner index (K-major), as the
+// output product's B operand tokens are (MN-major), so V needs no transposition.
+//
+// Every wait has a limit; past it the CTA gives up, reports KV_CACHE8_STALLED and
+// releases what it holds.
+#include "cache8_common.cuh"
+
+namespace kvc {
+namespace {
+
+constexpr float kNegInf = -INFINITY;
+// Weights are held as 2^(z - m) * 2^11, m at most kLag below the true maximum (as
+// the step kernel holds them).
+constexpr float kLift = 2048.0f, kLag = 4.0f;
+constexpr int kKeys = 128;           // keys of a tile
+constexpr int kSoftWarps = 8, kLoadWarps = 4;
+constexpr int kPromptThreads = (kSoftWarps + kLoadWarps + 1) * 32;
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ---------------------------------------------------------------- mbarriers
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{ .reg .pred q; mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 q, [%1], %2; selp.u32 %0, 1, 0, q; }"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0u;
+}
+__device__ __forceinline__ uint64_t now_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+// Wait for the phase of this parity; false when two seconds have passed or another
+// thread gave up.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* stop) {
+  if (mbar_try(bar, parity)) return true;
+  const uint64_t end = now_ns() + kWaitNs;
+  for (;;) {
+#pragma unroll 1
+    for (int n = 0; n < 32; ++n)
+      if (mbar_try(bar, parity)) return true;
+    if (*stop) return false;
+    if (now_ns() > end) {
+      *stop = 1u;
+      return false;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- tensor cores
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// The barrier gets an arrival when this thread's products so far are done.
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// Shared memory operand: start, byte strides, 128-byte swizzle.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((addr >> 4) & 0x3fffu) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+// kind::f16, FP16 operands, FP32 accumulator, M = 128; bt: B is MN-major.
+__host__ __device__ constexpr uint32_t tc_idesc(uint32_t n, uint32_t bt) {
+  return (1u << 4) | (bt << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+}
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{ .reg .pred q; setp.ne.u32 q, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{ .reg .pred q; setp.ne.u32 q, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, q; }" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// 32 columns of the warp's 32 TMEM lanes: a thread gets its lane's.
+__device__ __forceinline__ void tm_ld32(uint32_t at, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+}
+__device__ __forceinline__ void tm_st16(uint32_t at, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tm_st32(uint32_t at, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+template <int D>
+struct PromptShape {
+  static constexpr int DG = D >= 64 ? D / 64 : 1;        // 64-dim groups (D = 32: half of one)
+  static constexpr uint32_t kQTile = DG * 128 * 128;     // bytes
+  static constexpr uint32_t kTile = DG * kKeys * 128;    // of K or V
+  static constexpr uint32_t kQ = 0, kK = 2 * kQTile, kV = kK + 2 * kTile;
+  static constexpr uint32_t kScale = kV + 2 * kTile;     // [stage][K, V][128] FP32
+  static constexpr uint32_t kNan = kScale + 2 * 2 * kKeys * 4;         // [stage][token][D / 32] bits of V's NaN codes
+  static constexpr uint32_t kRowNan = kNan + 2 * kKeys * (D / 32) * 4; // [row][D / 32]: dims whose output is NaN
+  static constexpr uint32_t kBar = kRowNan + 256 * (D / 32) * 4;
+  static constexpr uint32_t kBytes = kBar + 256;
+  static constexpr uint32_t kS = 0, kO = 256;            // TMEM columns: scores 2 x 128, then outputs 2 x D
+};
+
+template <int DT, int D, bool PAGED16>
+__global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __grid_constant__ C8Params p) {
+  using S = PromptShape<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = (uint32_t)__cvta_generic_to_shared(smem);
+  const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
+
+  // late row tiles first: under a causal mask they have the most keys
+  const uint32_t us = blockIdx.x / p.H, head = blockIdx.x - us * p.H;
+  const C8Seq q = c8_find(p, p.n_units - 1u - us, p.G, kPromptRows, 1u, 0u);
+  const uint32_t rows = (uint32_t)q.n_new * p.G, r0 = q.unit * kPromptRows;
+  if (q.unit > rows / kPromptRows || r0 >= rows || rows < p.min_rows || rows > p.max_rows) return;
+  const uint32_t n_rows = min(kPromptRows, rows - r0);
+  const uint32_t n_tiles = n_rows > 128u ? 2u : 1u;
+
+  // the keys that some row sees
+  const int32_t first_pos = q.start + (int32_t)(r0 / p.G), last_pos = q.start + (int32_t)((r0 + n_rows - 1u) / p.G);
+  const int32_t hi = max(p.causal ? min(q.len, last_pos + 1) : q.len, 0);
+  int32_t lo = p.window && first_pos >= 0 ? max(0, first_pos - (int32_t)min(p.window, 0x7fffffffu) + 1) : 0;
+  lo &= ~15;
+  const int32_t n_steps = hi > lo ? (hi - lo + kKeys - 1) / kKeys : 0;
+
+  // barriers
+  const uint32_t bar = sbase + S::kBar;
+  const uint32_t k_full = bar, k_empty = bar + 16, v_full = bar + 32, v_empty = bar + 48;  // [2]
+  const uint32_t s_full = bar + 64, p_full = bar + 80, pv_done = bar + 96;                  // [2]
+  volatile uint32_t* stop = reinterpret_cast<volatile uint32_t*>(smem + S::kBar + 112);
+  uint32_t* nan_seen = reinterpret_cast<uint32_t*>(smem + S::kBar + 116);   // [stage]: a byte a loading warp, V has NaN codes
+  uint32_t* any_row_nan = reinterpret_cast<uint32_t*>(smem + S::kBar + 124);
+  uint32_t* tm_at = reinterpret_cast<uint32_t*>(smem + S::kBar + 128);
+  if (tid == 0) {
+    for (uint32_t i = 0; i < 2; ++i) {
+      mbar_init(k_full + 8 * i, kLoadWarps * 32);
+      mbar_init(k_empty + 8 * i, 1);
+      mbar_init(v_full + 8 * i, kLoadWarps * 32);
+      mbar_init(v_empty + 8 * i, 1);
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(p_full + 8 * i, 128);
+      mbar_init(pv_done + 8 * i, 1);
+      nan_seen[i] = 0;
+    }
+    *stop = 0;
+    *any_row_nan = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kSoftWarps + kLoadWarps) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(tm_at))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+
+  // ---- Q to shared memory, a softmax thread to a row; bf16 rows are scaled by a
+  // power of two into FP16's range (exact but for values 2^-39 of the row's largest)
+  const uint32_t r = tid;  // row of the CTA, for threads of the softmax
+  const bool in = tid < 256u && r < n_rows;
+  const uint32_t rr = r0 + (in ? r : 0u), tok_r = rr / p.G, hd = head * p.G + rr - tok_r * p.G;
+  float rf = 0.0f;
+  if (tid < 256u) {
+    const uint16_t* src = p.a + ((int64_t)q.row + tok_r) * p.a_row + (int64_t)hd * p.a_head;
+    int ex = 0;
+    if (DT == 1) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 x = in ? ld_nc16(src + 8 * c) : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          m = max(m, (w[k] & 0x7fffu) < 0x7f80u ? (w[k] & 0x7fffu) : 0u);
+          m = max(m, ((w[k] >> 16) & 0x7fffu) < 0x7f80u ? ((w[k] >> 16) & 0x7fffu) : 0u);
+        }
+      }
+      ex = m ? min(max(14 - ((int)(m >> 7) - 127), -120), 120) : 0;
+    }
+    const float f = __uint_as_float((uint32_t)(127 + ex) << 23);
+    rf = p.scale_log2 * __uint_as_float((uint32_t)(127 - ex) << 23);
+    uint8_t* dst = smem + S::kQ + (r >> 7) * S::kQTile + (r & 127u) * 128;
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+      uint4 x = in ? ld_nc16(src + 8 * c) : make_uint4(0, 0, 0, 0);
+      if (DT == 1) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = pack2<0>(lo_f32<1>(w[k]) * f, hi_f32<1>(w[k]) * f);
+      }
+      *reinterpret_cast<uint4*>(dst + (c >> 3) * (128 * 128) + (((c & 7) ^ (r & 7u)) << 4)) = x;
+    }
+    uint32_t* rn = reinterpret_cast<uint32_t*>(smem + S::kRowNan) + r * (D / 32);
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) rn[k] = 0;
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = *tm_at;
+
+  if (warp < kSoftWarps) {
+    // ================================================================ softmax
+    const uint32_t t = warp >> 2;
+    float m = kNegInf, l = 0.0f, vref = 1.17549435e-38f, vinv = 0.0f;
+    bool fine = true;
+    if (t < n_tiles) {
+      const uint32_t tl = tm + ((warp & 3u) << 21);  // the warp's 32 lanes (lane << 16)
+      const uint32_t s_at = tl + S::kS + t * 128, o_at = tl + S::kO + t * D;
+      const int32_t pos = q.start + (int32_t)tok_r;
+      int32_t vis_hi = p.causal ? min(q.len, pos + 1) : q.len;
+      const int32_t vis_lo = p.window ? (int32_t)max((int64_t)0, (int64_t)pos - p.window + 1) : 0;
+      if (!in || pos < 0) vis_hi = 0;
+      // tiles of keys between these are seen whole by every row of the tile
+      const uint32_t ra = r0 + t * 128, rb = r0 + min(n_rows, t * 128 + 128u) - 1u;
+      const int32_t pos_a = q.start + (int32_t)(ra / p.G), pos_b = q.start + (int32_t)(rb / p.G);
+      const int32_t full_hi = min(hi, pos_a < 0 ? 0 : p.causal ? min(q.len, pos_a + 1) : q.len);
+      const int32_t full_lo = p.window ? (int32_t)max((int64_t)0, (int64_t)pos_b - p.window + 1) : 0;
+      for (int32_t j = 0; j < n_steps && fine; ++j) {
+        const int32_t tok0 = lo + j * kKeys;
+        const uint32_t st = j & 1;
+        const float* ks = reinterpret_cast<const float*>(smem + S::kScale) + st * 2 * kKeys;
+        const float* vs = ks + kKeys;
+        fine = mbar_wait(v_full + 8 * st, (j >> 1) & 1, stop) && mbar_wait(s_full + 8 * t, j & 1, stop);
+        fine = __all_sync(0xffffffffu, fine);
+        if (!fine) break;
+        __syncwarp();
+        tc_fence_after();
+        // holes of K: a token without a page has the scale 0
+        bool hole = false;
+        if (PAGED16) {
+#pragma unroll
+          for (int g = 0; g < kKeys / 16; ++g) hole |= ks[16 * g] == 0.0f;
+        } else {
+#pragma unroll
+          for (int i = 0; i < kKeys / 32; ++i) hole |= ks[32 * i + lane] == 0.0f;
+          hole = __any_sync(0xffffffffu, hole);
+        }
+        const bool masked = hole || tok0 + kKeys > full_hi || tok0 < full_lo;
+        // the largest V scale among what the row sees: another page's must not push its weights out of FP16's range
+        float vt = 0.0f;
+        if (PAGED16) {
+#pragma unroll
+          for (int g = 0; g < kKeys / 16; ++g)
+            if (!masked || (tok0 + 16 * g < vis_hi && tok0 + 16 * g + 16 > vis_lo)) vt = fmaxf(vt, vs[16 * g]);
+        } else if (!masked) {
+#pragma unroll
+          for (int i = 0; i < kKeys / 32; ++i) vt = fmaxf(vt, vs[32 * i + lane]);
+#pragma unroll
+          for (int d = 1; d < 32; d *= 2) vt = fmaxf(vt, __shfl_xor_sync(0xffffffffu, vt, d));
+        } else {
+          for (int32_t c = max(0, vis_lo - tok0); c < min(kKeys, vis_hi - tok0); ++c) vt = fmaxf(vt, vs[c]);
+          __syncwarp();
+        }
+        // 32 scores, scaled and masked
+        auto load = [&](int c, float (&z)[32]) {
+          uint32_t x[32];
+          tm_ld32(s_at + 32 * c, x);
+          tm_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int col = 32 * c + i;
+            z[i] = __uint_as_float(x[i]) * (ks[PAGED16 ? col & ~15 : col] * rf);
+            if (masked) {
+              const int32_t tok = tok0 + col;
+              if (tok >= vis_hi || tok < vis_lo || ks[PAGED16 ? col & ~15 : col] == 0.0f) z[i] = kNegInf;
+            }
+          }
+        };
+        float mt = kNegInf;
+#pragma unroll
+        for (int c = 0; c < kKeys / 32; ++c) {
+          float z[32];
+          load(c, z);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) mt = fmaxf(mt, z[i]);
+        }
+        const bool grow = mt > m + kLag;
+        if (__any_sync(0xffffffffu, grow || vt > vref)) {
+          const float vn = fmaxf(vt, vref);
+          const float mn = grow ? mt : m;
+          const float f = m == kNegInf ? 0.0f : ex2(m - mn);
+          l *= f;
+          m = mn;
+          if (j > 0) {  // the accumulator, once the products before are done
+            fine = __all_sync(0xffffffffu, mbar_wait(pv_done + 8 * t, (j - 1) & 1, stop));
+            if (!fine) break;
+            __syncwarp();
+            tc_fence_after();
+            const float fo = f * (vref / vn);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t x[32];
+              tm_ld32(o_at + 32 * c, x);
+              tm_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * fo);
+              tm_st32(o_at + 32 * c, x);
+            }
+          }
+          vref = vn;
+          vinv = kLift / vn;
+        }
+        const float base = m == kNegInf ? 0.0f : m;
+        if (masked && nan_seen[st]) {
+          // V has NaN codes (laid out as 0): the dims that a token seen by this row has them at
+          const uint32_t* bits = reinterpret_cast<const uint32_t*>(smem + S::kNan) + st * kKeys * (D / 32);
+          uint32_t* rn = reinterpret_cast<uint32_t*>(smem + S::kRowNan) + r * (D / 32);
+          uint32_t any = 0;
+          for (int32_t c = max(0, vis_lo - tok0); c < min(kKeys, vis_hi - tok0); ++c)
+            for (int k = 0; k < D / 32; ++k) {
+              const uint32_t b = bits[c * (D / 32) + k];
+              any |= b;
+              rn[k] |= b;
+            }
+          if (any) *any_row_nan = 1;
+        } else if (nan_seen[st]) {
+          const uint32_t* bits = reinterpret_cast<const uint32_t*>(smem + S::kNan) + st * kKeys * (D / 32);
+          uint32_t* rn = reinterpret_cast<uint32_t*>(smem + S::kRowNan) + r * (D / 32);
+          for (int32_t c = 0; c < kKeys; ++c)
+            for (int k = 0; k < D / 32; ++k) rn[k] |= bits[c * (D / 32) + k];
+          *any_row_nan = 1;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < kKeys / 32; ++c) {
+          float z[32];
+          load(c, z);
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float p0 = ex2(z[i] - base), p1 = ex2(z[i + 1] - base);
+            l += p0 + p1;
+            float w0 = p0 * (vs[PAGED16 ? (32 * c + i) & ~15 : 32 * c + i] * vinv);
+            float w1 = p1 * (vs[PAGED16 ? (32 * c + i) & ~15 : 32 * c + i + 1] * vinv);
+            if (masked) {  // 0 whatever the scale of the page that holds a token the row does not see
+              w0 = z[i] == kNegInf ? 0.0f : w0;
+              w1 = z[i + 1] == kNegInf ? 0.0f : w1;
+            }
+            w[i / 2] = pack2<0>(w0, w1);
+          }
+          tm_st16(s_at + 16 * c, w);
+        }
+        tm_wait_st();
+        tc_fence_before();
+        mbar_arrive(p_full + 8 * t);
+      }
+      // ---- outputs
+      if (n_steps > 0 && fine) {
+        fine = __all_sync(0xffffffffu, mbar_wait(pv_done + 8 * t, (n_steps - 1) & 1, stop));
+        tc_fence_after();
+      }
+      if (fine) {
+        const float inv = l == 0.0f ? 0.0f : vref / (l * kLift);
+        uint16_t* out = p.b + ((int64_t)q.row + tok_r) * p.b_row + (int64_t)hd * p.b_head;
+        const uint32_t* rn = reinterpret_cast<const uint32_t*>(smem + S::kRowNan) + r * (D / 32);
+        const bool fix = *any_row_nan != 0u;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t x[32];
+          __syncwarp();
+          if (n_steps > 0) {
+            tm_ld32(o_at + 32 * c, x);
+            tm_wait_ld();
+          }
+          if (in) {
+            if (fix && rn[c]) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if ((rn[c] >> i) & 1u) x[i] = 0x7fffffffu;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              float y[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) y[k] = inv == 0.0f ? 0.0f : __uint_as_float(x[i + k]) * inv;
+              st16(out + 32 * c + i, pack8<DT>(y));
+            }
+          }
+        }
+        if (p.lse && in)
+          st4(p.lse + ((int64_t)q.row + tok_r) * p.HQ + hd,
+              __float_as_uint(l == 0.0f ? kNegInf : (m + log2f(l)) * 0.693147180559945309f));
+      }
+    }
+  } else if (warp < kSoftWarps + kLoadWarps) {
+    // ================================================================ codes to FP16 tiles
+    // 16-byte chunks of codes: chunk c of token row i * RPI + row; a chunk makes two
+    // 16-byte chunks of FP16, written by lanes c, c + 4 in opposite order (8 lanes then
+    // hit 8 different bank groups)
+    constexpr int CPR = D / 16;                  // chunks of a token
+    constexpr int RPI = kLoadWarps * 32 / CPR;   // token rows at once
+    constexpr int N = kKeys / RPI;               // chunks of a thread and tile
+    const uint32_t lt = tid - kSoftWarps * 32u;
+    const uint32_t row = lt / CPR, c = lt % CPR;
+    const uint8_t* kb = p.k + (int64_t)head * p.sh + c * 16;
+    const uint8_t* vb = p.v + (int64_t)head * p.sh + c * 16;
+    const uint32_t dst = (c >> 2) * (kKeys * 128);
+    const uint32_t flip = (c >> 2) & 1u;
+    bool bad = false;
+    // byte offset of the token's row in the cache, -1: no such token or page
+    auto place = [&](int32_t tok, int32_t& id) -> int64_t {
+      id = -1;
+      if (tok >= hi) return -1;
+      const uint32_t i = c8_div_t(p, (uint32_t)tok);
+      id = c8_page(p, q.s, i);
+      if (id < 0) {
+        bad = true;
+        return -1;
+      }
+      return (int64_t)id * p.sb + (int64_t)((uint32_t)tok - i * p.T) * p.st;
+    };
+    uint4 kc[N], vc[N];
+    float ksc = 0.0f, vsc = 0.0f;
+    auto fetch = [&](int32_t j) {
+      const int32_t tok0 = lo + j * kKeys;
+      int32_t id;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int64_t off = place(tok0 + (int32_t)(i * RPI + row), id);
+        kc[i] = off >= 0 ? ld_nc16(kb + off) : make_uint4(0, 0, 0, 0);
+        vc[i] = off >= 0 ? ld_nc16(vb + off) : make_uint4(0, 0, 0, 0);
+      }
+      ksc = vsc = 0.0f;
+      if (place(tok0 + (int32_t)lt, id) >= 0) {
+        ksc = ldg_f32(p.k_scale + (int64_t)id * p.H + head);
+        vsc = ldg_f32(p.v_scale + (int64_t)id * p.H + head);
+      }
+    };
+    auto put = [&](uint8_t* tile, int i, uint4 x) {
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      uint4 h[2];
+      c8_dec4(w[0], h[0].x, h[0].y);
+      c8_dec4(w[1], h[0].z, h[0].w);
+      c8_dec4(w[2], h[1].x, h[1].y);
+      c8_dec4(w[3], h[1].z, h[1].w);
+      const uint32_t tr = i * RPI + row;
+      uint8_t* at = tile + dst + tr * 128;
+#pragma unroll
+      for (uint32_t k = 0; k < 2; ++k) {
+        const uint32_t part = k ^ flip;
+        *reinterpret_cast<uint4*>(at + ((((c & 3u) * 2 + part) ^ (tr & 7u)) << 4)) = part ? h[1] : h[0];
+      }
+    };
+    if (n_steps > 0) fetch(0);
+    bool fine = true;
+    for (int32_t j = 0; j < n_steps && fine; ++j) {
+      const uint32_t st = j & 1, ph = (j >> 1) & 1;
+      fine = mbar_wait(k_empty + 8 * st, ph ^ 1u, stop);
+      if (!fine) break;
+      uint8_t* kt = smem + S::kK + st * S::kTile;
+#pragma unroll
+      for (int i = 0; i < N; ++i) put(kt, i, kc[i]);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(k_full + 8 * st);
+      fine = mbar_wait(v_empty + 8 * st, ph ^ 1u, stop);
+      if (!fine) break;
+      uint8_t* vt = smem + S::kV + st * S::kTile;
+      uint32_t any = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(&vc[i]);
+        uint32_t bits = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t nb = ((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+          w[k] &= ~((nb >> 7) * 0xffu);
+          bits |= (((nb >> 7) * 0x01020408u) >> 24) << (4 * k);  // one bit per byte, in order
+        }
+        any |= bits;
+        // 16 bits of the token's D, kept for the rows that see it
+        reinterpret_cast<uint16_t*>(smem + S::kNan)[(st * kKeys + i * RPI + row) * (D / 16) + c] = (uint16_t)bits;
+        put(vt, i, vc[i]);
+      }
+      any = __any_sync(0xffffffffu, any != 0u) ? 1u : 0u;
+      if (lane == 0) reinterpret_cast<uint8_t*>(nan_seen)[4 * st + warp - kSoftWarps] = (uint8_t)any;
+      float* sc = reinterpret_cast<float*>(smem + S::kScale) + st * 2 * kKeys;
+      sc[lt] = ksc;
+      sc[kKeys + lt] = vsc;
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      mbar_arrive(v_full + 8 * st);
+      if (j + 1 < n_steps) fetch(j + 1);
+    }
+    if (bad) c8_error(p, q.s, KV_CACHE8_BAD_PAGE);
+  } else if (lane == 0 && n_steps > 0) {
+    // ================================================================ products
+    bool fine = true;
+    auto scores = [&](uint32_t t, int32_t j) {
+      const uint32_t a = sbase + S::kQ + t * S::kQTile, b = sbase + S::kK + (j & 1) * S::kTile;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        tc_mma_ss(tm + S::kS + t * 128, tc_desc(a + (k >> 2) * (128 * 128) + (k & 3) * 32, 16, 1024),
+                  tc_desc(b + (k >> 2) * (kKeys * 128) + (k & 3) * 32, 16, 1024), tc_idesc(kKeys, 0), k > 0);
+      tc_commit(s_full + 8 * t);
+    };
+    fine = mbar_wait(k_full, 0, stop);
+    if (fine) {
+      tc_fence_after();
+      for (uint32_t t = 0; t < n_tiles; ++t) scores(t, 0);
+      tc_commit(k_empty);
+    }
+    for (int32_t j = 0; j < n_steps && fine; ++j) {
+      const uint32_t st = j & 1;
+      fine = mbar_wait(v_full + 8 * st, (j >> 1) & 1, stop);
+      if (!fine) break;
+      for (uint32_t t = 0; t < n_tiles; ++t) {
+        fine = mbar_wait(p_full + 8 * t, j & 1, stop);
+        if (!fine) break;
+        tc_fence_after();
+        const uint32_t b = sbase + S::kV + st * S::kTile;
+#pragma unroll
+        for (int k = 0; k < kKeys / 16; ++k)
+          tc_mma_ts(tm + S::kO + t * D, tm + S::kS + t * 128 + 8 * k, tc_desc(b + k * 2048, kKeys * 128, 1024),
+                    tc_idesc(D, 1), j > 0 || k > 0);
+        tc_commit(pv_done + 8 * t);
+        if (t + 1 == n_tiles) tc_commit(v_empty + 8 * st);
+        if (j + 1 < n_steps) {
+          if (t == 0) {
+            fine = mbar_wait(k_full + 8 * ((j + 1) & 1), ((j + 1) >> 1) & 1, stop);
+            if (!fine) break;
+            tc_fence_after();
+          }
+          scores(t, j + 1);
+          if (t + 1 == n_tiles) tc_commit(k_empty + 8 * ((j + 1) & 1));
+        }
+      }
+    }
+    if (!fine) {
+      // products still in flight end before their memory goes
+      uint32_t* spare = reinterpret_cast<uint32_t*>(smem + S::kBar + 136);
+      const uint32_t sb = (uint32_t)__cvta_generic_to_shared(spare);
+      mbar_init(sb, 1);
+      tc_commit(sb);
+      *stop = 0u;  // the others have given up or will at their own limit
+      mbar_wait(sb, 0, stop);
+      *stop = 1u;
+      if (p.errors) atomicOr(p.errors + q.s, KV_CACHE8_STALLED);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  // (counts threads: the roles' loops may leave a warp diverged)
+  asm volatile("barrier.sync 0;" ::: "memory");
+  if (warp == kSoftWarps + kLoadWarps) {
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
+  }
+}
+
+template <int DT, int D, bool PAGED16>
+int prompt_launch(const C8Params& p, void* stream) {
+  constexpr int bytes = PromptShape<D>::kBytes;
+  const auto kernel = c8_prompt_kernel<DT, D, PAGED16>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return KV_ERR_CUDA;
+  const uint64_t gx = (uint64_t)p.n_units * p.H;
+  if (gx > 0x7fffffffull) return KV_ERR_INVALID_ARG;
+  return dbg_launch(
+      stream,
+      [&] {
+        kernel<<<(unsigned)gx, kPromptThreads, bytes, (cudaStream_t)stream>>>(p);
+        return cudaGetLastError();
+      },
+      p);
+}
+
+template <int DT, int D>
+int prompt_d(const C8Params& p, void* stream) {
+  return p.T % 16 == 0 ? prompt_launch<DT, D, true>(p, stream) : prompt_launch<DT, D, false>(p, stream);
+}
+
+}  // namespace
+
+int launch_c8_prompt(const C8Params& p, void* stream) {
+  switch (p.D) {
+    case 32: return p.dtype == KV_DT_FP16 ? prompt_d<0, 32>(p, stream) : prompt_d<1, 32>(p, stream);
+    case 64: return p.dtype == KV_DT_FP16 ? prompt_d<0, 64>(p, stream) : prompt_d<1, 64>(p, stream);
+    case 128: return p.dtype == KV_DT_FP16 ? prompt_d<0, 128>(p, stream) : prompt_d<1, 128>(p, stream);
+  }
+  return KV_ERR_UNSUPPORTED_HEAD_DIM;
+}
+
+}  // namespace kvc

@@ -41,7 +41,7 @@ __device__ __forceinline__ bool page_job(const C8Params& p, uint32_t warp, PageJ
   if (u >= p.n_units) return false;
   j.role = r >= p.H ? 1u : 0u;
   j.head = r - j.role * p.H;
-  j.q = c8_find(p, u, 1u, p.T, 2u, 1u);
+  j.q = c8_find(p, u, 1u, p.T, 2u, p.cu ? 0u : 1u);
   const int32_t T = (int32_t)p.T;
   j.page = (int32_t)(c8_div_t(p, (uint32_t)max(j.q.start, 0)) + j.q.unit);
   const int64_t first = (int64_t)j.page * T;

@@ -158,8 +158,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
   const uint32_t us = blockIdx.x / p.H, head = blockIdx.x - us * p.H;
   const uint32_t u = us / p.splits, split = us - u * p.splits;
 
-  const uint32_t tiles1 = (p.G + kStepRows - 1) / kStepRows;
-  const C8Seq q = c8_find(p, u, p.G, kStepRows, 1u, tiles1);
+  const C8Seq q = c8_find(p, u, p.G, kStepRows, 1u, p.per_seq);
   const uint32_t rows = (uint32_t)q.n_new * p.G, r0 = q.unit * kStepRows;
   if (r0 >= rows || rows < p.min_rows || rows > p.max_rows) return;
   const uint32_t n_rows = min(kStepRows, rows - r0);
@@ -341,7 +340,8 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
 #pragma unroll
   for (int n = 0; n < S::NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
   float m[2] = {kNegInf, kNegInf}, l[2] = {0.0f, 0.0f};
-  float vref = 1.17549435e-38f, vinv = 0.0f;  // V scales are held relative to the largest so far
+  // V scales are held relative to the largest that the row has seen
+  float vref[2] = {1.17549435e-38f, 1.17549435e-38f}, vinv[2] = {0.0f, 0.0f};
 
   int stage = 0;
   for (int32_t t = (int32_t)warp; t < n_steps; t += W) {
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
       }
     }
     // scales of tokens 16 t16 + 4 qd .. + 3; column (h, e) of a tile is token 2 h + e of these
-    float vt = 0.0f;
+    float vt[2] = {0.0f, 0.0f};
     bool hole = false;  // a token has the scale 0 of one that was not copied
     float4 vs[HT];
 #pragma unroll
@@ -410,17 +410,18 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
           s[h][0] *= f0; s[h][1] *= f0;
           s[h][2] *= f1; s[h][3] *= f1;
         }
-        vt = fmaxf(vt, vs[t16].x);
+        vt[0] = fmaxf(vt[0], vs[t16].x);
       } else {
         hole |= k4.x == 0.0f || k4.y == 0.0f || k4.z == 0.0f || k4.w == 0.0f;
         s[2 * t16][0] *= k4.x * rf[0]; s[2 * t16][1] *= k4.y * rf[0];
         s[2 * t16][2] *= k4.x * rf[1]; s[2 * t16][3] *= k4.y * rf[1];
         s[2 * t16 + 1][0] *= k4.z * rf[0]; s[2 * t16 + 1][1] *= k4.w * rf[0];
         s[2 * t16 + 1][2] *= k4.z * rf[1]; s[2 * t16 + 1][3] *= k4.w * rf[1];
-        vt = fmaxf(vt, fmaxf(fmaxf(vs[t16].x, vs[t16].y), fmaxf(vs[t16].z, vs[t16].w)));
+        vt[0] = fmaxf(vt[0], fmaxf(fmaxf(vs[t16].x, vs[t16].y), fmaxf(vs[t16].z, vs[t16].w)));
       }
     }
     if (!PAGED16) hole = __any_sync(0xffffffffu, hole);
+    vt[1] = vt[0];
     const bool masked = hole || tok0 + TS > full_hi || tok0 < full_lo;
     if (masked) {
       // visible keys of this lane's rows g and g + 8
@@ -444,6 +445,20 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
               (hole && *reinterpret_cast<const float*>(sp + 2 * S::kK + i * 4) == 0.0f))
             s[h][e] = kNegInf;
         }
+      // the scale of a page that the row does not see must not push its weights out of FP16's range
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        vt[r] = 0.0f;
+#pragma unroll
+        for (int t16 = 0; t16 < HT; ++t16) {
+          const float v4[4] = {vs[t16].x, vs[t16].y, vs[t16].z, vs[t16].w};
+#pragma unroll
+          for (int i = 0; i < (PAGED16 ? 1 : 4); ++i) {
+            const int32_t a = tok0 + 16 * t16 + (PAGED16 ? 0 : (int32_t)(4 * qd) + i);
+            if (a < vis_hi[r] && a + (PAGED16 ? 16 : 1) > vis_lo[r]) vt[r] = fmaxf(vt[r], v4[i]);
+          }
+        }
+      }
     }
     // running maxima; the sums are rescaled only where a maximum grew by more than kLag
     bool grow = false;
@@ -459,21 +474,23 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
       grow |= x > m[r] + kLag;  // -inf + kLag = -inf: any finite score of a fresh row
     }
     if (!PAGED16) {
-      vt = fmaxf(vt, __shfl_xor_sync(0xffffffffu, vt, 1));
-      vt = fmaxf(vt, __shfl_xor_sync(0xffffffffu, vt, 2));
-    }
-    if (__any_sync(0xffffffffu, grow || vt > vref)) {
-      const float vn = fmaxf(vt, vref);
-      const float fv = vref / vn;
-      vref = vn;
-      vinv = kLift / vn;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
+        vt[r] = fmaxf(vt[r], __shfl_xor_sync(0xffffffffu, vt[r], 1));
+        vt[r] = fmaxf(vt[r], __shfl_xor_sync(0xffffffffu, vt[r], 2));
+      }
+    }
+    if (__any_sync(0xffffffffu, grow || vt[0] > vref[0] || vt[1] > vref[1])) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float vn = fmaxf(vt[r], vref[r]);
         const float mn = mt[r] > m[r] + kLag ? mt[r] : m[r];
         const float f = m[r] == kNegInf ? 0.0f : ex2(m[r] - mn);
+        const float fo = f * (vref[r] / vn);
         m[r] = mn;
         l[r] *= f;
-        const float fo = f * fv;
+        vref[r] = vn;
+        vinv[r] = kLift / vn;
 #pragma unroll
         for (int n = 0; n < S::NT; ++n) {
           o[n][2 * r] *= fo;
@@ -485,8 +502,8 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
     uint32_t pa[HT][4];
 #pragma unroll
     for (int t16 = 0; t16 < HT; ++t16) {
-      const float w4[4] = {vs[t16].x * vinv, (PAGED16 ? vs[t16].x : vs[t16].y) * vinv,
-                           (PAGED16 ? vs[t16].x : vs[t16].z) * vinv, (PAGED16 ? vs[t16].x : vs[t16].w) * vinv};
+      const float v4[4] = {vs[t16].x, PAGED16 ? vs[t16].x : vs[t16].y, PAGED16 ? vs[t16].x : vs[t16].z,
+                           PAGED16 ? vs[t16].x : vs[t16].w};
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -494,7 +511,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
           const float z0 = s[2 * t16 + h][2 * r], z1 = s[2 * t16 + h][2 * r + 1];
           const float p0 = ex2(z0 - (r ? b1 : b0)), p1 = ex2(z1 - (r ? b1 : b0));
           l[r] += p0 + p1;
-          float x0 = p0 * w4[2 * h], x1 = p1 * w4[2 * h + 1];
+          float x0 = p0 * (v4[2 * h] * vinv[r]), x1 = p1 * (v4[2 * h + 1] * vinv[r]);
           if (masked) {  // 0 whatever the scale of the page that holds a token the row does not see
             x0 = z0 == kNegInf ? 0.0f : x0;
             x1 = z1 == kNegInf ? 0.0f : x1;
@@ -586,7 +603,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
 #pragma unroll
     for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_m[row * W + w]);
     const float f = m[r] == kNegInf ? 0.0f : ex2(m[r] - mx);
-    const float fo = m[r] == kNegInf ? 0.0f : f * (vref * (1.0f / kLift));
+    const float fo = m[r] == kNegInf ? 0.0f : f * (vref[r] * (1.0f / kLift));
     if (qd == 0) s_l[row * W + warp] = l[r] * f;
     // column 2 qd + e of tile n is dim 8 n + 2 qd + e
     float* dst = s_o + (warp * 16 + row) * OS + 2 * qd;
