@@ -321,12 +321,33 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
           }
         };
         float mt = kNegInf;
+        // whole tiles of 16-token pages: a factor for 16 columns, maxima of the bare products
+        const bool whole = PAGED16 && !masked;
+        if (whole) {
+          uint32_t x[2][32];
+          tm_ld32(s_at, x[0]);
 #pragma unroll
-        for (int c = 0; c < kKeys / 32; ++c) {
-          float z[32];
-          load(c, z);
+          for (int c = 0; c < kKeys / 32; ++c) {
+            tm_wait_ld();
+            if (c + 1 < kKeys / 32) tm_ld32(s_at + 32 * (c + 1), x[(c + 1) & 1]);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) mt = fmaxf(mt, z[i]);
+            for (int g = 0; g < 2; ++g) {
+              float y[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                y[i] = fmaxf(fmaxf(__uint_as_float(x[c & 1][16 * g + i]), __uint_as_float(x[c & 1][16 * g + 4 + i])),
+                             fmaxf(__uint_as_float(x[c & 1][16 * g + 8 + i]), __uint_as_float(x[c & 1][16 * g + 12 + i])));
+              mt = fmaxf(mt, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) * (ks[32 * c + 16 * g] * rf));
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < kKeys / 32; ++c) {
+            float z[32];
+            load(c, z);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) mt = fmaxf(mt, z[i]);
+          }
         }
         const bool grow = mt > m + kLag;
         if (__any_sync(0xffffffffu, grow || vt > vref)) {
@@ -375,24 +396,50 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
           *any_row_nan = 1;
         }
         __syncwarp();
+        // 2^(s f - m) in one step, unless m is so large that its own rounding would show
+        if (whole && !__any_sync(0xffffffffu, fabsf(base) >= 1048576.0f)) {
+          float2 sum = make_float2(0.0f, 0.0f);
+          const float2 nb = make_float2(-base, -base);
+          uint32_t x[2][32];
+          tm_ld32(s_at, x[0]);
 #pragma unroll
-        for (int c = 0; c < kKeys / 32; ++c) {
-          float z[32];
-          load(c, z);
-          uint32_t w[16];
+          for (int c = 0; c < kKeys / 32; ++c) {
+            tm_wait_ld();
+            if (c + 1 < kKeys / 32) tm_ld32(s_at + 32 * (c + 1), x[(c + 1) & 1]);
+            uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float p0 = ex2(z[i] - base), p1 = ex2(z[i + 1] - base);
-            l += p0 + p1;
-            float w0 = p0 * (vs[PAGED16 ? (32 * c + i) & ~15 : 32 * c + i] * vinv);
-            float w1 = p1 * (vs[PAGED16 ? (32 * c + i) & ~15 : 32 * c + i + 1] * vinv);
-            if (masked) {  // 0 whatever the scale of the page that holds a token the row does not see
-              w0 = z[i] == kNegInf ? 0.0f : w0;
-              w1 = z[i + 1] == kNegInf ? 0.0f : w1;
+            for (int g = 0; g < 2; ++g) {
+              const float f = ks[32 * c + 16 * g] * rf, v = vs[32 * c + 16 * g] * vinv;
+              const float2 f2 = make_float2(f, f), v2 = make_float2(v, v);
+#pragma unroll
+              for (int i = 16 * g; i < 16 * g + 16; i += 2) {
+                const float2 z = fma2(make_float2(__uint_as_float(x[c & 1][i]), __uint_as_float(x[c & 1][i + 1])), f2, nb);
+                const float2 e = make_float2(ex2(z.x), ex2(z.y));
+                sum = add2(sum, e);
+                const float2 y = mul2(e, v2);
+                w[i / 2] = pack2<0>(y.x, y.y);
+              }
             }
-            w[i / 2] = pack2<0>(w0, w1);
+            tm_st16(s_at + 16 * c, w);
           }
-          tm_st16(s_at + 16 * c, w);
+          l += sum.x + sum.y;
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < kKeys / 32; ++c) {
+            float z[32];
+            load(c, z);
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float p0 = ex2(z[i] - base), p1 = ex2(z[i + 1] - base);
+              l += p0 + p1;
+              const float v0 = vs[PAGED16 ? (32 * c + i) & ~15 : 32 * c + i], v1 = vs[PAGED16 ? (32 * c + i) & ~15 : 32 * c + i + 1];
+              // 0 whatever the scale of the page that holds a token the row does not see
+              const float w0 = z[i] == kNegInf ? 0.0f : p0 * (v0 * vinv), w1 = z[i + 1] == kNegInf ? 0.0f : p1 * (v1 * vinv);
+              w[i / 2] = pack2<0>(w0, w1);
+            }
+            tm_st16(s_at + 16 * c, w);
+          }
         }
         tm_wait_st();
         tc_fence_before();
@@ -451,7 +498,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
     const uint32_t dst = (c >> 2) * (kKeys * 128);
     const uint32_t flip = (c >> 2) & 1u;
     bool bad = false;
-    // byte offset of the token's row in the cache, -1: no such token or page
+    // Byte offset in the cache of a token's row (PAGED16: of a run of 16 tokens), -1:
+    // none.  PAGED16: lane g & 7 holds the offset and page of run g of a tile, asked
+    // for a tile ahead; tokens past the last one in its run hold anything.
     auto place = [&](int32_t tok, int32_t& id) -> int64_t {
       id = -1;
       if (tok >= hi) return -1;
@@ -463,21 +512,43 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
       }
       return (int64_t)id * p.sb + (int64_t)((uint32_t)tok - i * p.T) * p.st;
     };
+    const int64_t row_off = (int64_t)(row & 15u) * p.st;
     uint4 kc[N], vc[N];
     float ksc = 0.0f, vsc = 0.0f;
-    auto fetch = [&](int32_t j) {
-      const int32_t tok0 = lo + j * kKeys;
-      int32_t id;
+    int32_t id = -1, id_next = -1;
+    int64_t run = -1, run_next = -1;
+    auto ask = [&](int32_t j) {  // runs of tile j
+      run_next = -1;
+      id_next = -1;
+      if (PAGED16 && j < n_steps) run_next = place(lo + j * kKeys + 16 * (int32_t)(lane & 7u), id_next);
+    };
+    auto off_of = [&](int32_t j, int i) -> int64_t {
+      if (PAGED16) {
+        const int64_t o = __shfl_sync(0xffffffffu, run, (i * RPI + row) >> 4);
+        return o >= 0 ? o + row_off : -1;
+      }
+      int32_t x;
+      return place(lo + j * kKeys + (int32_t)(i * RPI + row), x);
+    };
+    auto fetch_k = [&](int32_t j) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const int64_t off = place(tok0 + (int32_t)(i * RPI + row), id);
+        const int64_t off = off_of(j, i);
         kc[i] = off >= 0 ? ld_nc16(kb + off) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto fetch_v = [&](int32_t j) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int64_t off = off_of(j, i);
         vc[i] = off >= 0 ? ld_nc16(vb + off) : make_uint4(0, 0, 0, 0);
       }
       ksc = vsc = 0.0f;
-      if (place(tok0 + (int32_t)lt, id) >= 0) {
-        ksc = ldg_f32(p.k_scale + (int64_t)id * p.H + head);
-        vsc = ldg_f32(p.v_scale + (int64_t)id * p.H + head);
+      int32_t at = PAGED16 ? __shfl_sync(0xffffffffu, id, lt >> 4) : -1;
+      if (!PAGED16) place(lo + j * kKeys + (int32_t)lt, at);
+      if (at >= 0) {
+        ksc = ldg_f32(p.k_scale + (int64_t)at * p.H + head);
+        vsc = ldg_f32(p.v_scale + (int64_t)at * p.H + head);
       }
     };
     auto put = [&](uint8_t* tile, int i, uint4 x) {
@@ -495,18 +566,29 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
         *reinterpret_cast<uint4*>(at + ((((c & 3u) * 2 + part) ^ (tr & 7u)) << 4)) = part ? h[1] : h[0];
       }
     };
-    if (n_steps > 0) fetch(0);
+    ask(0);
+    run = run_next;
+    id = id_next;
+    if (n_steps > 0) {
+      fetch_k(0);
+      fetch_v(0);
+    }
+    ask(1);
     bool fine = true;
     for (int32_t j = 0; j < n_steps && fine; ++j) {
       const uint32_t st = j & 1, ph = (j >> 1) & 1;
-      fine = mbar_wait(k_empty + 8 * st, ph ^ 1u, stop);
+      fine = __all_sync(0xffffffffu, mbar_wait(k_empty + 8 * st, ph ^ 1u, stop));
       if (!fine) break;
       uint8_t* kt = smem + S::kK + st * S::kTile;
 #pragma unroll
       for (int i = 0; i < N; ++i) put(kt, i, kc[i]);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(k_full + 8 * st);
-      fine = mbar_wait(v_empty + 8 * st, ph ^ 1u, stop);
+      run = run_next;
+      id = id_next;
+      __syncwarp();
+      if (j + 1 < n_steps) fetch_k(j + 1);
+      fine = __all_sync(0xffffffffu, mbar_wait(v_empty + 8 * st, ph ^ 1u, stop));
       if (!fine) break;
       uint8_t* vt = smem + S::kV + st * S::kTile;
       uint32_t any = 0;
@@ -532,7 +614,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
       sc[kKeys + lt] = vsc;
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       mbar_arrive(v_full + 8 * st);
-      if (j + 1 < n_steps) fetch(j + 1);
+      __syncwarp();
+      if (j + 1 < n_steps) fetch_v(j + 1);
+      ask(j + 2);
     }
     if (bad) c8_error(p, q.s, KV_CACHE8_BAD_PAGE);
   } else if (lane == 0 && n_steps > 0) {
