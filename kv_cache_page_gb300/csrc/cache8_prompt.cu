@@ -30,15 +30,27 @@ namespace {
 constexpr float kNegInf = -INFINITY;
 // Weights are held as 2^(z - m) * 2^11, m at most kLag below the true maximum (as
 // the step kernel holds them).
-constexpr float kLift = 2048.0f, kLag = 4.0f;
+constexpr float kLift = 11.0f, kLag = 4.0f;  // kLift: the logarithm
 constexpr int kKeys = 128;           // keys of a tile
-constexpr int kSoftWarps = 8, kLoadWarps = 4;
-constexpr int kPromptThreads = (kSoftWarps + kLoadWarps + 1) * 32;
-constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kSoftWarps = 8, kKWarps = 4, kVWarps = 3, kMmaWarp = kSoftWarps + kKWarps + kVWarps;
+constexpr int kPromptThreads = (kMmaWarp + 1) * 32;
+constexpr long long kWaitClocks = 4000000000ll;
+constexpr uint32_t kWaitHint = 100000;  // ns that one try may sleep (polling would take issue slots from the softmax)
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
 
@@ -52,28 +64,23 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{ .reg .pred q; mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 q, [%1], %2; selp.u32 %0, 1, 0, q; }"
+      "{ .reg .pred q; mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 q, [%1], %2, %3; selp.u32 %0, 1, 0, q; }"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "r"(kWaitHint)
       : "memory");
   return ok != 0u;
 }
-__device__ __forceinline__ uint64_t now_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-  return t;
-}
-// Wait for the phase of this parity; false when two seconds have passed or another
-// thread gave up.
+// Wait for the phase of this parity; false when some two seconds have passed or
+// another thread gave up.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* stop) {
   if (mbar_try(bar, parity)) return true;
-  const uint64_t end = now_ns() + kWaitNs;
+  const long long begin = clock64();
   for (;;) {
 #pragma unroll 1
-    for (int n = 0; n < 32; ++n)
+    for (int n = 0; n < 8; ++n)
       if (mbar_try(bar, parity)) return true;
     if (*stop) return false;
-    if (now_ns() > end) {
+    if (clock64() - begin > kWaitClocks) {
       *stop = 1u;
       return false;
     }
@@ -88,9 +95,15 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 // Shared memory operand: start, byte strides, 128-byte swizzle.
-__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+__host__ __device__ constexpr uint64_t tc_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
   return (uint64_t)((addr >> 4) & 0x3fffu) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) |
          (1ull << 46) | (2ull << 61);
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{ .reg .pred q; elect.sync _|q, 0xffffffff; selp.u32 %0, 1, 0, q; }" : "=r"(ok));
+  return ok != 0u;
 }
 // kind::f16, FP16 operands, FP32 accumulator, M = 128; bt: B is MN-major.
 __host__ __device__ constexpr uint32_t tc_idesc(uint32_t n, uint32_t bt) {
@@ -146,13 +159,261 @@ struct PromptShape {
   static constexpr uint32_t kQTile = DG * 128 * 128;     // bytes
   static constexpr uint32_t kTile = DG * kKeys * 128;    // of K or V
   static constexpr uint32_t kQ = 0, kK = 2 * kQTile, kV = kK + 2 * kTile;
-  static constexpr uint32_t kScale = kV + 2 * kTile;     // [stage][K, V][128] FP32
-  static constexpr uint32_t kNan = kScale + 2 * 2 * kKeys * 4;         // [stage][token][D / 32] bits of V's NaN codes
+  static constexpr uint32_t kScale = kV + 2 * kTile;     // [stage][K, V, log2 V][128] FP32
+  static constexpr uint32_t kNan = kScale + 2 * 3 * kKeys * 4;         // [stage][token][D / 32] bits of V's NaN codes
   static constexpr uint32_t kRowNan = kNan + 2 * kKeys * (D / 32) * 4; // [row][D / 32]: dims whose output is NaN
   static constexpr uint32_t kBar = kRowNan + 256 * (D / 32) * 4;
   static constexpr uint32_t kBytes = kBar + 256;
   static constexpr uint32_t kS = 0, kO = 256;            // TMEM columns: scores 2 x 128, then outputs 2 x D
 };
+
+// ---------------------------------------------------------------- a row's scores
+// A thread's row of a 128-key tile: bare products in TMEM at s_at, K's and V's
+// scales per token (of whole pages per 16 tokens), rf the row's factor; z = s k rf.
+// MASK: only columns [lo_c, hi_c) are seen, and of these none whose K scale is 0 (a
+// token without a page).  Chunks of 32 columns; the next one is on its way while
+// one is worked on.
+template <bool PAGED16, bool MASK>
+__device__ __forceinline__ float row_max(uint32_t s_at, const float* ks, float rf, int32_t lo_c, int32_t hi_c) {
+  float mt = kNegInf;
+  uint32_t x[2][32];
+  tm_ld32(s_at, x[0]);
+#pragma unroll
+  for (int c = 0; c < kKeys / 32; ++c) {
+    tm_wait_ld();
+    if (c + 1 < kKeys / 32) tm_ld32(s_at + 32 * (c + 1), x[(c + 1) & 1]);
+    if (PAGED16) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const float k = ks[32 * c + 16 * g];
+        const int32_t hg = MASK && k == 0.0f ? -1 : hi_c;
+        float y[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int col = 32 * c + 16 * g + i;
+          y[i] = __uint_as_float(x[c & 1][16 * g + i]);
+          if (MASK && !(col < hg && col >= lo_c)) y[i] = kNegInf;
+        }
+#pragma unroll
+        for (int i = 0; i < 5; ++i) y[i] = max3(y[3 * i], y[3 * i + 1], y[3 * i + 2]);
+        y[0] = max3(max3(y[0], y[1], y[2]), max3(y[3], y[4], y[15]), kNegInf);
+        mt = fmaxf(mt, __fmul_rn(y[0], __fmul_rn(k, rf)));  // (a hole: -inf * 0, which the maximum leaves out)
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; i += 4) {
+        const float4 k = *reinterpret_cast<const float4*>(ks + 32 * c + i);
+        const float kk[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int col = 32 * c + i + e;
+          float z = __fmul_rn(__uint_as_float(x[c & 1][i + e]), __fmul_rn(kk[e], rf));
+          if (MASK && !(col < hi_c && col >= lo_c && kk[e] != 0.0f)) z = kNegInf;
+          mt = fmaxf(mt, z);
+        }
+      }
+    }
+  }
+  return mt;
+}
+// The weights times V's scale (relative to the row's reference, 2^-lref), as FP16
+// over the scores; the sum of the bare weights.  The scale goes into the exponent,
+// w = 2^(z - base + lv + lref) with lv its logarithm, and out of the sum again by
+// its inverse, once for the tokens that share it.
+// EXACT: z rounded as row_max rounded it before base is taken off.
+template <bool PAGED16, bool MASK, bool EXACT>
+__device__ __forceinline__ float row_weights(uint32_t s_at, const float* ks, const float* lv, float rf, float lref,
+                                             float base, int32_t lo_c, int32_t hi_c) {
+  constexpr int G = PAGED16 ? 16 : 4;  // columns handled together; of whole pages they share their scales
+  float total = 0.0f;
+  uint32_t x[2][32];
+  tm_ld32(s_at, x[0]);
+#pragma unroll
+  for (int c = 0; c < kKeys / 32; ++c) {
+    tm_wait_ld();
+    if (c + 1 < kKeys / 32) tm_ld32(s_at + 32 * (c + 1), x[(c + 1) & 1]);
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 32; i += G) {
+      const int col = 32 * c + i;
+      float kk[4], ll[4];
+      if (PAGED16) {
+        kk[0] = kk[1] = kk[2] = kk[3] = ks[col];
+        ll[0] = ll[1] = ll[2] = ll[3] = lv[col] + lref;
+        // a page that the row sees nothing of: its scale must not matter
+        if (MASK && (col >= hi_c || col + 16 <= lo_c)) ll[0] = ll[1] = ll[2] = ll[3] = 0.0f;
+      } else {
+        const float4 k = *reinterpret_cast<const float4*>(ks + col), l = *reinterpret_cast<const float4*>(lv + col);
+        kk[0] = k.x; kk[1] = k.y; kk[2] = k.z; kk[3] = k.w;
+        ll[0] = l.x + lref; ll[1] = l.y + lref; ll[2] = l.z + lref; ll[3] = l.w + lref;
+      }
+      float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int e = 0; e < G; e += 2) {
+        const float k0 = kk[e & 3], k1 = kk[(e + 1) & 3];
+        const float2 xx = make_float2(__uint_as_float(x[c & 1][i + e]), __uint_as_float(x[c & 1][i + e + 1]));
+        const float2 f = make_float2(__fmul_rn(k0, rf), __fmul_rn(k1, rf));
+        float2 z;
+        if (EXACT)
+          z = make_float2(__fadd_rn(__fadd_rn(__fmul_rn(xx.x, f.x), -base), ll[e & 3]),
+                          __fadd_rn(__fadd_rn(__fmul_rn(xx.y, f.y), -base), ll[(e + 1) & 3]));
+        else
+          z = fma2(xx, f, make_float2(ll[e & 3] - base, ll[(e + 1) & 3] - base));
+        if (MASK) {
+          z.x = col + e < hi_c && col + e >= lo_c && k0 != 0.0f ? z.x : kNegInf;
+          z.y = col + e + 1 < hi_c && col + e + 1 >= lo_c && k1 != 0.0f ? z.y : kNegInf;
+        }
+        const float2 y = make_float2(ex2(z.x), ex2(z.y));
+        if (PAGED16) {
+          sum = add2(sum, y);
+        } else {
+          if (!MASK || z.x != kNegInf) total += y.x * ex2(-ll[e & 3]);
+          if (!MASK || z.y != kNegInf) total += y.y * ex2(-ll[(e + 1) & 3]);
+        }
+        w[(i + e) / 2] = pack2<0>(y.x, y.y);
+      }
+      if (PAGED16) total += (sum.x + sum.y) * ex2(-ll[0]);
+    }
+    tm_st16(s_at + 16 * c, w);
+  }
+  return total;
+}
+
+// ---------------------------------------------------------------- codes to FP16 tiles
+// W warps bring K (IS_K) or V of tile after tile into its two stages.  A 16-byte
+// chunk of codes, CPR of a 64-dim group a token, a thread to each, makes two 16-byte
+// chunks of FP16 (8 lanes in turn, 4 chunks of two tokens, write to 8 different bank
+// groups).  The codes of the next tile are on their way while one is written, its
+// pages known a tile earlier.
+template <int D, bool PAGED16, bool IS_K, int W>
+__device__ __forceinline__ void load_tiles(const C8Params& p, const C8Seq& q, uint8_t* smem, uint32_t head, int32_t lo,
+                                           int32_t hi, int32_t n_steps, uint32_t full, uint32_t empty,
+                                           volatile uint32_t* stop, uint32_t* nan_seen) {
+  using S = PromptShape<D>;
+  constexpr int CPR = D >= 64 ? 4 : 2;
+  constexpr int RPI = W * 32 / CPR;                        // token rows at once
+  constexpr int NR = (kKeys + RPI - 1) / RPI, N = NR * S::DG;  // chunks of a thread and tile: rows, then groups
+  const uint32_t lane = threadIdx.x & 31u;
+  const uint32_t lt = threadIdx.x - (kSoftWarps + (IS_K ? 0 : kKWarps)) * 32u;
+  const uint32_t row = lt / CPR, c = lt % CPR;
+  const uint8_t* src = (IS_K ? p.k : p.v) + (int64_t)head * p.sh + c * 16;
+  const uint32_t dst0 = row * 128 + (((2 * c) ^ (row & 7u)) << 4), dst1 = row * 128 + (((2 * c + 1) ^ (row & 7u)) << 4);
+  bool bad = false;
+  // Byte offset in the cache of a token's row (PAGED16: of a run of 16 tokens), -1:
+  // none.  PAGED16: lane g & 7 holds the offset and page of run g of a tile; tokens
+  // past the last one in its run hold anything.
+  auto place = [&](int32_t tok, int32_t& id) -> int64_t {
+    id = -1;
+    if (tok >= hi) return -1;
+    const uint32_t i = c8_div_t(p, (uint32_t)tok);
+    id = c8_page(p, q.s, i);
+    if (id < 0) {
+      bad = true;
+      return -1;
+    }
+    return (int64_t)id * p.sb + (int64_t)((uint32_t)tok - i * p.T) * p.st;
+  };
+  uint4 x[N];  // (of tokens without a page: what an earlier tile had; their scales are 0)
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = make_uint4(0, 0, 0, 0);
+  const int64_t row_off[2] = {(int64_t)(row & 15u) * p.st, (int64_t)((row + RPI) & 15u) * p.st};
+  // the scales of both, brought with V: a V stage stays until the softmax is done with its tile, a K stage does not
+  float ksc[(kKeys + W * 32 - 1) / (W * 32)], vsc[(kKeys + W * 32 - 1) / (W * 32)];
+  int32_t id = -1;
+  int64_t run = -1;
+  auto ask = [&](int32_t j) {  // runs of tile j
+    run = -1;
+    id = -1;
+    if (PAGED16 && j < n_steps) run = place(lo + j * kKeys + 16 * (int32_t)(lane & 7u), id);
+  };
+  auto fetch = [&](int32_t j) {
+    const int32_t tok0 = lo + j * kKeys;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const uint32_t r = i * RPI + row;  // token row of the tile
+      int64_t off = -1;
+      if (PAGED16) {
+        off = __shfl_sync(0xffffffffu, run, (r >> 4) & 7u);
+      } else if (kKeys % RPI == 0 || r < kKeys) {
+        int32_t ignore;
+        off = place(tok0 + (int32_t)r, ignore);
+      }
+      if (off >= 0 && (kKeys % RPI == 0 || r < kKeys)) {
+        const uint8_t* at = src + off + (PAGED16 ? row_off[i & 1] : 0);
+#pragma unroll
+        for (int g = 0; g < S::DG; ++g) x[i * S::DG + g] = ld_nc16(at + 64 * g);
+      }
+    }
+#pragma unroll
+    for (int i = 0; !IS_K && i * W * 32 < kKeys; ++i) {
+      const uint32_t r = i * W * 32 + lt;
+      int32_t at = PAGED16 ? __shfl_sync(0xffffffffu, id, (r >> 4) & 7u) : -1;
+      if (!PAGED16 && r < kKeys) place(tok0 + (int32_t)r, at);
+      ksc[i] = at >= 0 ? ldg_f32(p.k_scale + (int64_t)at * p.H + head) : 0.0f;
+      vsc[i] = at >= 0 ? ldg_f32(p.v_scale + (int64_t)at * p.H + head) : 0.0f;
+    }
+  };
+  auto nan_of = [](uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; };
+  ask(0);
+  if (n_steps > 0) fetch(0);
+  ask(1);
+  for (int32_t j = 0; j < n_steps; ++j) {
+    const uint32_t st = j & 1, ph = (j >> 1) & 1;
+    if (!__all_sync(0xffffffffu, mbar_wait(empty + 8 * st, ph ^ 1u, stop))) break;
+    uint8_t* tile = smem + (IS_K ? S::kK : S::kV) + st * S::kTile;
+    if (!IS_K) {
+      uint32_t any = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) any |= nan_of(x[i].x) | nan_of(x[i].y) | nan_of(x[i].z) | nan_of(x[i].w);
+      any = __any_sync(0xffffffffu, any != 0u) ? 1u : 0u;
+      if (any) {  // NaN codes become 0; where they were is kept, a bit each, for the rows that see them
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          uint32_t* w = reinterpret_cast<uint32_t*>(&x[i]);
+          uint32_t bits = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t nb = nan_of(w[k]);
+            w[k] &= ~((nb >> 7) * 0xffu);
+            bits |= (((nb >> 7) * 0x01020408u) >> 24) << (4 * k);  // one bit per byte, in order
+          }
+          const uint32_t r = (i / S::DG) * RPI + row;
+          if (r < kKeys)
+            reinterpret_cast<uint16_t*>(smem + S::kNan)[(st * kKeys + r) * (D / 16) + (i % S::DG) * 4 + c] =
+                (uint16_t)bits;
+        }
+      }
+      if (lane == 0) reinterpret_cast<uint8_t*>(nan_seen)[4 * st + (lt >> 5)] = (uint8_t)any;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      uint4 h0, h1;
+      c8_dec4(x[i].x, h0.x, h0.y);
+      c8_dec4(x[i].y, h0.z, h0.w);
+      c8_dec4(x[i].z, h1.x, h1.y);
+      c8_dec4(x[i].w, h1.z, h1.w);
+      uint8_t* at = tile + (i % S::DG) * (kKeys * 128) + (i / S::DG) * (RPI * 128);
+      if (kKeys % RPI == 0 || (i / S::DG) * RPI + row < kKeys) {
+        *reinterpret_cast<uint4*>(at + dst0) = h0;
+        *reinterpret_cast<uint4*>(at + dst1) = h1;
+      }
+    }
+    float* sc = reinterpret_cast<float*>(smem + S::kScale) + st * 3 * kKeys;
+#pragma unroll
+    for (int i = 0; !IS_K && i * W * 32 < kKeys; ++i)
+      if (kKeys % (W * 32) == 0 || i * W * 32 + lt < kKeys) {
+        sc[i * W * 32 + lt] = ksc[i];
+        sc[kKeys + i * W * 32 + lt] = vsc[i];
+        sc[2 * kKeys + i * W * 32 + lt] = vsc[i] > 0.0f ? lg2(vsc[i]) : vsc[i];
+      }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    mbar_arrive(full + 8 * st);
+    __syncwarp();
+    if (j + 1 < n_steps) fetch(j + 1);
+    ask(j + 2);
+  }
+  if (bad) c8_error(p, q.s, KV_CACHE8_BAD_PAGE);
+}
 
 template <int DT, int D, bool PAGED16>
 __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __grid_constant__ C8Params p) {
@@ -180,31 +441,38 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
   const uint32_t bar = sbase + S::kBar;
   const uint32_t k_full = bar, k_empty = bar + 16, v_full = bar + 32, v_empty = bar + 48;  // [2]
   const uint32_t s_full = bar + 64, p_full = bar + 80, pv_done = bar + 96;                  // [2]
+  const uint32_t q_full = bar + 144;
   volatile uint32_t* stop = reinterpret_cast<volatile uint32_t*>(smem + S::kBar + 112);
   uint32_t* nan_seen = reinterpret_cast<uint32_t*>(smem + S::kBar + 116);   // [stage]: a byte a loading warp, V has NaN codes
   uint32_t* any_row_nan = reinterpret_cast<uint32_t*>(smem + S::kBar + 124);
   uint32_t* tm_at = reinterpret_cast<uint32_t*>(smem + S::kBar + 128);
   if (tid == 0) {
     for (uint32_t i = 0; i < 2; ++i) {
-      mbar_init(k_full + 8 * i, kLoadWarps * 32);
+      mbar_init(k_full + 8 * i, kKWarps * 32);
       mbar_init(k_empty + 8 * i, 1);
-      mbar_init(v_full + 8 * i, kLoadWarps * 32);
+      mbar_init(v_full + 8 * i, kVWarps * 32);
       mbar_init(v_empty + 8 * i, 1);
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_full + 8 * i, 128);
       mbar_init(pv_done + 8 * i, 1);
       nan_seen[i] = 0;
     }
+    mbar_init(q_full, 256);
     *stop = 0;
     *any_row_nan = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kSoftWarps + kLoadWarps) {
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      (uint32_t)__cvta_generic_to_shared(tm_at))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = *tm_at;
 
   // ---- Q to shared memory, a softmax thread to a row; bf16 rows are scaled by a
   // power of two into FP16's range (exact but for values 2^-39 of the row's largest)
@@ -246,16 +514,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) rn[k] = 0;
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    mbar_arrive(q_full);
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tm = *tm_at;
 
   if (warp < kSoftWarps) {
     // ================================================================ softmax
     const uint32_t t = warp >> 2;
-    float m = kNegInf, l = 0.0f, vref = 1.17549435e-38f, vinv = 0.0f;
+    float m = kNegInf, l = 0.0f, vref = 1.17549435e-38f, lref = 0.0f;  // lref: 11 - log2(vref), once the row has seen a scale
     bool fine = true;
     if (t < n_tiles) {
       const uint32_t tl = tm + ((warp & 3u) << 21);  // the warp's 32 lanes (lane << 16)
@@ -272,7 +537,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
       for (int32_t j = 0; j < n_steps && fine; ++j) {
         const int32_t tok0 = lo + j * kKeys;
         const uint32_t st = j & 1;
-        const float* ks = reinterpret_cast<const float*>(smem + S::kScale) + st * 2 * kKeys;
+        const float* ks = reinterpret_cast<const float*>(smem + S::kScale) + st * 3 * kKeys;
         const float* vs = ks + kKeys;
         fine = mbar_wait(v_full + 8 * st, (j >> 1) & 1, stop) && mbar_wait(s_full + 8 * t, j & 1, stop);
         fine = __all_sync(0xffffffffu, fine);
@@ -305,50 +570,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
           for (int32_t c = max(0, vis_lo - tok0); c < min(kKeys, vis_hi - tok0); ++c) vt = fmaxf(vt, vs[c]);
           __syncwarp();
         }
-        // 32 scores, scaled and masked
-        auto load = [&](int c, float (&z)[32]) {
-          uint32_t x[32];
-          tm_ld32(s_at + 32 * c, x);
-          tm_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int col = 32 * c + i;
-            z[i] = __uint_as_float(x[i]) * (ks[PAGED16 ? col & ~15 : col] * rf);
-            if (masked) {
-              const int32_t tok = tok0 + col;
-              if (tok >= vis_hi || tok < vis_lo || ks[PAGED16 ? col & ~15 : col] == 0.0f) z[i] = kNegInf;
-            }
-          }
-        };
-        float mt = kNegInf;
-        // whole tiles of 16-token pages: a factor for 16 columns, maxima of the bare products
-        const bool whole = PAGED16 && !masked;
-        if (whole) {
-          uint32_t x[2][32];
-          tm_ld32(s_at, x[0]);
-#pragma unroll
-          for (int c = 0; c < kKeys / 32; ++c) {
-            tm_wait_ld();
-            if (c + 1 < kKeys / 32) tm_ld32(s_at + 32 * (c + 1), x[(c + 1) & 1]);
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              float y[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                y[i] = fmaxf(fmaxf(__uint_as_float(x[c & 1][16 * g + i]), __uint_as_float(x[c & 1][16 * g + 4 + i])),
-                             fmaxf(__uint_as_float(x[c & 1][16 * g + 8 + i]), __uint_as_float(x[c & 1][16 * g + 12 + i])));
-              mt = fmaxf(mt, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) * (ks[32 * c + 16 * g] * rf));
-            }
-          }
-        } else {
-#pragma unroll 1
-          for (int c = 0; c < kKeys / 32; ++c) {
-            float z[32];
-            load(c, z);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) mt = fmaxf(mt, z[i]);
-          }
-        }
+        // columns [lo_c, hi_c) of the tile are seen
+        const int32_t hi_c = vis_hi - tok0, lo_c = vis_lo - tok0;
+        float mt = masked ? row_max<PAGED16, true>(s_at, ks, rf, lo_c, hi_c)
+                          : row_max<PAGED16, false>(s_at, ks, rf, lo_c, hi_c);
         const bool grow = mt > m + kLag;
         if (__any_sync(0xffffffffu, grow || vt > vref)) {
           const float vn = fmaxf(vt, vref);
@@ -373,74 +598,43 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
             }
           }
           vref = vn;
-          vinv = kLift / vn;
+          if (vn > 1.17549435e-38f) lref = kLift - lg2(vn);
         }
         const float base = m == kNegInf ? 0.0f : m;
+        // (bits are kept by the loading warps that saw one: rows 8 w .. 8 w + 7 of a round of kVWarps * 8)
+        auto tok_nan = [&](int32_t c) {
+          constexpr int R = D >= 64 ? 8 : 16;
+          return (nan_seen[st] >> (8 * ((c / R) % kVWarps))) & 1u;
+        };
         if (masked && nan_seen[st]) {
           // V has NaN codes (laid out as 0): the dims that a token seen by this row has them at
           const uint32_t* bits = reinterpret_cast<const uint32_t*>(smem + S::kNan) + st * kKeys * (D / 32);
           uint32_t* rn = reinterpret_cast<uint32_t*>(smem + S::kRowNan) + r * (D / 32);
           uint32_t any = 0;
           for (int32_t c = max(0, vis_lo - tok0); c < min(kKeys, vis_hi - tok0); ++c)
-            for (int k = 0; k < D / 32; ++k) {
-              const uint32_t b = bits[c * (D / 32) + k];
-              any |= b;
-              rn[k] |= b;
-            }
+            if (tok_nan(c))
+              for (int k = 0; k < D / 32; ++k) {
+                const uint32_t b = bits[c * (D / 32) + k];
+                any |= b;
+                rn[k] |= b;
+              }
           if (any) *any_row_nan = 1;
         } else if (nan_seen[st]) {
           const uint32_t* bits = reinterpret_cast<const uint32_t*>(smem + S::kNan) + st * kKeys * (D / 32);
           uint32_t* rn = reinterpret_cast<uint32_t*>(smem + S::kRowNan) + r * (D / 32);
           for (int32_t c = 0; c < kKeys; ++c)
-            for (int k = 0; k < D / 32; ++k) rn[k] |= bits[c * (D / 32) + k];
+            if (tok_nan(c))
+              for (int k = 0; k < D / 32; ++k) rn[k] |= bits[c * (D / 32) + k];
           *any_row_nan = 1;
         }
         __syncwarp();
         // 2^(s f - m) in one step, unless m is so large that its own rounding would show
-        if (whole && !__any_sync(0xffffffffu, fabsf(base) >= 1048576.0f)) {
-          float2 sum = make_float2(0.0f, 0.0f);
-          const float2 nb = make_float2(-base, -base);
-          uint32_t x[2][32];
-          tm_ld32(s_at, x[0]);
-#pragma unroll
-          for (int c = 0; c < kKeys / 32; ++c) {
-            tm_wait_ld();
-            if (c + 1 < kKeys / 32) tm_ld32(s_at + 32 * (c + 1), x[(c + 1) & 1]);
-            uint32_t w[16];
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              const float f = ks[32 * c + 16 * g] * rf, v = vs[32 * c + 16 * g] * vinv;
-              const float2 f2 = make_float2(f, f), v2 = make_float2(v, v);
-#pragma unroll
-              for (int i = 16 * g; i < 16 * g + 16; i += 2) {
-                const float2 z = fma2(make_float2(__uint_as_float(x[c & 1][i]), __uint_as_float(x[c & 1][i + 1])), f2, nb);
-                const float2 e = make_float2(ex2(z.x), ex2(z.y));
-                sum = add2(sum, e);
-                const float2 y = mul2(e, v2);
-                w[i / 2] = pack2<0>(y.x, y.y);
-              }
-            }
-            tm_st16(s_at + 16 * c, w);
-          }
-          l += sum.x + sum.y;
-        } else {
-#pragma unroll 1
-          for (int c = 0; c < kKeys / 32; ++c) {
-            float z[32];
-            load(c, z);
-            uint32_t w[16];
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float p0 = ex2(z[i] - base), p1 = ex2(z[i + 1] - base);
-              l += p0 + p1;
-              const float v0 = vs[PAGED16 ? (32 * c + i) & ~15 : 32 * c + i], v1 = vs[PAGED16 ? (32 * c + i) & ~15 : 32 * c + i + 1];
-              // 0 whatever the scale of the page that holds a token the row does not see
-              const float w0 = z[i] == kNegInf ? 0.0f : p0 * (v0 * vinv), w1 = z[i + 1] == kNegInf ? 0.0f : p1 * (v1 * vinv);
-              w[i / 2] = pack2<0>(w0, w1);
-            }
-            tm_st16(s_at + 16 * c, w);
-          }
-        }
+        if (__any_sync(0xffffffffu, fabsf(base) >= 1048576.0f))
+          l += row_weights<PAGED16, true, true>(s_at, ks, vs + kKeys, rf, lref, base, lo_c, hi_c);
+        else if (masked)
+          l += row_weights<PAGED16, true, false>(s_at, ks, vs + kKeys, rf, lref, base, lo_c, hi_c);
+        else
+          l += row_weights<PAGED16, false, false>(s_at, ks, vs + kKeys, rf, lref, base, lo_c, hi_c);
         tm_wait_st();
         tc_fence_before();
         mbar_arrive(p_full + 8 * t);
@@ -451,7 +645,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
         tc_fence_after();
       }
       if (fine) {
-        const float inv = l == 0.0f ? 0.0f : vref / (l * kLift);
+        const float inv = l == 0.0f ? 0.0f : vref / (l * 2048.0f);
         uint16_t* out = p.b + ((int64_t)q.row + tok_r) * p.b_row + (int64_t)hd * p.b_head;
         const uint32_t* rn = reinterpret_cast<const uint32_t*>(smem + S::kRowNan) + r * (D / 32);
         const bool fix = *any_row_nan != 0u;
@@ -483,202 +677,76 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
               __float_as_uint(l == 0.0f ? kNegInf : (m + log2f(l)) * 0.693147180559945309f));
       }
     }
-  } else if (warp < kSoftWarps + kLoadWarps) {
+  } else if (warp < kMmaWarp) {
     // ================================================================ codes to FP16 tiles
-    // 16-byte chunks of codes: chunk c of token row i * RPI + row; a chunk makes two
-    // 16-byte chunks of FP16, written by lanes c, c + 4 in opposite order (8 lanes then
-    // hit 8 different bank groups)
-    constexpr int CPR = D / 16;                  // chunks of a token
-    constexpr int RPI = kLoadWarps * 32 / CPR;   // token rows at once
-    constexpr int N = kKeys / RPI;               // chunks of a thread and tile
-    const uint32_t lt = tid - kSoftWarps * 32u;
-    const uint32_t row = lt / CPR, c = lt % CPR;
-    const uint8_t* kb = p.k + (int64_t)head * p.sh + c * 16;
-    const uint8_t* vb = p.v + (int64_t)head * p.sh + c * 16;
-    const uint32_t dst = (c >> 2) * (kKeys * 128);
-    const uint32_t flip = (c >> 2) & 1u;
-    bool bad = false;
-    // Byte offset in the cache of a token's row (PAGED16: of a run of 16 tokens), -1:
-    // none.  PAGED16: lane g & 7 holds the offset and page of run g of a tile, asked
-    // for a tile ahead; tokens past the last one in its run hold anything.
-    auto place = [&](int32_t tok, int32_t& id) -> int64_t {
-      id = -1;
-      if (tok >= hi) return -1;
-      const uint32_t i = c8_div_t(p, (uint32_t)tok);
-      id = c8_page(p, q.s, i);
-      if (id < 0) {
-        bad = true;
-        return -1;
-      }
-      return (int64_t)id * p.sb + (int64_t)((uint32_t)tok - i * p.T) * p.st;
-    };
-    const int64_t row_off = (int64_t)(row & 15u) * p.st;
-    uint4 kc[N], vc[N];
-    float ksc = 0.0f, vsc = 0.0f;
-    int32_t id = -1, id_next = -1;
-    int64_t run = -1, run_next = -1;
-    auto ask = [&](int32_t j) {  // runs of tile j
-      run_next = -1;
-      id_next = -1;
-      if (PAGED16 && j < n_steps) run_next = place(lo + j * kKeys + 16 * (int32_t)(lane & 7u), id_next);
-    };
-    auto off_of = [&](int32_t j, int i) -> int64_t {
-      if (PAGED16) {
-        const int64_t o = __shfl_sync(0xffffffffu, run, (i * RPI + row) >> 4);
-        return o >= 0 ? o + row_off : -1;
-      }
-      int32_t x;
-      return place(lo + j * kKeys + (int32_t)(i * RPI + row), x);
-    };
-    auto fetch_k = [&](int32_t j) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int64_t off = off_of(j, i);
-        kc[i] = off >= 0 ? ld_nc16(kb + off) : make_uint4(0, 0, 0, 0);
-      }
-    };
-    auto fetch_v = [&](int32_t j) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int64_t off = off_of(j, i);
-        vc[i] = off >= 0 ? ld_nc16(vb + off) : make_uint4(0, 0, 0, 0);
-      }
-      ksc = vsc = 0.0f;
-      int32_t at = PAGED16 ? __shfl_sync(0xffffffffu, id, lt >> 4) : -1;
-      if (!PAGED16) place(lo + j * kKeys + (int32_t)lt, at);
-      if (at >= 0) {
-        ksc = ldg_f32(p.k_scale + (int64_t)at * p.H + head);
-        vsc = ldg_f32(p.v_scale + (int64_t)at * p.H + head);
-      }
-    };
-    auto put = [&](uint8_t* tile, int i, uint4 x) {
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      uint4 h[2];
-      c8_dec4(w[0], h[0].x, h[0].y);
-      c8_dec4(w[1], h[0].z, h[0].w);
-      c8_dec4(w[2], h[1].x, h[1].y);
-      c8_dec4(w[3], h[1].z, h[1].w);
-      const uint32_t tr = i * RPI + row;
-      uint8_t* at = tile + dst + tr * 128;
-#pragma unroll
-      for (uint32_t k = 0; k < 2; ++k) {
-        const uint32_t part = k ^ flip;
-        *reinterpret_cast<uint4*>(at + ((((c & 3u) * 2 + part) ^ (tr & 7u)) << 4)) = part ? h[1] : h[0];
-      }
-    };
-    ask(0);
-    run = run_next;
-    id = id_next;
-    if (n_steps > 0) {
-      fetch_k(0);
-      fetch_v(0);
-    }
-    ask(1);
-    bool fine = true;
-    for (int32_t j = 0; j < n_steps && fine; ++j) {
-      const uint32_t st = j & 1, ph = (j >> 1) & 1;
-      fine = __all_sync(0xffffffffu, mbar_wait(k_empty + 8 * st, ph ^ 1u, stop));
-      if (!fine) break;
-      uint8_t* kt = smem + S::kK + st * S::kTile;
-#pragma unroll
-      for (int i = 0; i < N; ++i) put(kt, i, kc[i]);
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(k_full + 8 * st);
-      run = run_next;
-      id = id_next;
-      __syncwarp();
-      if (j + 1 < n_steps) fetch_k(j + 1);
-      fine = __all_sync(0xffffffffu, mbar_wait(v_empty + 8 * st, ph ^ 1u, stop));
-      if (!fine) break;
-      uint8_t* vt = smem + S::kV + st * S::kTile;
-      uint32_t any = 0;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(&vc[i]);
-        uint32_t bits = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t nb = ((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-          w[k] &= ~((nb >> 7) * 0xffu);
-          bits |= (((nb >> 7) * 0x01020408u) >> 24) << (4 * k);  // one bit per byte, in order
-        }
-        any |= bits;
-        // 16 bits of the token's D, kept for the rows that see it
-        reinterpret_cast<uint16_t*>(smem + S::kNan)[(st * kKeys + i * RPI + row) * (D / 16) + c] = (uint16_t)bits;
-        put(vt, i, vc[i]);
-      }
-      any = __any_sync(0xffffffffu, any != 0u) ? 1u : 0u;
-      if (lane == 0) reinterpret_cast<uint8_t*>(nan_seen)[4 * st + warp - kSoftWarps] = (uint8_t)any;
-      float* sc = reinterpret_cast<float*>(smem + S::kScale) + st * 2 * kKeys;
-      sc[lt] = ksc;
-      sc[kKeys + lt] = vsc;
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(v_full + 8 * st);
-      __syncwarp();
-      if (j + 1 < n_steps) fetch_v(j + 1);
-      ask(j + 2);
-    }
-    if (bad) c8_error(p, q.s, KV_CACHE8_BAD_PAGE);
-  } else if (lane == 0 && n_steps > 0) {
+    if (warp < kSoftWarps + kKWarps)
+      load_tiles<D, PAGED16, true, kKWarps>(p, q, smem, head, lo, hi, n_steps, k_full, k_empty, stop, nan_seen);
+    else
+      load_tiles<D, PAGED16, false, kVWarps>(p, q, smem, head, lo, hi, n_steps, v_full, v_empty, stop, nan_seen);
+  } else if (n_steps > 0) {
     // ================================================================ products
+    // The whole warp walks, one lane issues: what the instructions take is uniform.
+    // (All 512 columns are allocated, so TMEM starts at column 0.)
+    const bool one = elect_one();
     bool fine = true;
+    constexpr uint64_t kDescK = tc_desc(0, 16, 1024), kDescV = tc_desc(0, kKeys * 128, 1024);
+    const uint32_t q_lo = (sbase + S::kQ) >> 4, k_lo = (sbase + S::kK) >> 4, v_lo = (sbase + S::kV) >> 4;
     auto scores = [&](uint32_t t, int32_t j) {
-      const uint32_t a = sbase + S::kQ + t * S::kQTile, b = sbase + S::kK + (j & 1) * S::kTile;
+      const uint64_t a = kDescK | (q_lo + t * (S::kQTile >> 4)), b = kDescK | (k_lo + (j & 1) * (S::kTile >> 4));
+      if (one) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        tc_mma_ss(tm + S::kS + t * 128, tc_desc(a + (k >> 2) * (128 * 128) + (k & 3) * 32, 16, 1024),
-                  tc_desc(b + (k >> 2) * (kKeys * 128) + (k & 3) * 32, 16, 1024), tc_idesc(kKeys, 0), k > 0);
-      tc_commit(s_full + 8 * t);
+        for (int k = 0; k < D / 16; ++k)
+          tc_mma_ss(S::kS + t * 128, a + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
+                    b + (((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4), tc_idesc(kKeys, 0), k > 0);
+        tc_commit(s_full + 8 * t);
+      }
     };
-    fine = mbar_wait(k_full, 0, stop);
-    if (fine) {
+    auto wait = [&](uint32_t at, uint32_t parity) {
+      fine = __all_sync(0xffffffffu, mbar_wait(at, parity, stop));
+      __syncwarp();
       tc_fence_after();
+      return fine;
+    };
+    if (wait(q_full, 0) && wait(k_full, 0)) {
       for (uint32_t t = 0; t < n_tiles; ++t) scores(t, 0);
-      tc_commit(k_empty);
+      if (one) tc_commit(k_empty);
     }
     for (int32_t j = 0; j < n_steps && fine; ++j) {
       const uint32_t st = j & 1;
-      fine = mbar_wait(v_full + 8 * st, (j >> 1) & 1, stop);
-      if (!fine) break;
+      if (!wait(v_full + 8 * st, (j >> 1) & 1)) break;
       for (uint32_t t = 0; t < n_tiles; ++t) {
-        fine = mbar_wait(p_full + 8 * t, j & 1, stop);
-        if (!fine) break;
-        tc_fence_after();
-        const uint32_t b = sbase + S::kV + st * S::kTile;
+        if (!wait(p_full + 8 * t, j & 1)) break;
+        const uint64_t b = kDescV | (v_lo + st * (S::kTile >> 4));
+        if (one) {
 #pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
-          tc_mma_ts(tm + S::kO + t * D, tm + S::kS + t * 128 + 8 * k, tc_desc(b + k * 2048, kKeys * 128, 1024),
-                    tc_idesc(D, 1), j > 0 || k > 0);
-        tc_commit(pv_done + 8 * t);
-        if (t + 1 == n_tiles) tc_commit(v_empty + 8 * st);
+          for (int k = 0; k < kKeys / 16; ++k)
+            tc_mma_ts(S::kO + t * D, S::kS + t * 128 + 8 * k, b + ((k * 2048) >> 4), tc_idesc(D, 1), j > 0 || k > 0);
+          tc_commit(pv_done + 8 * t);
+          if (t + 1 == n_tiles) tc_commit(v_empty + 8 * st);
+        }
         if (j + 1 < n_steps) {
-          if (t == 0) {
-            fine = mbar_wait(k_full + 8 * ((j + 1) & 1), ((j + 1) >> 1) & 1, stop);
-            if (!fine) break;
-            tc_fence_after();
-          }
+          if (t == 0 && !wait(k_full + 8 * ((j + 1) & 1), ((j + 1) >> 1) & 1)) break;
           scores(t, j + 1);
-          if (t + 1 == n_tiles) tc_commit(k_empty + 8 * ((j + 1) & 1));
+          if (one && t + 1 == n_tiles) tc_commit(k_empty + 8 * ((j + 1) & 1));
         }
       }
     }
-    if (!fine) {
+    if (!fine && one) {
       // products still in flight end before their memory goes
-      uint32_t* spare = reinterpret_cast<uint32_t*>(smem + S::kBar + 136);
-      const uint32_t sb = (uint32_t)__cvta_generic_to_shared(spare);
+      const uint32_t sb = (uint32_t)__cvta_generic_to_shared(smem + S::kBar + 136);
       mbar_init(sb, 1);
       tc_commit(sb);
       *stop = 0u;  // the others have given up or will at their own limit
       mbar_wait(sb, 0, stop);
       *stop = 1u;
-      if (p.errors) atomicOr(p.errors + q.s, KV_CACHE8_STALLED);
+      c8_error(p, q.s, KV_CACHE8_STALLED);
     }
   }
   __syncwarp();
   tc_fence_before();
   // (counts threads: the roles' loops may leave a warp diverged)
   asm volatile("barrier.sync 0;" ::: "memory");
-  if (warp == kSoftWarps + kLoadWarps) {
+  if (warp == kMmaWarp) {
     __syncwarp();
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");

@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
         m[r] = mn;
         l[r] *= f;
         vref[r] = vn;
-        vinv[r] = kLift / vn;
+        vinv[r] = vt[r] > 0.0f || vinv[r] != 0.0f ? kLift / vn : 0.0f;  // 0 until the row has seen a scale
 #pragma unroll
         for (int n = 0; n < S::NT; ++n) {
           o[n][2 * r] *= fo;
