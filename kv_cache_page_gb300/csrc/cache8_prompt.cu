@@ -7,9 +7,9 @@
 // them, by the exponentials.  A CTA takes 256 rows (two tiles of 128: the G query
 // heads that share a KV head, times 256 / G new tokens) of one sequence and KV
 // head, and walks the keys 128 at a time:
-//   warps 8-11  read the codes, make FP16 of them (exactly) and lay them out for the
-//               tensor cores, K and V two tiles deep;
-//   warp 12     issues the products: scores of both row tiles into TMEM, weights
+//   warps 8-11, 12-14  read the codes of V and of K, make FP16 of them (exactly) and
+//               lay them out for the tensor cores, two tiles deep;
+//   warp 15     issues the products: scores of both row tiles into TMEM, weights
 //               (from TMEM) times V into accumulators in TMEM;
 //   warps 0-3, 4-7  the softmax of row tile 0 and 1, a thread to a row: scores from
 //               TMEM, weights back over them as FP16, the running maximum and sum.
@@ -32,7 +32,7 @@ constexpr float kNegInf = -INFINITY;
 // the step kernel holds them).
 constexpr float kLift = 11.0f, kLag = 4.0f;  // kLift: the logarithm
 constexpr int kKeys = 128;           // keys of a tile
-constexpr int kSoftWarps = 8, kKWarps = 4, kVWarps = 3, kMmaWarp = kSoftWarps + kKWarps + kVWarps;
+constexpr int kSoftWarps = 8, kVWarps = 4, kKWarps = 3, kMmaWarp = kSoftWarps + kKWarps + kVWarps;
 constexpr int kPromptThreads = (kMmaWarp + 1) * 32;
 constexpr long long kWaitClocks = 4000000000ll;
 constexpr uint32_t kWaitHint = 100000;  // ns that one try may sleep (polling would take issue slots from the softmax)
@@ -53,6 +53,17 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
+
+// The split of the registers between the roles (see the kernel).  The
+// bounds-checked build leaves it out: its checks are calls, which the compiler
+// cannot fit into a fixed split.
+#ifdef KVC_BOUNDS_CHECK
+__device__ __forceinline__ void regs_inc() {}
+__device__ __forceinline__ void regs_dec() {}
+#else
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 176;"); }
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
+#endif
 
 // ---------------------------------------------------------------- mbarriers
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
@@ -159,8 +170,9 @@ struct PromptShape {
   static constexpr uint32_t kQTile = DG * 128 * 128;     // bytes
   static constexpr uint32_t kTile = DG * kKeys * 128;    // of K or V
   static constexpr uint32_t kQ = 0, kK = 2 * kQTile, kV = kK + 2 * kTile;
-  static constexpr uint32_t kScale = kV + 2 * kTile;     // [stage][K, V, log2 V][128] FP32
-  static constexpr uint32_t kNan = kScale + 2 * 3 * kKeys * 4;         // [stage][token][D / 32] bits of V's NaN codes
+  static constexpr uint32_t kScale = kV + 2 * kTile;     // [stage] FP32: K[128], V[128], log2 V[128] (whole pages: 8 of each), V's largest, whether K has a 0
+  static constexpr uint32_t kScaleStage = (3 * kKeys + 4) * 4;
+  static constexpr uint32_t kNan = kScale + 2 * kScaleStage;         // [stage][token][D / 32] bits of V's NaN codes
   static constexpr uint32_t kRowNan = kNan + 2 * kKeys * (D / 32) * 4; // [row][D / 32]: dims whose output is NaN
   static constexpr uint32_t kBar = kRowNan + 256 * (D / 32) * 4;
   static constexpr uint32_t kBytes = kBar + 256;
@@ -168,35 +180,31 @@ struct PromptShape {
 };
 
 // ---------------------------------------------------------------- a row's scores
-// A thread's row of a 128-key tile: bare products in TMEM at s_at, K's and V's
-// scales per token (of whole pages per 16 tokens), rf the row's factor; z = s k rf.
-// MASK: only columns [lo_c, hi_c) are seen, and of these none whose K scale is 0 (a
-// token without a page).  Chunks of 32 columns; the next one is on its way while
-// one is worked on.
+// A thread's row of a 128-key tile: bare products x; K's and V's scales, of whole
+// pages per 16 tokens, else per token; rf the row's factor; z = x k rf.  MASK: only
+// columns [lo_c, hi_c) are seen, and of these none whose K scale is 0 (a token
+// without a page).
 template <bool PAGED16, bool MASK>
-__device__ __forceinline__ float row_max(uint32_t s_at, const float* ks, float rf, int32_t lo_c, int32_t hi_c) {
+__device__ __forceinline__ float row_max(const uint32_t (&x)[4][32], const float* ks, float rf, int32_t lo_c,
+                                         int32_t hi_c) {
   float mt = kNegInf;
-  uint32_t x[2][32];
-  tm_ld32(s_at, x[0]);
 #pragma unroll
   for (int c = 0; c < kKeys / 32; ++c) {
-    tm_wait_ld();
-    if (c + 1 < kKeys / 32) tm_ld32(s_at + 32 * (c + 1), x[(c + 1) & 1]);
     if (PAGED16) {
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const float k = ks[32 * c + 16 * g];
+        const float k = ks[2 * c + g];
         const int32_t hg = MASK && k == 0.0f ? -1 : hi_c;
         float y[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int col = 32 * c + 16 * g + i;
-          y[i] = __uint_as_float(x[c & 1][16 * g + i]);
+          y[i] = __uint_as_float(x[c][16 * g + i]);
           if (MASK && !(col < hg && col >= lo_c)) y[i] = kNegInf;
         }
 #pragma unroll
         for (int i = 0; i < 5; ++i) y[i] = max3(y[3 * i], y[3 * i + 1], y[3 * i + 2]);
-        y[0] = max3(max3(y[0], y[1], y[2]), max3(y[3], y[4], y[15]), kNegInf);
+        y[0] = fmaxf(max3(y[0], y[1], y[2]), max3(y[3], y[4], y[15]));
         mt = fmaxf(mt, __fmul_rn(y[0], __fmul_rn(k, rf)));  // (a hole: -inf * 0, which the maximum leaves out)
       }
     } else {
@@ -207,7 +215,7 @@ __device__ __forceinline__ float row_max(uint32_t s_at, const float* ks, float r
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int col = 32 * c + i + e;
-          float z = __fmul_rn(__uint_as_float(x[c & 1][i + e]), __fmul_rn(kk[e], rf));
+          float z = __fmul_rn(__uint_as_float(x[c][i + e]), __fmul_rn(kk[e], rf));
           if (MASK && !(col < hi_c && col >= lo_c && kk[e] != 0.0f)) z = kNegInf;
           mt = fmaxf(mt, z);
         }
@@ -222,24 +230,20 @@ __device__ __forceinline__ float row_max(uint32_t s_at, const float* ks, float r
 // its inverse, once for the tokens that share it.
 // EXACT: z rounded as row_max rounded it before base is taken off.
 template <bool PAGED16, bool MASK, bool EXACT>
-__device__ __forceinline__ float row_weights(uint32_t s_at, const float* ks, const float* lv, float rf, float lref,
-                                             float base, int32_t lo_c, int32_t hi_c) {
+__device__ __forceinline__ float row_weights(const uint32_t (&x)[4][32], uint32_t s_at, const float* ks, const float* lv,
+                                             float rf, float lref, float base, int32_t lo_c, int32_t hi_c) {
   constexpr int G = PAGED16 ? 16 : 4;  // columns handled together; of whole pages they share their scales
   float total = 0.0f;
-  uint32_t x[2][32];
-  tm_ld32(s_at, x[0]);
 #pragma unroll
   for (int c = 0; c < kKeys / 32; ++c) {
-    tm_wait_ld();
-    if (c + 1 < kKeys / 32) tm_ld32(s_at + 32 * (c + 1), x[(c + 1) & 1]);
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 32; i += G) {
       const int col = 32 * c + i;
       float kk[4], ll[4];
       if (PAGED16) {
-        kk[0] = kk[1] = kk[2] = kk[3] = ks[col];
-        ll[0] = ll[1] = ll[2] = ll[3] = lv[col] + lref;
+        kk[0] = kk[1] = kk[2] = kk[3] = ks[col / 16];
+        ll[0] = ll[1] = ll[2] = ll[3] = lv[col / 16] + lref;
         // a page that the row sees nothing of: its scale must not matter
         if (MASK && (col >= hi_c || col + 16 <= lo_c)) ll[0] = ll[1] = ll[2] = ll[3] = 0.0f;
       } else {
@@ -251,7 +255,7 @@ __device__ __forceinline__ float row_weights(uint32_t s_at, const float* ks, con
 #pragma unroll
       for (int e = 0; e < G; e += 2) {
         const float k0 = kk[e & 3], k1 = kk[(e + 1) & 3];
-        const float2 xx = make_float2(__uint_as_float(x[c & 1][i + e]), __uint_as_float(x[c & 1][i + e + 1]));
+        const float2 xx = make_float2(__uint_as_float(x[c][i + e]), __uint_as_float(x[c][i + e + 1]));
         const float2 f = make_float2(__fmul_rn(k0, rf), __fmul_rn(k1, rf));
         float2 z;
         if (EXACT)
@@ -294,7 +298,7 @@ __device__ __forceinline__ void load_tiles(const C8Params& p, const C8Seq& q, ui
   constexpr int RPI = W * 32 / CPR;                        // token rows at once
   constexpr int NR = (kKeys + RPI - 1) / RPI, N = NR * S::DG;  // chunks of a thread and tile: rows, then groups
   const uint32_t lane = threadIdx.x & 31u;
-  const uint32_t lt = threadIdx.x - (kSoftWarps + (IS_K ? 0 : kKWarps)) * 32u;
+  const uint32_t lt = threadIdx.x - (kSoftWarps + (IS_K ? kVWarps : 0)) * 32u;
   const uint32_t row = lt / CPR, c = lt % CPR;
   const uint8_t* src = (IS_K ? p.k : p.v) + (int64_t)head * p.sh + c * 16;
   const uint32_t dst0 = row * 128 + (((2 * c) ^ (row & 7u)) << 4), dst1 = row * 128 + (((2 * c + 1) ^ (row & 7u)) << 4);
@@ -344,11 +348,15 @@ __device__ __forceinline__ void load_tiles(const C8Params& p, const C8Seq& q, ui
         for (int g = 0; g < S::DG; ++g) x[i * S::DG + g] = ld_nc16(at + 64 * g);
       }
     }
+    if (!IS_K && PAGED16) {  // lane g & 7: run g
+      ksc[0] = id >= 0 ? ldg_f32(p.k_scale + (int64_t)id * p.H + head) : 0.0f;
+      vsc[0] = id >= 0 ? ldg_f32(p.v_scale + (int64_t)id * p.H + head) : 0.0f;
+    }
 #pragma unroll
-    for (int i = 0; !IS_K && i * W * 32 < kKeys; ++i) {
+    for (int i = 0; !IS_K && !PAGED16 && i * W * 32 < kKeys; ++i) {
       const uint32_t r = i * W * 32 + lt;
-      int32_t at = PAGED16 ? __shfl_sync(0xffffffffu, id, (r >> 4) & 7u) : -1;
-      if (!PAGED16 && r < kKeys) place(tok0 + (int32_t)r, at);
+      int32_t at = -1;
+      if (r < kKeys) place(tok0 + (int32_t)r, at);
       ksc[i] = at >= 0 ? ldg_f32(p.k_scale + (int64_t)at * p.H + head) : 0.0f;
       vsc[i] = at >= 0 ? ldg_f32(p.v_scale + (int64_t)at * p.H + head) : 0.0f;
     }
@@ -398,9 +406,24 @@ __device__ __forceinline__ void load_tiles(const C8Params& p, const C8Seq& q, ui
         *reinterpret_cast<uint4*>(at + dst1) = h1;
       }
     }
-    float* sc = reinterpret_cast<float*>(smem + S::kScale) + st * 3 * kKeys;
+    float* sc = reinterpret_cast<float*>(smem + S::kScale + st * S::kScaleStage);
+    if (!IS_K && PAGED16 && lt < 32u) {
+      float top = vsc[0];
 #pragma unroll
-    for (int i = 0; !IS_K && i * W * 32 < kKeys; ++i)
+      for (int d = 1; d < 8; d *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      const bool hole = __any_sync(0xffffffffu, ksc[0] == 0.0f);
+      if (lane < 8u) {
+        sc[lane] = ksc[0];
+        sc[kKeys + lane] = vsc[0];
+        sc[2 * kKeys + lane] = vsc[0] > 0.0f ? lg2(vsc[0]) : vsc[0];
+      }
+      if (lane == 0u) {
+        sc[3 * kKeys] = top;
+        sc[3 * kKeys + 1] = hole ? 1.0f : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; !IS_K && !PAGED16 && i * W * 32 < kKeys; ++i)
       if (kKeys % (W * 32) == 0 || i * W * 32 + lt < kKeys) {
         sc[i * W * 32 + lt] = ksc[i];
         sc[kKeys + i * W * 32 + lt] = vsc[i];
@@ -517,8 +540,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
     mbar_arrive(q_full);
   }
 
+  // Registers: 512 threads start with 128 each; the softmax takes 176 (a row's 128
+  // scores at once), the others keep 80: 256 x 176 + 256 x 80 = 512 x 128.
+  static_assert(kPromptThreads == 512 && kSoftWarps == 8, "");
   if (warp < kSoftWarps) {
     // ================================================================ softmax
+    regs_inc();
     const uint32_t t = warp >> 2;
     float m = kNegInf, l = 0.0f, vref = 1.17549435e-38f, lref = 0.0f;  // lref: 11 - log2(vref), once the row has seen a scale
     bool fine = true;
@@ -537,43 +564,48 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
       for (int32_t j = 0; j < n_steps && fine; ++j) {
         const int32_t tok0 = lo + j * kKeys;
         const uint32_t st = j & 1;
-        const float* ks = reinterpret_cast<const float*>(smem + S::kScale) + st * 3 * kKeys;
+        const float* ks = reinterpret_cast<const float*>(smem + S::kScale + st * S::kScaleStage);
         const float* vs = ks + kKeys;
         fine = mbar_wait(v_full + 8 * st, (j >> 1) & 1, stop) && mbar_wait(s_full + 8 * t, j & 1, stop);
         fine = __all_sync(0xffffffffu, fine);
         if (!fine) break;
         __syncwarp();
         tc_fence_after();
-        // holes of K: a token without a page has the scale 0
-        bool hole = false;
-        if (PAGED16) {
+        uint32_t x[4][32];
 #pragma unroll
-          for (int g = 0; g < kKeys / 16; ++g) hole |= ks[16 * g] == 0.0f;
-        } else {
+        for (int c = 0; c < kKeys / 32; ++c) tm_ld32(s_at + 32 * c, x[c]);
+        // holes of K (a token without a page has the scale 0), the largest scale of V
+        float vt = ks[3 * kKeys];
+        bool hole = ks[3 * kKeys + 1] != 0.0f;
+        if (!PAGED16) {
+          vt = 0.0f;
 #pragma unroll
-          for (int i = 0; i < kKeys / 32; ++i) hole |= ks[32 * i + lane] == 0.0f;
+          for (int i = 0; i < kKeys / 32; ++i) {
+            vt = fmaxf(vt, vs[32 * i + lane]);
+            hole |= ks[32 * i + lane] == 0.0f;
+          }
+#pragma unroll
+          for (int d = 1; d < 32; d *= 2) vt = fmaxf(vt, __shfl_xor_sync(0xffffffffu, vt, d));
           hole = __any_sync(0xffffffffu, hole);
         }
         const bool masked = hole || tok0 + kKeys > full_hi || tok0 < full_lo;
-        // the largest V scale among what the row sees: another page's must not push its weights out of FP16's range
-        float vt = 0.0f;
-        if (PAGED16) {
+        // among what the row sees: another page's scale must not push its weights out of FP16's range
+        if (masked) {
+          vt = 0.0f;
+          if (PAGED16) {
 #pragma unroll
-          for (int g = 0; g < kKeys / 16; ++g)
-            if (!masked || (tok0 + 16 * g < vis_hi && tok0 + 16 * g + 16 > vis_lo)) vt = fmaxf(vt, vs[16 * g]);
-        } else if (!masked) {
-#pragma unroll
-          for (int i = 0; i < kKeys / 32; ++i) vt = fmaxf(vt, vs[32 * i + lane]);
-#pragma unroll
-          for (int d = 1; d < 32; d *= 2) vt = fmaxf(vt, __shfl_xor_sync(0xffffffffu, vt, d));
-        } else {
-          for (int32_t c = max(0, vis_lo - tok0); c < min(kKeys, vis_hi - tok0); ++c) vt = fmaxf(vt, vs[c]);
-          __syncwarp();
+            for (int g = 0; g < kKeys / 16; ++g)
+              if (tok0 + 16 * g < vis_hi && tok0 + 16 * g + 16 > vis_lo) vt = fmaxf(vt, vs[g]);
+          } else {
+            for (int32_t c = max(0, vis_lo - tok0); c < min(kKeys, vis_hi - tok0); ++c) vt = fmaxf(vt, vs[c]);
+            __syncwarp();
+          }
         }
+        tm_wait_ld();
         // columns [lo_c, hi_c) of the tile are seen
         const int32_t hi_c = vis_hi - tok0, lo_c = vis_lo - tok0;
-        float mt = masked ? row_max<PAGED16, true>(s_at, ks, rf, lo_c, hi_c)
-                          : row_max<PAGED16, false>(s_at, ks, rf, lo_c, hi_c);
+        float mt = masked ? row_max<PAGED16, true>(x, ks, rf, lo_c, hi_c)
+                          : row_max<PAGED16, false>(x, ks, rf, lo_c, hi_c);
         const bool grow = mt > m + kLag;
         if (__any_sync(0xffffffffu, grow || vt > vref)) {
           const float vn = fmaxf(vt, vref);
@@ -587,15 +619,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
             __syncwarp();
             tc_fence_after();
             const float fo = f * (vref / vn);
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
-              uint32_t x[32];
-              tm_ld32(o_at + 32 * c, x);
+              uint32_t y[32];
+              tm_ld32(o_at + 32 * c, y);
               tm_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * fo);
-              tm_st32(o_at + 32 * c, x);
+              for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * fo);
+              tm_st32(o_at + 32 * c, y);
             }
+#pragma unroll
+            for (int c = 0; c < kKeys / 32; ++c) tm_ld32(s_at + 32 * c, x[c]);  // (not kept in registers meanwhile)
+            tm_wait_ld();
           }
           vref = vn;
           if (vn > 1.17549435e-38f) lref = kLift - lg2(vn);
@@ -630,11 +665,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
         __syncwarp();
         // 2^(s f - m) in one step, unless m is so large that its own rounding would show
         if (__any_sync(0xffffffffu, fabsf(base) >= 1048576.0f))
-          l += row_weights<PAGED16, true, true>(s_at, ks, vs + kKeys, rf, lref, base, lo_c, hi_c);
+          l += row_weights<PAGED16, true, true>(x, s_at, ks, vs + kKeys, rf, lref, base, lo_c, hi_c);
         else if (masked)
-          l += row_weights<PAGED16, true, false>(s_at, ks, vs + kKeys, rf, lref, base, lo_c, hi_c);
+          l += row_weights<PAGED16, true, false>(x, s_at, ks, vs + kKeys, rf, lref, base, lo_c, hi_c);
         else
-          l += row_weights<PAGED16, false, false>(s_at, ks, vs + kKeys, rf, lref, base, lo_c, hi_c);
+          l += row_weights<PAGED16, false, false>(x, s_at, ks, vs + kKeys, rf, lref, base, lo_c, hi_c);
         tm_wait_st();
         tc_fence_before();
         mbar_arrive(p_full + 8 * t);
@@ -679,12 +714,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
     }
   } else if (warp < kMmaWarp) {
     // ================================================================ codes to FP16 tiles
-    if (warp < kSoftWarps + kKWarps)
-      load_tiles<D, PAGED16, true, kKWarps>(p, q, smem, head, lo, hi, n_steps, k_full, k_empty, stop, nan_seen);
-    else
+    regs_dec();
+    if (warp < kSoftWarps + kVWarps)
       load_tiles<D, PAGED16, false, kVWarps>(p, q, smem, head, lo, hi, n_steps, v_full, v_empty, stop, nan_seen);
-  } else if (n_steps > 0) {
+    else
+      load_tiles<D, PAGED16, true, kKWarps>(p, q, smem, head, lo, hi, n_steps, k_full, k_empty, stop, nan_seen);
+  } else {
     // ================================================================ products
+    regs_dec();
+    if (n_steps > 0) {
     // The whole warp walks, one lane issues: what the instructions take is uniform.
     // (All 512 columns are allocated, so TMEM starts at column 0.)
     const bool one = elect_one();
@@ -740,6 +778,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
       mbar_wait(sb, 0, stop);
       *stop = 1u;
       c8_error(p, q.s, KV_CACHE8_STALLED);
+    }
     }
   }
   __syncwarp();
