@@ -180,16 +180,21 @@ struct PromptShape {
 };
 
 // ---------------------------------------------------------------- a row's scores
-// A thread's row of a 128-key tile: bare products x; K's and V's scales, of whole
-// pages per 16 tokens, else per token; rf the row's factor; z = x k rf.  MASK: only
+// A thread's row of a 128-key tile: bare products in TMEM at s_at (read twice, 32 at
+// a time, the next on their way: holding all 128 left the compiler too few registers
+// to overlap anything); K's and V's scales, of whole pages per 16 tokens, else per
+// token; rf the row's factor; z = x k rf.  MASK: only
 // columns [lo_c, hi_c) are seen, and of these none whose K scale is 0 (a token
 // without a page).
 template <bool PAGED16, bool MASK>
-__device__ __forceinline__ float row_max(const uint32_t (&x)[4][32], const float* ks, float rf, int32_t lo_c,
-                                         int32_t hi_c) {
+__device__ __forceinline__ float row_max(uint32_t s_at, const float* ks, float rf, int32_t lo_c, int32_t hi_c) {
   float mt = kNegInf;
+  uint32_t x[2][32];
+  tm_ld32(s_at, x[0]);
 #pragma unroll
   for (int c = 0; c < kKeys / 32; ++c) {
+    tm_wait_ld();
+    if (c + 1 < kKeys / 32) tm_ld32(s_at + 32 * (c + 1), x[(c + 1) & 1]);
     if (PAGED16) {
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
@@ -199,7 +204,7 @@ __device__ __forceinline__ float row_max(const uint32_t (&x)[4][32], const float
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int col = 32 * c + 16 * g + i;
-          y[i] = __uint_as_float(x[c][16 * g + i]);
+          y[i] = __uint_as_float(x[c & 1][16 * g + i]);
           if (MASK && !(col < hg && col >= lo_c)) y[i] = kNegInf;
         }
 #pragma unroll
@@ -215,7 +220,7 @@ __device__ __forceinline__ float row_max(const uint32_t (&x)[4][32], const float
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int col = 32 * c + i + e;
-          float z = __fmul_rn(__uint_as_float(x[c][i + e]), __fmul_rn(kk[e], rf));
+          float z = __fmul_rn(__uint_as_float(x[c & 1][i + e]), __fmul_rn(kk[e], rf));
           if (MASK && !(col < hi_c && col >= lo_c && kk[e] != 0.0f)) z = kNegInf;
           mt = fmaxf(mt, z);
         }
@@ -230,12 +235,16 @@ __device__ __forceinline__ float row_max(const uint32_t (&x)[4][32], const float
 // its inverse, once for the tokens that share it.
 // EXACT: z rounded as row_max rounded it before base is taken off.
 template <bool PAGED16, bool MASK, bool EXACT>
-__device__ __forceinline__ float row_weights(const uint32_t (&x)[4][32], uint32_t s_at, const float* ks, const float* lv,
-                                             float rf, float lref, float base, int32_t lo_c, int32_t hi_c) {
+__device__ __forceinline__ float row_weights(uint32_t s_at, const float* ks, const float* lv, float rf, float lref,
+                                             float base, int32_t lo_c, int32_t hi_c) {
   constexpr int G = PAGED16 ? 16 : 4;  // columns handled together; of whole pages they share their scales
   float total = 0.0f;
+  uint32_t x[2][32];
+  tm_ld32(s_at, x[0]);
 #pragma unroll
   for (int c = 0; c < kKeys / 32; ++c) {
+    tm_wait_ld();
+    if (c + 1 < kKeys / 32) tm_ld32(s_at + 32 * (c + 1), x[(c + 1) & 1]);
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 32; i += G) {
@@ -255,7 +264,7 @@ __device__ __forceinline__ float row_weights(const uint32_t (&x)[4][32], uint32_
 #pragma unroll
       for (int e = 0; e < G; e += 2) {
         const float k0 = kk[e & 3], k1 = kk[(e + 1) & 3];
-        const float2 xx = make_float2(__uint_as_float(x[c][i + e]), __uint_as_float(x[c][i + e + 1]));
+        const float2 xx = make_float2(__uint_as_float(x[c & 1][i + e]), __uint_as_float(x[c & 1][i + e + 1]));
         const float2 f = make_float2(__fmul_rn(k0, rf), __fmul_rn(k1, rf));
         float2 z;
         if (EXACT)
@@ -571,9 +580,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
         if (!fine) break;
         __syncwarp();
         tc_fence_after();
-        uint32_t x[4][32];
-#pragma unroll
-        for (int c = 0; c < kKeys / 32; ++c) tm_ld32(s_at + 32 * c, x[c]);
         // holes of K (a token without a page has the scale 0), the largest scale of V
         float vt = ks[3 * kKeys];
         bool hole = ks[3 * kKeys + 1] != 0.0f;
@@ -601,11 +607,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
             __syncwarp();
           }
         }
-        tm_wait_ld();
         // columns [lo_c, hi_c) of the tile are seen
         const int32_t hi_c = vis_hi - tok0, lo_c = vis_lo - tok0;
-        float mt = masked ? row_max<PAGED16, true>(x, ks, rf, lo_c, hi_c)
-                          : row_max<PAGED16, false>(x, ks, rf, lo_c, hi_c);
+        float mt = masked ? row_max<PAGED16, true>(s_at, ks, rf, lo_c, hi_c)
+                          : row_max<PAGED16, false>(s_at, ks, rf, lo_c, hi_c);
         const bool grow = mt > m + kLag;
         if (__any_sync(0xffffffffu, grow || vt > vref)) {
           const float vn = fmaxf(vt, vref);
@@ -628,9 +633,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
               for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * fo);
               tm_st32(o_at + 32 * c, y);
             }
-#pragma unroll
-            for (int c = 0; c < kKeys / 32; ++c) tm_ld32(s_at + 32 * c, x[c]);  // (not kept in registers meanwhile)
-            tm_wait_ld();
           }
           vref = vn;
           if (vn > 1.17549435e-38f) lref = kLift - lg2(vn);
@@ -665,11 +667,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
         __syncwarp();
         // 2^(s f - m) in one step, unless m is so large that its own rounding would show
         if (__any_sync(0xffffffffu, fabsf(base) >= 1048576.0f))
-          l += row_weights<PAGED16, true, true>(x, s_at, ks, vs + kKeys, rf, lref, base, lo_c, hi_c);
+          l += row_weights<PAGED16, true, true>(s_at, ks, vs + kKeys, rf, lref, base, lo_c, hi_c);
         else if (masked)
-          l += row_weights<PAGED16, true, false>(x, s_at, ks, vs + kKeys, rf, lref, base, lo_c, hi_c);
+          l += row_weights<PAGED16, true, false>(s_at, ks, vs + kKeys, rf, lref, base, lo_c, hi_c);
         else
-          l += row_weights<PAGED16, false, false>(x, s_at, ks, vs + kKeys, rf, lref, base, lo_c, hi_c);
+          l += row_weights<PAGED16, false, false>(s_at, ks, vs + kKeys, rf, lref, base, lo_c, hi_c);
         tm_wait_st();
         tc_fence_before();
         mbar_arrive(p_full + 8 * t);
