@@ -187,7 +187,8 @@ struct PromptShape {
 // columns [lo_c, hi_c) are seen, and of these none whose K scale is 0 (a token
 // without a page).
 template <bool PAGED16, bool MASK>
-__device__ __forceinline__ float row_max(uint32_t s_at, const float* ks, float rf, int32_t lo_c, int32_t hi_c) {
+__device__ __forceinline__ float row_max(uint32_t s_at, const float* ks, const float (&f8)[8], float rf, int32_t lo_c,
+                                         int32_t hi_c) {
   float mt = kNegInf;
   uint32_t x[2][32];
   tm_ld32(s_at, x[0]);
@@ -198,8 +199,8 @@ __device__ __forceinline__ float row_max(uint32_t s_at, const float* ks, float r
     if (PAGED16) {
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const float k = ks[2 * c + g];
-        const int32_t hg = MASK && k == 0.0f ? -1 : hi_c;
+        const float f = f8[2 * c + g];
+        const int32_t hg = MASK && f == 0.0f ? -1 : hi_c;
         float y[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -210,7 +211,7 @@ __device__ __forceinline__ float row_max(uint32_t s_at, const float* ks, float r
 #pragma unroll
         for (int i = 0; i < 5; ++i) y[i] = max3(y[3 * i], y[3 * i + 1], y[3 * i + 2]);
         y[0] = fmaxf(max3(y[0], y[1], y[2]), max3(y[3], y[4], y[15]));
-        mt = fmaxf(mt, __fmul_rn(y[0], __fmul_rn(k, rf)));  // (a hole: -inf * 0, which the maximum leaves out)
+        mt = fmaxf(mt, __fmul_rn(y[0], f));  // (a hole: -inf * 0, which the maximum leaves out)
       }
     } else {
 #pragma unroll
@@ -235,8 +236,9 @@ __device__ __forceinline__ float row_max(uint32_t s_at, const float* ks, float r
 // its inverse, once for the tokens that share it.
 // EXACT: z rounded as row_max rounded it before base is taken off.
 template <bool PAGED16, bool MASK, bool EXACT>
-__device__ __forceinline__ float row_weights(uint32_t s_at, const float* ks, const float* lv, float rf, float lref,
-                                             float base, int32_t lo_c, int32_t hi_c) {
+__device__ __forceinline__ float row_weights(uint32_t s_at, const float* ks, const float* lv, const float (&f8)[8],
+                                             const float (&l8)[8], float rf, float lref, float base, int32_t lo_c,
+                                             int32_t hi_c) {
   constexpr int G = PAGED16 ? 16 : 4;  // columns handled together; of whole pages they share their scales
   float total = 0.0f;
   uint32_t x[2][32];
@@ -251,8 +253,8 @@ __device__ __forceinline__ float row_weights(uint32_t s_at, const float* ks, con
       const int col = 32 * c + i;
       float kk[4], ll[4];
       if (PAGED16) {
-        kk[0] = kk[1] = kk[2] = kk[3] = ks[col / 16];
-        ll[0] = ll[1] = ll[2] = ll[3] = lv[col / 16] + lref;
+        kk[0] = kk[1] = kk[2] = kk[3] = f8[col / 16];
+        ll[0] = ll[1] = ll[2] = ll[3] = l8[col / 16] + lref;
         // a page that the row sees nothing of: its scale must not matter
         if (MASK && (col >= hi_c || col + 16 <= lo_c)) ll[0] = ll[1] = ll[2] = ll[3] = 0.0f;
       } else {
@@ -265,7 +267,7 @@ __device__ __forceinline__ float row_weights(uint32_t s_at, const float* ks, con
       for (int e = 0; e < G; e += 2) {
         const float k0 = kk[e & 3], k1 = kk[(e + 1) & 3];
         const float2 xx = make_float2(__uint_as_float(x[c & 1][i + e]), __uint_as_float(x[c & 1][i + e + 1]));
-        const float2 f = make_float2(__fmul_rn(k0, rf), __fmul_rn(k1, rf));
+        const float2 f = PAGED16 ? make_float2(k0, k1) : make_float2(__fmul_rn(k0, rf), __fmul_rn(k1, rf));
         float2 z;
         if (EXACT)
           z = make_float2(__fadd_rn(__fadd_rn(__fmul_rn(xx.x, f.x), -base), ll[e & 3]),
@@ -301,7 +303,7 @@ __device__ __forceinline__ float row_weights(uint32_t s_at, const float* ks, con
 template <int D, bool PAGED16, bool IS_K, int W>
 __device__ __forceinline__ void load_tiles(const C8Params& p, const C8Seq& q, uint8_t* smem, uint32_t head, int32_t lo,
                                            int32_t hi, int32_t n_steps, uint32_t full, uint32_t empty,
-                                           volatile uint32_t* stop, uint32_t* nan_seen) {
+                                           uint32_t scales, volatile uint32_t* stop, uint32_t* nan_seen) {
   using S = PromptShape<D>;
   constexpr int CPR = D >= 64 ? 4 : 2;
   constexpr int RPI = W * 32 / CPR;                        // token rows at once
@@ -334,13 +336,24 @@ __device__ __forceinline__ void load_tiles(const C8Params& p, const C8Seq& q, ui
   float ksc[(kKeys + W * 32 - 1) / (W * 32)], vsc[(kKeys + W * 32 - 1) / (W * 32)];
   int32_t id = -1;
   int64_t run = -1;
-  auto ask = [&](int32_t j) {  // runs of tile j
-    run = -1;
-    id = -1;
-    if (PAGED16 && j < n_steps) run = place(lo + j * kKeys + 16 * (int32_t)(lane & 7u), id);
+  int32_t entry = -2;  // raw table entry of this lane's run of the tile asked for, -2: past the last token
+  auto ask = [&](int32_t j) {
+    const int32_t tok = lo + j * kKeys + 16 * (int32_t)(lane & 7u);
+    entry = -2;
+    if (PAGED16 && tok < hi) {
+      const uint32_t i = c8_div_t(p, (uint32_t)tok);
+      entry = i < p.table_width ? ldg_i32(p.tables + (int64_t)q.s * p.table_stride + i) : -1;
+    }
   };
   auto fetch = [&](int32_t j) {
     const int32_t tok0 = lo + j * kKeys;
+    if (PAGED16) {
+      const int32_t tok = tok0 + 16 * (int32_t)(lane & 7u);
+      const bool ok = (uint32_t)entry < p.num_blocks;
+      bad |= !ok && entry != -2;
+      id = ok ? entry : -1;
+      run = ok ? (int64_t)entry * p.sb + (int64_t)((uint32_t)tok - c8_div_t(p, (uint32_t)tok) * p.T) * p.st : -1;
+    }
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
       const uint32_t r = i * RPI + row;  // token row of the tile
@@ -402,19 +415,6 @@ __device__ __forceinline__ void load_tiles(const C8Params& p, const C8Seq& q, ui
       }
       if (lane == 0) reinterpret_cast<uint8_t*>(nan_seen)[4 * st + (lt >> 5)] = (uint8_t)any;
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      uint4 h0, h1;
-      c8_dec4(x[i].x, h0.x, h0.y);
-      c8_dec4(x[i].y, h0.z, h0.w);
-      c8_dec4(x[i].z, h1.x, h1.y);
-      c8_dec4(x[i].w, h1.z, h1.w);
-      uint8_t* at = tile + (i % S::DG) * (kKeys * 128) + (i / S::DG) * (RPI * 128);
-      if (kKeys % RPI == 0 || (i / S::DG) * RPI + row < kKeys) {
-        *reinterpret_cast<uint4*>(at + dst0) = h0;
-        *reinterpret_cast<uint4*>(at + dst1) = h1;
-      }
-    }
     float* sc = reinterpret_cast<float*>(smem + S::kScale + st * S::kScaleStage);
     if (!IS_K && PAGED16 && lt < 32u) {
       float top = vsc[0];
@@ -438,6 +438,20 @@ __device__ __forceinline__ void load_tiles(const C8Params& p, const C8Seq& q, ui
         sc[kKeys + i * W * 32 + lt] = vsc[i];
         sc[2 * kKeys + i * W * 32 + lt] = vsc[i] > 0.0f ? lg2(vsc[i]) : vsc[i];
       }
+    if (!IS_K) mbar_arrive(scales + 8 * st);  // the softmax needs these and the NaN flags, before V itself is wanted
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      uint4 h0, h1;
+      c8_dec4(x[i].x, h0.x, h0.y);
+      c8_dec4(x[i].y, h0.z, h0.w);
+      c8_dec4(x[i].z, h1.x, h1.y);
+      c8_dec4(x[i].w, h1.z, h1.w);
+      uint8_t* at = tile + (i % S::DG) * (kKeys * 128) + (i / S::DG) * (RPI * 128);
+      if (kKeys % RPI == 0 || (i / S::DG) * RPI + row < kKeys) {
+        *reinterpret_cast<uint4*>(at + dst0) = h0;
+        *reinterpret_cast<uint4*>(at + dst1) = h1;
+      }
+    }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     mbar_arrive(full + 8 * st);
     __syncwarp();
@@ -473,7 +487,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
   const uint32_t bar = sbase + S::kBar;
   const uint32_t k_full = bar, k_empty = bar + 16, v_full = bar + 32, v_empty = bar + 48;  // [2]
   const uint32_t s_full = bar + 64, p_full = bar + 80, pv_done = bar + 96;                  // [2]
-  const uint32_t q_full = bar + 144;
+  const uint32_t q_full = bar + 144, c_full = bar + 152;                                   // c_full: [2]
   volatile uint32_t* stop = reinterpret_cast<volatile uint32_t*>(smem + S::kBar + 112);
   uint32_t* nan_seen = reinterpret_cast<uint32_t*>(smem + S::kBar + 116);   // [stage]: a byte a loading warp, V has NaN codes
   uint32_t* any_row_nan = reinterpret_cast<uint32_t*>(smem + S::kBar + 124);
@@ -484,6 +498,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
       mbar_init(k_empty + 8 * i, 1);
       mbar_init(v_full + 8 * i, kVWarps * 32);
       mbar_init(v_empty + 8 * i, 1);
+      mbar_init(c_full + 8 * i, kVWarps * 32);
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_full + 8 * i, 128);
       mbar_init(pv_done + 8 * i, 1);
@@ -506,47 +521,56 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
   tc_fence_after();
   const uint32_t tm = *tm_at;
 
-  // ---- Q to shared memory, a softmax thread to a row; bf16 rows are scaled by a
-  // power of two into FP16's range (exact but for values 2^-39 of the row's largest)
+  // ---- Q to shared memory, each softmax warp its own 32 rows; bf16 rows are scaled by
+  // a power of two into FP16's range (exact but for values 2^-39 of the row's largest)
   const uint32_t r = tid;  // row of the CTA, for threads of the softmax
   const bool in = tid < 256u && r < n_rows;
   const uint32_t rr = r0 + (in ? r : 0u), tok_r = rr / p.G, hd = head * p.G + rr - tok_r * p.G;
-  float rf = 0.0f;
+  float rf = p.scale_log2;
   if (tid < 256u) {
-    const uint16_t* src = p.a + ((int64_t)q.row + tok_r) * p.a_row + (int64_t)hd * p.a_head;
-    int ex = 0;
-    if (DT == 1) {
-      uint32_t m = 0;
+    constexpr uint32_t LPR = D / 8, RPI = 32 / LPR;  // lanes of a row, rows at once
+    const int64_t off = in ? ((int64_t)q.row + tok_r) * p.a_row + (int64_t)hd * p.a_head : -1;
+    const uint32_t c = lane % LPR;
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 x = in ? ld_nc16(src + 8 * c) : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    for (uint32_t h = 0; h < LPR; h += LPR / 2) {  // half of the rows' loads in flight at a time
+      uint4 x[LPR / 2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          m = max(m, (w[k] & 0x7fffu) < 0x7f80u ? (w[k] & 0x7fffu) : 0u);
-          m = max(m, ((w[k] >> 16) & 0x7fffu) < 0x7f80u ? ((w[k] >> 16) & 0x7fffu) : 0u);
+      for (uint32_t i = 0; i < LPR / 2; ++i) {
+        const int64_t o = __shfl_sync(0xffffffffu, off, (h + i) * RPI + lane / LPR);
+        x[i] = o >= 0 ? ld_nc16(p.a + o + 8 * c) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (uint32_t i = 0; i < LPR / 2; ++i) {
+        const uint32_t row = (h + i) * RPI + lane / LPR;
+        if (DT == 1) {
+          uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, m = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            m = max(m, (w[k] & 0x7fffu) < 0x7f80u ? (w[k] & 0x7fffu) : 0u);
+            m = max(m, ((w[k] >> 16) & 0x7fffu) < 0x7f80u ? ((w[k] >> 16) & 0x7fffu) : 0u);
+          }
+#pragma unroll
+          for (uint32_t d = LPR / 2; d; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+          // the largest magnitude, in [2^k, 2^(k+1)), goes to [2^14, 2^15)
+          const int ex = m ? min(max(14 - ((int)(m >> 7) - 127), -120), 120) : 0;
+          const float f = __uint_as_float((uint32_t)(127 + ex) << 23);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[k] = pack2<0>(lo_f32<1>(w[k]) * f, hi_f32<1>(w[k]) * f);
+          x[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          // the row's thread undoes the scaling in its factor
+          const int e_row = __shfl_sync(0xffffffffu, ex, (lane % RPI) * LPR);
+          if (lane / RPI == h + i) rf = p.scale_log2 * __uint_as_float((uint32_t)(127 - e_row) << 23);
         }
+        *reinterpret_cast<uint4*>(smem + S::kQ + (warp >> 2) * S::kQTile + (c >> 3) * (128 * 128) +
+                                  ((warp & 3u) * 32u + row) * 128 + (((c & 7u) ^ (row & 7u)) << 4)) = x[i];
       }
-      ex = m ? min(max(14 - ((int)(m >> 7) - 127), -120), 120) : 0;
-    }
-    const float f = __uint_as_float((uint32_t)(127 + ex) << 23);
-    rf = p.scale_log2 * __uint_as_float((uint32_t)(127 - ex) << 23);
-    uint8_t* dst = smem + S::kQ + (r >> 7) * S::kQTile + (r & 127u) * 128;
-#pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
-      uint4 x = in ? ld_nc16(src + 8 * c) : make_uint4(0, 0, 0, 0);
-      if (DT == 1) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = pack2<0>(lo_f32<1>(w[k]) * f, hi_f32<1>(w[k]) * f);
-      }
-      *reinterpret_cast<uint4*>(dst + (c >> 3) * (128 * 128) + (((c & 7) ^ (r & 7u)) << 4)) = x;
     }
     uint32_t* rn = reinterpret_cast<uint32_t*>(smem + S::kRowNan) + r * (D / 32);
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) rn[k] = 0;
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     mbar_arrive(q_full);
+    __syncwarp();
   }
 
   // Registers: 512 threads start with 128 each; the softmax takes 176 (a row's 128
@@ -575,7 +599,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
         const uint32_t st = j & 1;
         const float* ks = reinterpret_cast<const float*>(smem + S::kScale + st * S::kScaleStage);
         const float* vs = ks + kKeys;
-        fine = mbar_wait(v_full + 8 * st, (j >> 1) & 1, stop) && mbar_wait(s_full + 8 * t, j & 1, stop);
+        fine = mbar_wait(c_full + 8 * st, (j >> 1) & 1, stop) && mbar_wait(s_full + 8 * t, j & 1, stop);
         fine = __all_sync(0xffffffffu, fine);
         if (!fine) break;
         __syncwarp();
@@ -609,8 +633,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
         }
         // columns [lo_c, hi_c) of the tile are seen
         const int32_t hi_c = vis_hi - tok0, lo_c = vis_lo - tok0;
-        float mt = masked ? row_max<PAGED16, true>(s_at, ks, rf, lo_c, hi_c)
-                          : row_max<PAGED16, false>(s_at, ks, rf, lo_c, hi_c);
+        // (whole pages) K's scale times the row's factor, V's scale as a logarithm
+        float f8[8], l8[8];
+        if (PAGED16) {
+#pragma unroll
+          for (int g = 0; g < 8; g += 4) {
+            const float4 k = *reinterpret_cast<const float4*>(ks + g), v = *reinterpret_cast<const float4*>(vs + kKeys + g);
+            f8[g] = __fmul_rn(k.x, rf); f8[g + 1] = __fmul_rn(k.y, rf);
+            f8[g + 2] = __fmul_rn(k.z, rf); f8[g + 3] = __fmul_rn(k.w, rf);
+            l8[g] = v.x; l8[g + 1] = v.y; l8[g + 2] = v.z; l8[g + 3] = v.w;
+          }
+        }
+        float mt = masked ? row_max<PAGED16, true>(s_at, ks, f8, rf, lo_c, hi_c)
+                          : row_max<PAGED16, false>(s_at, ks, f8, rf, lo_c, hi_c);
         const bool grow = mt > m + kLag;
         if (__any_sync(0xffffffffu, grow || vt > vref)) {
           const float vn = fmaxf(vt, vref);
@@ -667,11 +702,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
         __syncwarp();
         // 2^(s f - m) in one step, unless m is so large that its own rounding would show
         if (__any_sync(0xffffffffu, fabsf(base) >= 1048576.0f))
-          l += row_weights<PAGED16, true, true>(s_at, ks, vs + kKeys, rf, lref, base, lo_c, hi_c);
+          l += row_weights<PAGED16, true, true>(s_at, ks, vs + kKeys, f8, l8, rf, lref, base, lo_c, hi_c);
         else if (masked)
-          l += row_weights<PAGED16, true, false>(s_at, ks, vs + kKeys, rf, lref, base, lo_c, hi_c);
+          l += row_weights<PAGED16, true, false>(s_at, ks, vs + kKeys, f8, l8, rf, lref, base, lo_c, hi_c);
         else
-          l += row_weights<PAGED16, false, false>(s_at, ks, vs + kKeys, rf, lref, base, lo_c, hi_c);
+          l += row_weights<PAGED16, false, false>(s_at, ks, vs + kKeys, f8, l8, rf, lref, base, lo_c, hi_c);
         tm_wait_st();
         tc_fence_before();
         mbar_arrive(p_full + 8 * t);
@@ -686,6 +721,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
         uint16_t* out = p.b + ((int64_t)q.row + tok_r) * p.b_row + (int64_t)hd * p.b_head;
         const uint32_t* rn = reinterpret_cast<const uint32_t*>(smem + S::kRowNan) + r * (D / 32);
         const bool fix = *any_row_nan != 0u;
+        const bool out32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t x[32];
@@ -700,12 +736,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
               for (int i = 0; i < 32; ++i)
                 if ((rn[c] >> i) & 1u) x[i] = 0x7fffffffu;
             }
+            uint4 y4[4];
 #pragma unroll
             for (int i = 0; i < 32; i += 8) {
               float y[8];
 #pragma unroll
               for (int k = 0; k < 8; ++k) y[k] = inv == 0.0f ? 0.0f : __uint_as_float(x[i + k]) * inv;
-              st16(out + 32 * c + i, pack8<DT>(y));
+              y4[i / 8] = pack8<DT>(y);
+            }
+            if (out32) {
+              st32(out + 32 * c, y4[0], y4[1]);
+              st32(out + 32 * c + 16, y4[2], y4[3]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) st16(out + 32 * c + 8 * i, y4[i]);
             }
           }
         }
@@ -718,9 +762,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
     // ================================================================ codes to FP16 tiles
     regs_dec();
     if (warp < kSoftWarps + kVWarps)
-      load_tiles<D, PAGED16, false, kVWarps>(p, q, smem, head, lo, hi, n_steps, v_full, v_empty, stop, nan_seen);
+      load_tiles<D, PAGED16, false, kVWarps>(p, q, smem, head, lo, hi, n_steps, v_full, v_empty, c_full, stop, nan_seen);
     else
-      load_tiles<D, PAGED16, true, kKWarps>(p, q, smem, head, lo, hi, n_steps, k_full, k_empty, stop, nan_seen);
+      load_tiles<D, PAGED16, true, kKWarps>(p, q, smem, head, lo, hi, n_steps, k_full, k_empty, 0u, stop, nan_seen);
   } else {
     // ================================================================ products
     regs_dec();
