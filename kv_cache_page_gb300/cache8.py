@@ -70,6 +70,14 @@ def lib():
     return _LIB
 
 
+def _stream(stream):
+    """The raw stream: torch's current one by its handle (a Stream object per call costs 3 us)."""
+    if stream is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
 def _int32(t, name, n=None):
     if t.dtype != torch.int32 or not t.is_cuda:
         raise ValueError(f"{name} must be an int32 CUDA tensor")
@@ -90,6 +98,8 @@ class Layer:
             if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous float32 CUDA tensor")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.code_bytes = min(t.untyped_storage().nbytes() - t.storage_offset() for t in (k, v))
+        self.scales = min(k_scale.numel(), v_scale.numel())
         self._c = _Layer(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
         self._ref = C.addressof(self._c)
 
@@ -141,6 +151,8 @@ class Cache8:
         self._codes = (strides[0] * (num_blocks - 1) + strides[1] * (block_tokens - 1) +
                        strides[2] * (num_kv_heads - 1) + head_dim)
         self._scales = num_blocks * num_kv_heads
+        L = lib()
+        self._write, self._read, self._attend = L.kv_cache8_write, L.kv_cache8_read, L.kv_cache8_attend
         h = C.c_void_p()
         self._h = None
         _codec._check(lib().kv_cache8_create(C.byref(g), C.byref(h)), "kv_cache8_create")
@@ -164,32 +176,33 @@ class Cache8:
         return Layer(*codes, *scales)
 
     def _layer(self, layer):
-        if layer.k.untyped_storage().nbytes() - layer.k.storage_offset() < self._codes or \
-                layer.v.untyped_storage().nbytes() - layer.v.storage_offset() < self._codes or \
-                layer.k_scale.numel() < self._scales or layer.v_scale.numel() < self._scales:
+        if layer.code_bytes < self._codes or layer.scales < self._scales:
             raise ValueError("the layer's tensors are smaller than the registered geometry")
         return layer._ref
 
     def _rows(self, t, batch, heads, name):
-        if t.dtype != self.dtype or not t.is_cuda:
+        if t.dtype is not self.dtype or not t.is_cuda:
             raise ValueError(f"{name} must be a {self.dtype} CUDA tensor")
-        if tuple(t.shape) != (batch.n_new, heads, self.head_dim) or t.stride(2) != 1:
+        row, head, one = t.stride() if t.dim() == 3 else (0, 0, 0)
+        if one != 1 or t.shape != (batch.n_new, heads, self.head_dim):
             raise ValueError(f"{name} must be [{batch.n_new}, {heads}, {self.head_dim}] with values side by side")
-        return _Rows(t.data_ptr(), t.stride(0), t.stride(1))
+        return _Rows(t.data_ptr(), row, head)
 
     def write(self, layer: Layer, batch: Batch, k, v, stream=None):
         """Quantise the batch's new tokens (k, v: [n_new, num_kv_heads, head_dim]) into
         their pages; a page's scale grows where the new values need it, and its earlier
         codes are rewritten under the grown scale."""
         kr, vr = self._rows(k, batch, self.num_kv_heads, "k"), self._rows(v, batch, self.num_kv_heads, "v")
-        _codec._check(lib().kv_cache8_write(self._h, self._layer(layer), batch._ref, C.addressof(kr), C.addressof(vr),
-                                            _codec._stream_handle(stream)), "kv_cache8_write")
+        rc = self._write(self._h, self._layer(layer), batch._ref, C.addressof(kr), C.addressof(vr), _stream(stream))
+        if rc:
+            _codec._check(rc, "kv_cache8_write")
 
     def read(self, layer: Layer, batch: Batch, k, v, stream=None):
         """The batch's new tokens back in 16 bits, into k and v."""
         kr, vr = self._rows(k, batch, self.num_kv_heads, "k"), self._rows(v, batch, self.num_kv_heads, "v")
-        _codec._check(lib().kv_cache8_read(self._h, self._layer(layer), batch._ref, C.addressof(kr), C.addressof(vr),
-                                           _codec._stream_handle(stream)), "kv_cache8_read")
+        rc = self._read(self._h, self._layer(layer), batch._ref, C.addressof(kr), C.addressof(vr), _stream(stream))
+        if rc:
+            _codec._check(rc, "kv_cache8_read")
 
     def attend_workspace(self, batch: Batch) -> int:
         """Bytes of the workspace that ``attend`` wants for this batch's sizes."""
@@ -205,10 +218,15 @@ class Cache8:
         ``attend_workspace(batch)`` bytes, zero-filled before its first use, not
         shared by calls that may run at the same time."""
         qr, outr = self._rows(q, batch, self.num_q_heads, "q"), self._rows(out, batch, self.num_q_heads, "out")
-        if lse is not None and (lse.dtype != torch.float32 or not lse.is_cuda or not lse.is_contiguous() or
-                                tuple(lse.shape) != (batch.n_new, self.num_q_heads)):
-            raise ValueError(f"lse must be a contiguous float32 CUDA tensor [{batch.n_new}, {self.num_q_heads}]")
-        if scale is not None and not (scale > 0 and math.isfinite(scale)):
+        at = None
+        if lse is not None:
+            if lse.dtype is not torch.float32 or not lse.is_cuda or lse.shape != (batch.n_new, self.num_q_heads) or \
+                    not lse.is_contiguous():
+                raise ValueError(f"lse must be a contiguous float32 CUDA tensor [{batch.n_new}, {self.num_q_heads}]")
+            at = lse.data_ptr()
+        if scale is None:
+            scale = 0.0
+        elif not (scale > 0 and math.isfinite(scale)):
             raise ValueError("scale must be finite and positive")
         if window < 0:
             raise ValueError("window must not be negative")
@@ -216,8 +234,8 @@ class Cache8:
         if workspace is not None:
             if not workspace.is_cuda or not workspace.is_contiguous():
                 raise ValueError("workspace must be a contiguous CUDA tensor")
-            ws, nb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        _codec._check(lib().kv_cache8_attend(self._h, self._layer(layer), batch._ref, C.addressof(qr), C.addressof(outr),
-                                             None if lse is None else lse.data_ptr(), scale or 0.0, window,
-                                             CAUSAL if causal else 0, ws, nb, _codec._stream_handle(stream)),
-                      "kv_cache8_attend")
+            ws, nb = workspace.data_ptr(), workspace.nbytes
+        rc = self._attend(self._h, self._layer(layer), batch._ref, C.addressof(qr), C.addressof(outr), at, scale, window,
+                          CAUSAL if causal else 0, ws, nb, _stream(stream))
+        if rc:
+            _codec._check(rc, "kv_cache8_attend")

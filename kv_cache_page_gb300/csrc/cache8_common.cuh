@@ -1,6 +1,8 @@
 // cache8_common.cuh -- what the kernels of the live 8-bit KV cache share: the
 // map from launch units to sequences, page lookups, number formats.
 #pragma once
+#include <atomic>
+
 #include "cache8_internal.h"
 #include "device_common.cuh"
 
@@ -133,6 +135,19 @@ __device__ __forceinline__ void c8_dec4(uint32_t w, uint32_t& h01, uint32_t& h23
 }
 __device__ __forceinline__ float2 c8_h2f(uint32_t h) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// Let `kernel` have `bytes` of dynamic shared memory on the current device; the
+// runtime is asked once per device (done: the kernel's own bits).
+template <typename F>
+inline bool allow_smem(F kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  if (dev < 64) done.fetch_or(bit, std::memory_order_release);
+  return true;
 }
 
 // FN<dtype, head_dim>(args) for the registered geometry.

@@ -842,8 +842,8 @@ template <int DT, int D, bool PAGED16>
 int prompt_launch(const C8Params& p, void* stream) {
   constexpr int bytes = PromptShape<D>::kBytes;
   const auto kernel = c8_prompt_kernel<DT, D, PAGED16>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-    return KV_ERR_CUDA;
+  static std::atomic<uint64_t> done{0};
+  if (!allow_smem(kernel, bytes, done)) return KV_ERR_CUDA;
   const uint64_t gx = (uint64_t)p.n_units * p.H;
   if (gx > 0x7fffffffull) return KV_ERR_INVALID_ARG;
   return dbg_launch(

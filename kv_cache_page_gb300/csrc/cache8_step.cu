@@ -734,8 +734,8 @@ template <int DT, int D, bool PAGED16, int W>
 int step_launch(const C8Params& p, void* stream) {
   constexpr int bytes = step_smem<D, W>();
   const auto kernel = c8_step_kernel<DT, D, PAGED16, W>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-    return KV_ERR_CUDA;
+  static std::atomic<uint64_t> done{0};
+  if (!allow_smem(kernel, bytes, done)) return KV_ERR_CUDA;
   const uint64_t gx = (uint64_t)p.n_units * p.splits * p.H;
   if (gx > 0x7fffffffull) return KV_ERR_INVALID_ARG;
   return dbg_launch(
