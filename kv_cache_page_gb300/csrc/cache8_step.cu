@@ -23,6 +23,8 @@
 //
 // What the walk costs besides bytes is instructions: 64 conversions and 32
 // products per 16 tokens and D = 128 are the floor.
+#include <type_traits>
+
 #include "cache8_common.cuh"
 
 namespace kvc {
@@ -706,28 +708,47 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
     if (part == 0) finish_row(row, mx, ls);
   }
   cta_sync();
-  // four dims a thread, all ranges in order, 16 loads in flight
-  for (uint32_t c4 = tid; c4 < n_rows * (D / 4); c4 += W * 32) {
-    const uint32_t r = c4 / (D / 4), d4 = c4 % (D / 4);
-    const float* src = base + r * D + d4 * 4;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (uint32_t k0 = 0; k0 < n_split; k0 += 16) {
-      float4 y[16];
+  // four dims a thread, all ranges in order, 16 loads in flight: of one place, or of 2 or 4 where there are few ranges
+  auto join = [&](auto per_place) {
+    constexpr uint32_t P = decltype(per_place)::value, C = 16 / P;
+    for (uint32_t c0 = tid; c0 < n_rows * (D / 4); c0 += W * 32 * C) {
+      float4 x[C];
 #pragma unroll
-      for (int k = 0; k < 16; ++k)
-        if (k0 + k < n_split) y[k] = ld_join4(src + (uint64_t)(k0 + k) * (kStepRows * (D + 2)));
+      for (uint32_t i = 0; i < C; ++i) x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (uint32_t k0 = 0; k0 < n_split; k0 += P) {
+        float4 y[C][P];
 #pragma unroll
-      for (int k = 0; k < 16; ++k)
-        if (k0 + k < n_split) {
-          const float f = s_ml[(k0 + k) * kStepRows + r].x;
-          x.x += y[k].x * f;
-          x.y += y[k].y * f;
-          x.z += y[k].z * f;
-          x.w += y[k].w * f;
+        for (uint32_t i = 0; i < C; ++i) {
+          const uint32_t c4 = c0 + i * W * 32;
+#pragma unroll
+          for (uint32_t k = 0; k < P; ++k)
+            if (k0 + k < n_split && c4 < n_rows * (D / 4))
+              y[i][k] = ld_join4(base + (uint64_t)(k0 + k) * (kStepRows * (D + 2)) + c4 * 4);
         }
+#pragma unroll
+        for (uint32_t i = 0; i < C; ++i) {
+          const uint32_t c4 = c0 + i * W * 32;
+#pragma unroll
+          for (uint32_t k = 0; k < P; ++k)
+            if (k0 + k < n_split && c4 < n_rows * (D / 4)) {
+              const float f = s_ml[(k0 + k) * kStepRows + c4 / (D / 4)].x;
+              x[i].x += y[i][k].x * f;
+              x[i].y += y[i][k].y * f;
+              x[i].z += y[i][k].z * f;
+              x[i].w += y[i][k].w * f;
+            }
+        }
+      }
+#pragma unroll
+      for (uint32_t i = 0; i < C; ++i) {
+        const uint32_t c4 = c0 + i * W * 32;
+        if (c4 < n_rows * (D / 4)) finish_out(c4 / (D / 4), c4 % (D / 4), x[i]);
+      }
     }
-    finish_out(r, d4, x);
-  }
+  };
+  if (n_split <= 4u) join(std::integral_constant<uint32_t, 4>{});
+  else if (n_split <= 8u) join(std::integral_constant<uint32_t, 8>{});
+  else join(std::integral_constant<uint32_t, 16>{});
 }
 
 template <int DT, int D, bool PAGED16, int W>
