@@ -307,6 +307,7 @@ int kv_cache8_attend(kv_cache8_t h, const kv_cache8_layer* layer, const kv_cache
   p.splits = sp.splits;
   p.chunk = sp.chunk;
   p.step_warps = sp.warps;
+  p.rows8 = !p.cu && p.G <= 8 ? 1u : 0u;  // (a hint of few new tokens is not enough: counts are read on the device)
   p.min_rows = 1;
   p.max_rows = prompts ? kStepMost : 0xffffffffu;
   p.tickets = static_cast<uint32_t*>(workspace);

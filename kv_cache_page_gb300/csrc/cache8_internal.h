@@ -47,6 +47,7 @@ struct C8Params {
   uint32_t step_warps;          // warps of a step CTA: 4, or as many as an SM holds (12; 8 for D = 256)
   uint32_t chunk;               // keys of a range (more where splits ranges of it do not reach)
   uint32_t min_rows, max_rows;  // sequences this launch serves: G * new within [min_rows, max_rows]
+  uint32_t rows8;               // step: every row tile has at most 8 rows
   uint32_t both_roles;          // write, read: a warp takes K and V of its page and head
   uint32_t per_seq;             // step: units of a sequence, 0: by cu_new
   uint32_t n_units;             // row tiles (step, prompt) or page units (write, read), an upper bound

@@ -98,7 +98,6 @@ struct StepShape {
   static constexpr int HT = TS / 16;                   // 16-token tiles of a step
   static constexpr int CH = D >= 64 ? 16 : 8;          // bytes of a K copy
   static constexpr int KC = D / 4 / CH;                // K copies of a lane and token
-  static constexpr int NT = D / 8;                     // 8-wide column tiles of the output
   static constexpr int VR = 512 / D;                   // token rows that a warp's 16-byte V copies cover
   static constexpr int kK = TS * D;                    // bytes of a stage's K and of its V
   // and FP32 scales of K and V per token; V tiles start at multiples of a row (addressed by xor)
@@ -146,9 +145,21 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
+// Transpose of an 8 x 8 tile of FP16, two values of a row to a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 // PAGED16: pages are whole 16-token tiles, so a tile lies in one page; otherwise
 // every token's page is looked up by itself.
-template <int DT, int D, bool PAGED16, int W>
+// N8: row tiles of at most 8 rows (one token and up to 8 query heads a KV head, the
+// usual step).  The products then have the tokens (scores) and the dims (output) as
+// their 16 rows and the 8 query rows as their columns: half the products, half the
+// exponentials and half the accumulators of 16 query rows.  The fragments of K and V
+// are the same; the weights pass through a transposition in registers.
+template <int DT, int D, bool PAGED16, int W, bool N8>
 __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
     c8_step_kernel(const __grid_constant__ C8Params p) {
   using S = StepShape<D>;
@@ -327,20 +338,26 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
         l4 = (dim >> 3) & 3u;
       }
       // fragment registers: a0 (row g, k lo), a1 (row g + 8, k lo), a2 (row g, k hi), a3 (row g + 8, k hi)
-      s_q[(ks * 32 + (r & 7u) * 4 + l4) * 4 + ((dim >> 1) & 1u) * 2 + (r >> 3)] = w[k];
+      // (N8: b0 (k lo), b1 (k hi) of column g)
+      if (!N8) s_q[(ks * 32 + (r & 7u) * 4 + l4) * 4 + ((dim >> 1) & 1u) * 2 + (r >> 3)] = w[k];
+      else if (r < 8u) s_q[(ks * 32 + r * 4 + l4) * 2 + ((dim >> 1) & 1u)] = w[k];
     }
     if (part == 0) s_row[r] = p.scale_log2 * __uint_as_float((uint32_t)(127 - ex) << 23);
   }
   cta_sync();
 
-  const float rf[2] = {s_row[g], s_row[g + 8]};
+  // this lane's rows of a score tile
+  const uint32_t row_of[2] = {N8 ? 2 * qd : g, N8 ? 2 * qd + 1 : g + 8};
+  const float rf[2] = {s_row[row_of[0]], s_row[row_of[1]]};
   // steps between these need no mask
   const int32_t full_hi = min(c_hi, first_pos < 0 ? 0 : p.causal ? min(q.len, first_pos + 1) : q.len);
   const int32_t full_lo = p.window ? (int32_t)max((int64_t)0, (int64_t)last_pos - p.window + 1) : 0;
 
-  float o[S::NT][4];
+  constexpr int NT = N8 ? D / 16 : D / 8;  // output tiles: 16 dims x 8 rows, or 16 rows x 8 dims
+  constexpr int SH = N8 ? HT : 2 * HT;     // score tiles: 16 tokens x 8 rows, or 16 rows x 8 tokens
+  float o[NT][4];
 #pragma unroll
-  for (int n = 0; n < S::NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
+  for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
   float m[2] = {kNegInf, kNegInf}, l[2] = {0.0f, 0.0f};
   // V scales are held relative to the largest that the row has seen
   float vref[2] = {1.17549435e-38f, 1.17549435e-38f}, vinv[2] = {0.0f, 0.0f};
@@ -366,10 +383,11 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
     stage = stage == NS - 1 ? 0 : stage + 1;
     const int32_t tok0 = c_lo + TS * t;
 
-    // scores: s[2 t16 + h][.] of columns 2 qd, + 1 of rows g, g + 8
-    float s[2 * HT][4];
+    // scores: s[2 t16 + h][.] of columns 2 qd, + 1 of rows g, g + 8 (N8: s[t16][.] of tokens g, g + 8 as rows,
+    // query rows 2 qd, + 1)
+    float s[SH][4];
 #pragma unroll
-    for (int h = 0; h < 2 * HT; ++h) s[h][0] = s[h][1] = s[h][2] = s[h][3] = 0.0f;
+    for (int h = 0; h < SH; ++h) s[h][0] = s[h][1] = s[h][2] = s[h][3] = 0.0f;
 #pragma unroll
     for (int c = 0; c < S::KC; ++c) {
       uint32_t kw[2 * HT][4];
@@ -386,63 +404,83 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
       }
 #pragma unroll
       for (int i = 0; i < S::CH / 4; ++i) {
-        const uint4 a = *reinterpret_cast<const uint4*>(s_q + ((c * (S::CH / 4) + i) * 32 + lane) * 4);
+        if constexpr (N8) {
+          const uint2 b = *reinterpret_cast<const uint2*>(s_q + ((c * (S::CH / 4) + i) * 32 + lane) * 2);
 #pragma unroll
-        for (int h = 0; h < 2 * HT; ++h) {
-          uint32_t b0, b1;
-          c8_dec4(kw[h][i], b0, b1);
-          mma16816(s[h], a.x, a.y, a.z, a.w, b0, b1);
+          for (int t16 = 0; t16 < HT; ++t16) {
+            uint32_t a0, a1, a2, a3;
+            c8_dec4(kw[2 * t16][i], a0, a2);
+            c8_dec4(kw[2 * t16 + 1][i], a1, a3);
+            mma16816(s[t16], a0, a1, a2, a3, b.x, b.y);
+          }
+        } else {
+          const uint4 a = *reinterpret_cast<const uint4*>(s_q + ((c * (S::CH / 4) + i) * 32 + lane) * 4);
+#pragma unroll
+          for (int h = 0; h < 2 * HT; ++h) {
+            uint32_t b0, b1;
+            c8_dec4(kw[h][i], b0, b1);
+            mma16816(s[h], a.x, a.y, a.z, a.w, b0, b1);
+          }
         }
       }
     }
     // scales of tokens 16 t16 + 4 qd .. + 3; column (h, e) of a tile is token 2 h + e of these
+    // (N8: of tokens tok_of(g, 0), tok_of(g, 1), in .x and .y)
     float vt[2] = {0.0f, 0.0f};
     bool hole = false;  // a token has the scale 0 of one that was not copied
     float4 vs[HT];
 #pragma unroll
     for (int t16 = 0; t16 < HT; ++t16) {
-      const uint32_t i = PAGED16 ? 16 * t16 : 16 * t16 + 4 * qd;
-      const float4 k4 = *reinterpret_cast<const float4*>(sp + 2 * S::kK + i * 4);
-      vs[t16] = *reinterpret_cast<const float4*>(sp + 2 * S::kK + 4 * TS + i * 4);
+      const float* kp = reinterpret_cast<const float*>(sp + 2 * S::kK) + 16 * t16;
+      const float* vp = kp + TS;
+      float4 k4;
       if (PAGED16) {
-        const float f0 = k4.x * rf[0], f1 = k4.x * rf[1];
+        k4 = make_float4(*kp, *kp, *kp, *kp);
+        vs[t16] = make_float4(*vp, *vp, *vp, *vp);
         hole |= k4.x == 0.0f;
-#pragma unroll
-        for (int h = 2 * t16; h < 2 * t16 + 2; ++h) {
-          s[h][0] *= f0; s[h][1] *= f0;
-          s[h][2] *= f1; s[h][3] *= f1;
-        }
         vt[0] = fmaxf(vt[0], vs[t16].x);
+      } else if (N8) {
+        k4 = make_float4(kp[tok_of(g, 0)], kp[tok_of(g, 1)], 1.0f, 1.0f);
+        vs[t16] = make_float4(vp[tok_of(g, 0)], vp[tok_of(g, 1)], 0.0f, 0.0f);
+        hole |= k4.x == 0.0f || k4.y == 0.0f;
+        vt[0] = fmaxf(vt[0], fmaxf(vs[t16].x, vs[t16].y));
       } else {
+        k4 = *reinterpret_cast<const float4*>(kp + 4 * qd);
+        vs[t16] = *reinterpret_cast<const float4*>(vp + 4 * qd);
         hole |= k4.x == 0.0f || k4.y == 0.0f || k4.z == 0.0f || k4.w == 0.0f;
-        s[2 * t16][0] *= k4.x * rf[0]; s[2 * t16][1] *= k4.y * rf[0];
-        s[2 * t16][2] *= k4.x * rf[1]; s[2 * t16][3] *= k4.y * rf[1];
-        s[2 * t16 + 1][0] *= k4.z * rf[0]; s[2 * t16 + 1][1] *= k4.w * rf[0];
-        s[2 * t16 + 1][2] *= k4.z * rf[1]; s[2 * t16 + 1][3] *= k4.w * rf[1];
         vt[0] = fmaxf(vt[0], fmaxf(fmaxf(vs[t16].x, vs[t16].y), fmaxf(vs[t16].z, vs[t16].w)));
+      }
+      if (N8) {
+        s[t16][0] *= k4.x * rf[0]; s[t16][1] *= k4.x * rf[1];
+        s[t16][2] *= k4.y * rf[0]; s[t16][3] *= k4.y * rf[1];
+      } else {
+        s[(2 * t16) % SH][0] *= k4.x * rf[0]; s[(2 * t16) % SH][1] *= k4.y * rf[0];
+        s[(2 * t16) % SH][2] *= k4.x * rf[1]; s[(2 * t16) % SH][3] *= k4.y * rf[1];
+        s[(2 * t16 + 1) % SH][0] *= k4.z * rf[0]; s[(2 * t16 + 1) % SH][1] *= k4.w * rf[0];
+        s[(2 * t16 + 1) % SH][2] *= k4.z * rf[1]; s[(2 * t16 + 1) % SH][3] *= k4.w * rf[1];
       }
     }
     if (!PAGED16) hole = __any_sync(0xffffffffu, hole);
     vt[1] = vt[0];
     const bool masked = hole || tok0 + TS > full_hi || tok0 < full_lo;
     if (masked) {
-      // visible keys of this lane's rows g and g + 8
+      // visible keys of this lane's rows
       int32_t vis_hi[2], vis_lo[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t r = g + 8 * h;
+        const uint32_t r = row_of[h];
         const int32_t pos = q.start + (int32_t)((r0 + r) / p.G);
         vis_hi[h] = p.causal ? min(c_hi, pos + 1) : c_hi;  // c_hi: at most the length
         vis_lo[h] = p.window ? (int32_t)max((int64_t)0, (int64_t)pos - p.window + 1) : 0;
         if (r >= n_rows || pos < 0) vis_hi[h] = 0;
       }
 #pragma unroll
-      for (int h = 0; h < 2 * HT; ++h)
+      for (int h = 0; h < SH; ++h)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const uint32_t i = 16 * (h >> 1) + 4 * qd + 2 * (h & 1) + (e & 1);
+          const uint32_t i = N8 ? 16 * h + tok_of(g, e >> 1) : 16 * (h >> 1) + 4 * qd + 2 * (h & 1) + (e & 1);
           const int32_t tok = tok0 + (int32_t)i;
-          const int r = e >> 1;
+          const int r = N8 ? e & 1 : e >> 1;
           if (tok >= vis_hi[r] || tok < vis_lo[r] ||
               (hole && *reinterpret_cast<const float*>(sp + 2 * S::kK + i * 4) == 0.0f))
             s[h][e] = kNegInf;
@@ -455,8 +493,8 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
         for (int t16 = 0; t16 < HT; ++t16) {
           const float v4[4] = {vs[t16].x, vs[t16].y, vs[t16].z, vs[t16].w};
 #pragma unroll
-          for (int i = 0; i < (PAGED16 ? 1 : 4); ++i) {
-            const int32_t a = tok0 + 16 * t16 + (PAGED16 ? 0 : (int32_t)(4 * qd) + i);
+          for (int i = 0; i < (PAGED16 ? 1 : N8 ? 2 : 4); ++i) {
+            const int32_t a = tok0 + 16 * t16 + (PAGED16 ? 0 : N8 ? (int32_t)tok_of(g, i) : (int32_t)(4 * qd) + i);
             if (a < vis_hi[r] && a + (PAGED16 ? 16 : 1) > vis_lo[r]) vt[r] = fmaxf(vt[r], v4[i]);
           }
         }
@@ -467,19 +505,19 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
     float mt[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      float x = fmaxf(s[0][2 * r], s[0][2 * r + 1]);
+      float x = kNegInf;
 #pragma unroll
-      for (int h = 1; h < 2 * HT; ++h) x = fmaxf(x, fmaxf(s[h][2 * r], s[h][2 * r + 1]));
-      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+      for (int h = 0; h < SH; ++h) x = fmaxf(x, N8 ? fmaxf(s[h][r], s[h][2 + r]) : fmaxf(s[h][2 * r], s[h][2 * r + 1]));
+#pragma unroll
+      for (int d = N8 ? 4 : 1; d < (N8 ? 32 : 4); d *= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
       mt[r] = x;
       grow |= x > m[r] + kLag;  // -inf + kLag = -inf: any finite score of a fresh row
     }
     if (!PAGED16) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        vt[r] = fmaxf(vt[r], __shfl_xor_sync(0xffffffffu, vt[r], 1));
-        vt[r] = fmaxf(vt[r], __shfl_xor_sync(0xffffffffu, vt[r], 2));
+#pragma unroll
+        for (int d = N8 ? 4 : 1; d < (N8 ? 32 : 4); d *= 2) vt[r] = fmaxf(vt[r], __shfl_xor_sync(0xffffffffu, vt[r], d));
       }
     }
     if (__any_sync(0xffffffffu, grow || vt[0] > vref[0] || vt[1] > vref[1])) {
@@ -494,9 +532,9 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
         vref[r] = vn;
         vinv[r] = vt[r] > 0.0f || vinv[r] != 0.0f ? kLift / vn : 0.0f;  // 0 until the row has seen a scale
 #pragma unroll
-        for (int n = 0; n < S::NT; ++n) {
-          o[n][2 * r] *= fo;
-          o[n][2 * r + 1] *= fo;
+        for (int n = 0; n < NT; ++n) {
+          o[n][N8 ? r : 2 * r] *= fo;
+          o[n][N8 ? 2 + r : 2 * r + 1] *= fo;
         }
       }
     }
@@ -507,19 +545,33 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
       const float v4[4] = {vs[t16].x, PAGED16 ? vs[t16].x : vs[t16].y, PAGED16 ? vs[t16].x : vs[t16].z,
                            PAGED16 ? vs[t16].x : vs[t16].w};
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float z0 = s[2 * t16 + h][2 * r], z1 = s[2 * t16 + h][2 * r + 1];
-          const float p0 = ex2(z0 - (r ? b1 : b0)), p1 = ex2(z1 - (r ? b1 : b0));
-          l[r] += p0 + p1;
-          float x0 = p0 * (v4[2 * h] * vinv[r]), x1 = p1 * (v4[2 * h + 1] * vinv[r]);
-          if (masked) {  // 0 whatever the scale of the page that holds a token the row does not see
+      for (int h = 0; h < 2; ++h) {
+        if constexpr (N8) {  // tokens tok_of(g, h), rows 2 qd, + 1: transposed to row g, tokens 4 qd + 2 h, + 1
+          const float z0 = s[t16][2 * h], z1 = s[t16][2 * h + 1];
+          const float p0 = ex2(z0 - b0), p1 = ex2(z1 - b1);
+          l[0] += p0;
+          l[1] += p1;
+          float x0 = p0 * ((h ? v4[1] : v4[0]) * vinv[0]), x1 = p1 * ((h ? v4[1] : v4[0]) * vinv[1]);
+          if (masked) {
             x0 = z0 == kNegInf ? 0.0f : x0;
             x1 = z1 == kNegInf ? 0.0f : x1;
           }
-          pa[t16][2 * h + r] = pack2<0>(x0, x1);
+          pa[t16][h] = transpose8(pack2<0>(x0, x1));
+        } else {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float z0 = s[(2 * t16 + h) % SH][2 * r], z1 = s[(2 * t16 + h) % SH][2 * r + 1];
+            const float p0 = ex2(z0 - (r ? b1 : b0)), p1 = ex2(z1 - (r ? b1 : b0));
+            l[r] += p0 + p1;
+            float x0 = p0 * (v4[2 * h] * vinv[r]), x1 = p1 * (v4[2 * h + 1] * vinv[r]);
+            if (masked) {  // 0 whatever the scale of the page that holds a token the row does not see
+              x0 = z0 == kNegInf ? 0.0f : x0;
+              x1 = z1 == kNegInf ? 0.0f : x1;
+            }
+            pa[t16][2 * h + r] = pack2<0>(x0, x1);
+          }
         }
+      }
     }
     // V: words of four tokens (4 qd .. + 3) at dims 8 n + g
     uint32_t any_nan = 0;
@@ -539,11 +591,21 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
             vw[k] &= ~((nb >> 7) * 0xffu);
           }
         }
+        if constexpr (N8) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t v0, v1;
-          c8_dec4(vw[k], v0, v1);
-          mma16816(o[4 * c + k], pa[t16][0], pa[t16][1], pa[t16][2], pa[t16][3], v0, v1);
+          for (int k = 0; k < 2; ++k) {  // dims 16 (2 c + k) + g, + 8
+            uint32_t a0, a1, a2, a3;
+            c8_dec4(vw[2 * k], a0, a2);
+            c8_dec4(vw[2 * k + 1], a1, a3);
+            mma16816(o[2 * c + k], a0, a1, a2, a3, pa[t16][0], pa[t16][1]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t v0, v1;
+            c8_dec4(vw[k], v0, v1);
+            mma16816(o[(4 * c + k) % NT], pa[t16][0], pa[t16][1], pa[t16][2], pa[t16][3], v0, v1);
+          }
         }
       }
     if (masked && __any_sync(0xffffffffu, any_nan != 0u)) {
@@ -552,27 +614,37 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
       for (int t16 = 0; t16 < HT; ++t16) {
         uint32_t seen[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h) {
+          if constexpr (N8) {
+            const float z0 = t16 ? s[HT - 1][2 * h] : s[0][2 * h], z1 = t16 ? s[HT - 1][2 * h + 1] : s[0][2 * h + 1];
+            seen[h] = transpose8((z0 == kNegInf ? 0u : 0x3c00u) | (z1 == kNegInf ? 0u : 0x3c000000u));
+          } else {
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float z0 = t16 ? s[2 * (HT - 1) + h][2 * r] : s[h][2 * r];
-            const float z1 = t16 ? s[2 * (HT - 1) + h][2 * r + 1] : s[h][2 * r + 1];
-            seen[2 * h + r] = (z0 == kNegInf ? 0u : 0x3c00u) | (z1 == kNegInf ? 0u : 0x3c000000u);
+            for (int r = 0; r < 2; ++r) {
+              const float z0 = t16 ? s[(2 * (HT - 1) + h) % SH][2 * r] : s[h][2 * r];
+              const float z1 = t16 ? s[(2 * (HT - 1) + h) % SH][2 * r + 1] : s[h][2 * r + 1];
+              seen[2 * h + r] = (z0 == kNegInf ? 0u : 0x3c00u) | (z1 == kNegInf ? 0u : 0x3c000000u);
+            }
           }
+        }
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
-          uint32_t vw[4];
+          uint32_t vw[4], v[4][2];
           ldsm_t16x2(vw, (sv ^ (c << 5)) + 16 * t16 * D);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const uint32_t nb = nan_bytes(vw[k]);  // 0x80 bytes -> 1.0 halves
-            const uint32_t v0 = (nb & 0x80u ? 0x3c00u : 0u) | (nb & 0x8000u ? 0x3c000000u : 0u);
-            const uint32_t v1 = (nb & 0x800000u ? 0x3c00u : 0u) | (nb & 0x80000000u ? 0x3c000000u : 0u);
+            v[k][0] = (nb & 0x80u ? 0x3c00u : 0u) | (nb & 0x8000u ? 0x3c000000u : 0u);
+            v[k][1] = (nb & 0x800000u ? 0x3c00u : 0u) | (nb & 0x80000000u ? 0x3c000000u : 0u);
+          }
+#pragma unroll
+          for (int k = 0; k < (N8 ? 2 : 4); ++k) {
             float cnt[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816(cnt, seen[0], seen[1], seen[2], seen[3], v0, v1);
+            if (N8) mma16816(cnt, v[(2 * k) & 3][0], v[(2 * k + 1) & 3][0], v[(2 * k) & 3][1], v[(2 * k + 1) & 3][1], seen[0], seen[1]);
+            else mma16816(cnt, seen[0], seen[1], seen[2], seen[3], v[k][0], v[k][1]);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (cnt[e] > 0.0f) o[4 * c + k][e] = __int_as_float(0x7fffffff);
+              if (cnt[e] > 0.0f) o[((N8 ? 2 : 4) * c + k) % NT][e] = __int_as_float(0x7fffffff);
           }
         }
       }
@@ -582,8 +654,8 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
   if (bad) c8_error(p, q.s, KV_CACHE8_BAD_PAGE);
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-    l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+#pragma unroll
+    for (int d = N8 ? 4 : 1; d < (N8 ? 32 : 4); d *= 2) l[r] += __shfl_xor_sync(0xffffffffu, l[r], d);
   }
 
   // ---- join the warps: every row to the largest maximum among them
@@ -593,25 +665,33 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
   float* s_o = reinterpret_cast<float*>(smem + S::kQ + S::kSmall);  // [warp][16][D + 4], over the slots
   static_assert((16 + 32 * W) * 4 + 128 <= S::kSmall, "");
   constexpr int OS = D + 4;
-  if (qd == 0) {
-    s_m[g * W + warp] = m[0];
-    s_m[(g + 8) * W + warp] = m[1];
+  const bool holder = N8 ? g == 0u : qd == 0u;  // one lane for each row
+  if (holder) {
+    s_m[row_of[0] * W + warp] = m[0];
+    s_m[row_of[1] * W + warp] = m[1];
   }
   cta_sync();
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
-    const uint32_t row = g + 8 * r;
+    const uint32_t row = row_of[r];
     float mx = kNegInf;
 #pragma unroll
     for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_m[row * W + w]);
     const float f = m[r] == kNegInf ? 0.0f : ex2(m[r] - mx);
     const float fo = m[r] == kNegInf ? 0.0f : f * (vref[r] * (1.0f / kLift));
-    if (qd == 0) s_l[row * W + warp] = l[r] * f;
-    // column 2 qd + e of tile n is dim 8 n + 2 qd + e
-    float* dst = s_o + (warp * 16 + row) * OS + 2 * qd;
+    if (holder) s_l[row * W + warp] = l[r] * f;
+    float* dst = s_o + (warp * 16 + row) * OS;
+    if (N8) {  // tile n: dims 16 n + g, + 8 of the lane's rows
 #pragma unroll
-    for (int n = 0; n < S::NT; ++n)
-      *reinterpret_cast<float2*>(dst + 8 * n) = make_float2(o[n][2 * r] * fo, o[n][2 * r + 1] * fo);
+      for (int n = 0; n < NT; ++n) {
+        dst[16 * n + g] = o[n][r] * fo;
+        dst[16 * n + 8 + g] = o[n][2 + r] * fo;
+      }
+    } else {  // column 2 qd + e of tile n is dim 8 n + 2 qd + e
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        *reinterpret_cast<float2*>(dst + 8 * n + 2 * qd) = make_float2(o[n][(2 * r) & 3] * fo, o[n][(2 * r + 1) & 3] * fo);
+    }
   }
   cta_sync();
   const uint32_t job = u * p.H + head;
@@ -751,10 +831,10 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
   else join(std::integral_constant<uint32_t, 16>{});
 }
 
-template <int DT, int D, bool PAGED16, int W>
+template <int DT, int D, bool PAGED16, int W, bool N8>
 int step_launch(const C8Params& p, void* stream) {
   constexpr int bytes = step_smem<D, W>();
-  const auto kernel = c8_step_kernel<DT, D, PAGED16, W>;
+  const auto kernel = c8_step_kernel<DT, D, PAGED16, W, N8>;
   static std::atomic<uint64_t> done{0};
   if (!allow_smem(kernel, bytes, done)) return KV_ERR_CUDA;
   const uint64_t gx = (uint64_t)p.n_units * p.splits * p.H;
@@ -768,12 +848,17 @@ int step_launch(const C8Params& p, void* stream) {
       p);
 }
 
-template <int DT, int D>
-int step_d(const C8Params& p, void* stream) {
+template <int DT, int D, bool PAGED16>
+int step_p(const C8Params& p, void* stream) {
   constexpr int BIG = D == 256 ? 8 : 12;
   if (p.step_warps > 4)
-    return p.T % 16 == 0 ? step_launch<DT, D, true, BIG>(p, stream) : step_launch<DT, D, false, BIG>(p, stream);
-  return p.T % 16 == 0 ? step_launch<DT, D, true, 4>(p, stream) : step_launch<DT, D, false, 4>(p, stream);
+    return p.rows8 ? step_launch<DT, D, PAGED16, BIG, true>(p, stream) : step_launch<DT, D, PAGED16, BIG, false>(p, stream);
+  return p.rows8 ? step_launch<DT, D, PAGED16, 4, true>(p, stream) : step_launch<DT, D, PAGED16, 4, false>(p, stream);
+}
+
+template <int DT, int D>
+int step_d(const C8Params& p, void* stream) {
+  return p.T % 16 == 0 ? step_p<DT, D, true>(p, stream) : step_p<DT, D, false>(p, stream);
 }
 
 }  // namespace
