@@ -96,7 +96,8 @@ typedef struct kv_cache8_batch {
   int64_t table_stride;     /* entries between table rows */
   const int32_t* tables;    /* device: page of tokens [i T, (i + 1) T) of sequence s at s * table_stride + i */
   const int32_t* lens;      /* device [n_seqs]: tokens held, the new ones among them */
-  const int32_t* cu_new;    /* device [n_seqs + 1], ascending from 0; NULL: one new token each */
+  const int32_t* cu_new;    /* device [n_seqs + 1], ascending from 0; NULL: one new token each (which attention
+                               then takes for granted, and is faster for) */
   uint32_t* errors;         /* device [n_seqs] or NULL: KV_CACHE8_* bits are or-ed in */
 } kv_cache8_batch;
 

@@ -2,8 +2,9 @@
 
 The codec itself is the C-ABI library ``libkvcodec.so`` built from ``csrc/``
 (hand-written CUDA kernels plus a small host library); ``codec`` is its thin
-ctypes binding and ``synth`` makes seeded synthetic KV caches.  Importing the
+ctypes binding and ``synth`` makes seeded synthetic KV caches.  ``cache8`` binds the
+live 8-bit KV cache of the same library (write, read back, attention).  Importing the
 package does not load the library; the first codec call does, and fails with a
 clear error when it has not been built.
 """
-__all__ = ["codec", "synth"]
+__all__ = ["cache8", "codec", "synth"]

@@ -21,8 +21,10 @@
 // stands (see tok_of).  Codes become FP16 exactly; K's scale multiplies the scores,
 // V's scale the weights.
 //
-// What the walk costs besides bytes is instructions: 64 conversions and 32
-// products per 16 tokens and D = 128 are the floor.
+// What the walk costs besides bytes is instructions, at 12 warps an SM: per 16
+// tokens and D = 128, 64 conversions and 32 products (16 with at most 8 query rows)
+// are the floor.  Measured on a GB300, 8 heads of 128: 64 sequences of 100 to 8192 tokens
+// 66 us (4.4 TB/s of codes), one of 131072 with 4 heads 36 us (3.8).
 #include <type_traits>
 
 #include "cache8_common.cuh"
