@@ -78,6 +78,13 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// One arrival for the warp, after what all its lanes did (32 arrivals on one
+// barrier are carried out one after the other).
+__device__ __forceinline__ void mbar_arrive_warp(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31u) == 0u) mbar_arrive(bar);
+  __syncwarp();
+}
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -176,10 +183,12 @@ struct PromptShape {
   static constexpr uint32_t kQTile = DG * 128 * 128;     // bytes
   static constexpr uint32_t kTile = DG * kKeys * 128;    // of K or V
   static constexpr uint32_t kQ = 0, kK = 2 * kQTile, kV = kK + 2 * kTile;
-  static constexpr uint32_t kScale = kV + 2 * kTile;     // [stage] FP32: K[128], V[128], log2 V[128] (whole pages: 8 of each), V's largest, whether K has a 0
+  // records of 4 tiles, FP32: K's scales [128], V's [128], log2 of V's [128] (whole pages: 8 of each), V's
+  // largest, whether K has a 0
+  static constexpr uint32_t kScale = kV + 2 * kTile;
   static constexpr uint32_t kScaleStage = (3 * kKeys + 4) * 4;
-  static constexpr uint32_t kNan = kScale + 2 * kScaleStage;         // [stage][token][D / 32] bits of V's NaN codes
-  static constexpr uint32_t kRowNan = kNan + 2 * kKeys * (D / 32) * 4; // [row][D / 32]: dims whose output is NaN
+  static constexpr uint32_t kNan = kScale + 4 * kScaleStage;         // [record][token][D / 32] bits of V's NaN codes
+  static constexpr uint32_t kRowNan = kNan + 4 * kKeys * (D / 32) * 4; // [row][D / 32]: dims whose output is NaN
   static constexpr uint32_t kBar = kRowNan + 256 * (D / 32) * 4;
   static constexpr uint32_t kBytes = kBar + 256;
   static constexpr uint32_t kS = 0, kO = 256;            // TMEM columns: scores 2 x 128, then outputs 2 x D
@@ -247,13 +256,13 @@ __device__ __forceinline__ float row_weights(uint32_t s_at, const float* ks, con
                                              int32_t hi_c) {
   constexpr int G = PAGED16 ? 16 : 4;  // columns handled together; of whole pages they share their scales
   float total = 0.0f;
-  uint32_t x[2][32];
+  uint32_t x[2][32], w[2][16];
   tm_ld32(s_at, x[0]);
 #pragma unroll
   for (int c = 0; c < kKeys / 32; ++c) {
     tm_wait_ld();
     if (c + 1 < kKeys / 32) tm_ld32(s_at + 32 * (c + 1), x[(c + 1) & 1]);
-    uint32_t w[16];
+    if (c > 0) tm_st16(s_at + 16 * (c - 1), w[(c - 1) & 1]);  // (a chunk late: this one's work fills its tail)
 #pragma unroll
     for (int i = 0; i < 32; i += G) {
       const int col = 32 * c + i;
@@ -291,12 +300,12 @@ __device__ __forceinline__ float row_weights(uint32_t s_at, const float* ks, con
           if (!MASK || z.x != kNegInf) total += y.x * ex2(-ll[e & 3]);
           if (!MASK || z.y != kNegInf) total += y.y * ex2(-ll[(e + 1) & 3]);
         }
-        w[(i + e) / 2] = pack2<0>(y.x, y.y);
+        w[c & 1][(i + e) / 2] = pack2<0>(y.x, y.y);
       }
       if (PAGED16) total += (sum.x + sum.y) * ex2(-ll[0]);
     }
-    tm_st16(s_at + 16 * c, w);
   }
+  tm_st16(s_at + 16 * (kKeys / 32 - 1), w[(kKeys / 32 - 1) & 1]);
   return total;
 }
 
@@ -395,8 +404,6 @@ __device__ __forceinline__ void load_tiles(const C8Params& p, const C8Seq& q, ui
   ask(1);
   for (int32_t j = 0; j < n_steps; ++j) {
     const uint32_t st = j & 1, ph = (j >> 1) & 1;
-    if (!__all_sync(0xffffffffu, mbar_wait(empty + 8 * st, ph ^ 1u, stop))) break;
-    uint8_t* tile = smem + (IS_K ? S::kK : S::kV) + st * S::kTile;
     if (!IS_K) {
       uint32_t any = 0;
 #pragma unroll
@@ -415,13 +422,13 @@ __device__ __forceinline__ void load_tiles(const C8Params& p, const C8Seq& q, ui
           }
           const uint32_t r = (i / S::DG) * RPI + row;
           if (r < kKeys)
-            reinterpret_cast<uint16_t*>(smem + S::kNan)[(st * kKeys + r) * (D / 16) + (i % S::DG) * 4 + c] =
+            reinterpret_cast<uint16_t*>(smem + S::kNan)[((j & 3) * kKeys + r) * (D / 16) + (i % S::DG) * 4 + c] =
                 (uint16_t)bits;
         }
       }
-      if (lane == 0) reinterpret_cast<uint8_t*>(nan_seen)[4 * st + (lt >> 5)] = (uint8_t)any;
+      if (lane == 0) reinterpret_cast<uint8_t*>(nan_seen)[4 * (j & 3) + (lt >> 5)] = (uint8_t)any;
     }
-    float* sc = reinterpret_cast<float*>(smem + S::kScale + st * S::kScaleStage);
+    float* sc = reinterpret_cast<float*>(smem + S::kScale + (j & 3) * S::kScaleStage);
     if (!IS_K && PAGED16 && lt < 32u) {
       float top = vsc[0];
 #pragma unroll
@@ -444,7 +451,11 @@ __device__ __forceinline__ void load_tiles(const C8Params& p, const C8Seq& q, ui
         sc[kKeys + i * W * 32 + lt] = vsc[i];
         sc[2 * kKeys + i * W * 32 + lt] = vsc[i] > 0.0f ? lg2(vsc[i]) : vsc[i];
       }
-    if (!IS_K) mbar_arrive(scales + 8 * st);  // the softmax needs these and the NaN flags, before V itself is wanted
+    // The softmax wants these and the NaN flags before V itself: they do not wait for V's stage.  (Record j mod 4
+    // is free: the softmax is past tile j - 3, whose product this loop has waited for.)
+    if (!IS_K) mbar_arrive_warp(scales + 8 * (j & 3));
+    if (!__all_sync(0xffffffffu, mbar_wait(empty + 8 * st, ph ^ 1u, stop))) break;
+    uint8_t* tile = smem + (IS_K ? S::kK : S::kV) + st * S::kTile;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       uint4 h0, h1;
@@ -459,8 +470,7 @@ __device__ __forceinline__ void load_tiles(const C8Params& p, const C8Seq& q, ui
       }
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    mbar_arrive(full + 8 * st);
-    __syncwarp();
+    mbar_arrive_warp(full + 8 * st);
     if (j + 1 < n_steps) fetch(j + 1);
     ask(j + 2);
   }
@@ -493,24 +503,25 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
   const uint32_t bar = sbase + S::kBar;
   const uint32_t k_full = bar, k_empty = bar + 16, v_full = bar + 32, v_empty = bar + 48;  // [2]
   const uint32_t s_full = bar + 64, p_full = bar + 80, pv_done = bar + 96;                  // [2]
-  const uint32_t q_full = bar + 144, c_full = bar + 152;                                   // c_full: [2]
+  const uint32_t q_full = bar + 144, c_full = bar + 152;                                   // c_full: [4]
   volatile uint32_t* stop = reinterpret_cast<volatile uint32_t*>(smem + S::kBar + 112);
-  uint32_t* nan_seen = reinterpret_cast<uint32_t*>(smem + S::kBar + 116);   // [stage]: a byte a loading warp, V has NaN codes
+  uint32_t* nan_seen = reinterpret_cast<uint32_t*>(smem + S::kBar + 192);   // [record]: a byte a loading warp, V has NaN codes
   uint32_t* any_row_nan = reinterpret_cast<uint32_t*>(smem + S::kBar + 124);
   uint32_t* tm_at = reinterpret_cast<uint32_t*>(smem + S::kBar + 128);
   if (tid == 0) {
     for (uint32_t i = 0; i < 2; ++i) {
-      mbar_init(k_full + 8 * i, kKWarps * 32);
+      mbar_init(k_full + 8 * i, kKWarps);
       mbar_init(k_empty + 8 * i, 1);
-      mbar_init(v_full + 8 * i, kVWarps * 32);
+      mbar_init(v_full + 8 * i, kVWarps);
       mbar_init(v_empty + 8 * i, 1);
-      mbar_init(c_full + 8 * i, kVWarps * 32);
+      mbar_init(c_full + 8 * i, kVWarps);
+      mbar_init(c_full + 8 * i + 16, kVWarps);
       mbar_init(s_full + 8 * i, 1);
-      mbar_init(p_full + 8 * i, 128);
+      mbar_init(p_full + 8 * i, 4);
       mbar_init(pv_done + 8 * i, 1);
-      nan_seen[i] = 0;
+      nan_seen[i] = nan_seen[i + 2] = 0;
     }
-    mbar_init(q_full, 256);
+    mbar_init(q_full, kSoftWarps);
     *stop = 0;
     *any_row_nan = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -575,8 +586,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) rn[k] = 0;
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    mbar_arrive(q_full);
-    __syncwarp();
+    mbar_arrive_warp(q_full);
   }
 
   // Registers: 512 threads start with 128 each; the softmax takes 176 (a row's 128
@@ -602,15 +612,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
       const int32_t full_lo = p.window ? (int32_t)max((int64_t)0, (int64_t)pos_b - p.window + 1) : 0;
       for (int32_t j = 0; j < n_steps && fine; ++j) {
         const int32_t tok0 = lo + j * kKeys;
-        const uint32_t st = j & 1;
-        const float* ks = reinterpret_cast<const float*>(smem + S::kScale + st * S::kScaleStage);
+        const uint32_t rec = j & 3;
+        const float* ks = reinterpret_cast<const float*>(smem + S::kScale + rec * S::kScaleStage);
         const float* vs = ks + kKeys;
-        fine = mbar_wait(c_full + 8 * st, (j >> 1) & 1, stop) && mbar_wait(s_full + 8 * t, j & 1, stop);
+        fine = mbar_wait(c_full + 8 * rec, (j >> 2) & 1, stop) && mbar_wait(s_full + 8 * t, j & 1, stop);
         fine = __all_sync(0xffffffffu, fine);
         if (!fine) break;
         __syncwarp();
         tc_fence_after();
         // holes of K (a token without a page has the scale 0), the largest scale of V
+        const uint32_t nan_w = nan_seen[rec];
         float vt = ks[3 * kKeys];
         bool hole = ks[3 * kKeys + 1] != 0.0f;
         if (!PAGED16) {
@@ -682,11 +693,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
         // (bits are kept by the loading warps that saw one: rows 8 w .. 8 w + 7 of a round of kVWarps * 8)
         auto tok_nan = [&](int32_t c) {
           constexpr int R = D >= 64 ? 8 : 16;
-          return (nan_seen[st] >> (8 * ((c / R) % kVWarps))) & 1u;
+          return (nan_w >> (8 * ((c / R) % kVWarps))) & 1u;
         };
-        if (masked && nan_seen[st]) {
+        if (masked && nan_w) {
           // V has NaN codes (laid out as 0): the dims that a token seen by this row has them at
-          const uint32_t* bits = reinterpret_cast<const uint32_t*>(smem + S::kNan) + st * kKeys * (D / 32);
+          const uint32_t* bits = reinterpret_cast<const uint32_t*>(smem + S::kNan) + rec * kKeys * (D / 32);
           uint32_t* rn = reinterpret_cast<uint32_t*>(smem + S::kRowNan) + r * (D / 32);
           uint32_t any = 0;
           for (int32_t c = max(0, vis_lo - tok0); c < min(kKeys, vis_hi - tok0); ++c)
@@ -697,8 +708,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
                 rn[k] |= b;
               }
           if (any) *any_row_nan = 1;
-        } else if (nan_seen[st]) {
-          const uint32_t* bits = reinterpret_cast<const uint32_t*>(smem + S::kNan) + st * kKeys * (D / 32);
+        } else if (nan_w) {
+          const uint32_t* bits = reinterpret_cast<const uint32_t*>(smem + S::kNan) + rec * kKeys * (D / 32);
           uint32_t* rn = reinterpret_cast<uint32_t*>(smem + S::kRowNan) + r * (D / 32);
           for (int32_t c = 0; c < kKeys; ++c)
             if (tok_nan(c))
@@ -715,7 +726,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
           l += row_weights<PAGED16, false, false>(s_at, ks, vs + kKeys, f8, l8, rf, lref, base, lo_c, hi_c);
         tm_wait_st();
         tc_fence_before();
-        mbar_arrive(p_full + 8 * t);
+        mbar_arrive_warp(p_full + 8 * t);
       }
       // ---- outputs
       if (n_steps > 0 && fine) {
