@@ -313,8 +313,8 @@ __device__ __forceinline__ float row_weights(uint32_t s_at, const float* ks, con
 // W warps bring K (IS_K) or V of tile after tile into its two stages.  A 16-byte
 // chunk of codes, CPR of a 64-dim group a token, a thread to each, makes two 16-byte
 // chunks of FP16 (8 lanes in turn, 4 chunks of two tokens, write to 8 different bank
-// groups).  The codes of the next tile are on their way while one is written, its
-// pages known a tile earlier.
+// groups).  A chunk of the next tile is asked for as soon as one of this tile is
+// written, its page known a tile earlier.
 template <int D, bool PAGED16, bool IS_K, int W>
 __device__ __forceinline__ void load_tiles(const C8Params& p, const C8Seq& q, uint8_t* smem, uint32_t head, int32_t lo,
                                            int32_t hi, int32_t n_steps, uint32_t full, uint32_t empty,
@@ -360,7 +360,9 @@ __device__ __forceinline__ void load_tiles(const C8Params& p, const C8Seq& q, ui
       entry = i < p.table_width ? ldg_i32(p.tables + (int64_t)q.s * p.table_stride + i) : -1;
     }
   };
-  auto fetch = [&](int32_t j) {
+  // Where the rows of tile j lie, and its scales (asked for; in registers a tile later).
+  const uint8_t* from[NR];
+  auto locate = [&](int32_t j) {
     const int32_t tok0 = lo + j * kKeys;
     if (PAGED16) {
       const int32_t tok = tok0 + 16 * (int32_t)(lane & 7u);
@@ -379,11 +381,7 @@ __device__ __forceinline__ void load_tiles(const C8Params& p, const C8Seq& q, ui
         int32_t ignore;
         off = place(tok0 + (int32_t)r, ignore);
       }
-      if (off >= 0 && (kKeys % RPI == 0 || r < kKeys)) {
-        const uint8_t* at = src + off + (PAGED16 ? row_off[i & 1] : 0);
-#pragma unroll
-        for (int g = 0; g < S::DG; ++g) x[i * S::DG + g] = ld_nc16(at + 64 * g);
-      }
+      from[i] = off >= 0 && (kKeys % RPI == 0 || r < kKeys) ? src + off + (PAGED16 ? row_off[i & 1] : 0) : nullptr;
     }
     if (!IS_K && PAGED16) {  // lane g & 7: run g
       ksc[0] = id >= 0 ? ldg_f32(p.k_scale + (int64_t)id * p.H + head) : 0.0f;
@@ -398,10 +396,15 @@ __device__ __forceinline__ void load_tiles(const C8Params& p, const C8Seq& q, ui
       vsc[i] = at >= 0 ? ldg_f32(p.v_scale + (int64_t)at * p.H + head) : 0.0f;
     }
   };
+  auto fetch = [&](int i) {  // chunk i of the tile located last
+    if (from[i / S::DG]) x[i] = ld_nc16(from[i / S::DG] + 64 * (i % S::DG));
+  };
   auto nan_of = [](uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; };
   ask(0);
-  if (n_steps > 0) fetch(0);
+  locate(0);
   ask(1);
+#pragma unroll
+  for (int i = 0; i < N; ++i) fetch(i);
   for (int32_t j = 0; j < n_steps; ++j) {
     const uint32_t st = j & 1, ph = (j >> 1) & 1;
     if (!IS_K) {
@@ -456,6 +459,8 @@ __device__ __forceinline__ void load_tiles(const C8Params& p, const C8Seq& q, ui
     if (!IS_K) mbar_arrive_warp(scales + 8 * (j & 3));
     if (!__all_sync(0xffffffffu, mbar_wait(empty + 8 * st, ph ^ 1u, stop))) break;
     uint8_t* tile = smem + (IS_K ? S::kK : S::kV) + st * S::kTile;
+    locate(j + 1);
+    ask(j + 2);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       uint4 h0, h1;
@@ -468,11 +473,10 @@ __device__ __forceinline__ void load_tiles(const C8Params& p, const C8Seq& q, ui
         *reinterpret_cast<uint4*>(at + dst0) = h0;
         *reinterpret_cast<uint4*>(at + dst1) = h1;
       }
+      fetch(i);  // the next tile's, while the others are converted
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     mbar_arrive_warp(full + 8 * st);
-    if (j + 1 < n_steps) fetch(j + 1);
-    ask(j + 2);
   }
   if (bad) c8_error(p, q.s, KV_CACHE8_BAD_PAGE);
 }
