@@ -55,41 +55,49 @@ __device__ __forceinline__ int32_t ldg_i32(const int32_t* p) {
   return (int32_t)ldg_u32(reinterpret_cast<const uint32_t*>(p));
 }
 
+// Row, count and length of sequence q.s from its cu_new pair and lens entry.
+__device__ __forceinline__ void c8_fill(const C8Params& p, C8Seq& q, int32_t c0, int32_t c1, int32_t len) {
+  q.row = (uint32_t)c0;
+  // rows past n_new are no memory of the caller's
+  q.n_new = c0 < 0 || (uint32_t)c0 > p.n_new || c1 < c0 ? 0 : min(c1 - c0, (int32_t)(p.n_new - (uint32_t)c0));
+  if (q.unit > 0x3fffffffu) q.n_new = 0;       // cu_new not ascending
+  q.len = min(max(0, len), 0x7fff0000);        // positions + a tile stay in 32 bits
+  q.start = q.len - q.n_new;
+}
+
 // The sequence of unit u: the last s with base(s) <= u, found by the whole warp
-// 32 probes at a time.  With per > 0, `per` units belong to each sequence.
+// 32 probes at a time; the last round's lanes hold what belongs to their sequence
+// already, so up to 32 sequences take one trip to memory.  With per > 0, `per` units
+// belong to each sequence.
 __device__ __forceinline__ C8Seq c8_find(const C8Params& p, uint32_t u, uint32_t w, uint32_t d, uint32_t x,
                                          uint32_t per) {
   C8Seq q;
-  uint32_t lo = 0;
   if (per) {
-    lo = u / per;
-    q.unit = u - lo * per;
-  } else {
-    const uint32_t lane = threadIdx.x & 31u;
-    uint32_t n = p.n_seqs;  // the answer is in [lo, lo + n)
-    while (n > 1u) {
-      const uint32_t step = (n + 31u) / 32u;
-      const uint32_t s = lo + lane * step;
-      const bool in = lane * step < n;
-      const bool le = in && c8_base((uint32_t)ldg_i32(p.cu + (in ? s : lo)), s, w, d, x) <= u;
-      const uint32_t k = 31u - (uint32_t)__clz(__ballot_sync(0xffffffffu, le || lane == 0u));
-      lo += k * step;
-      n = min(step, n - k * step);
-    }
-    q.unit = u - c8_base((uint32_t)ldg_i32(p.cu + lo), lo, w, d, x);
+    q.s = u / per;
+    q.unit = u - q.s * per;
+    const int32_t len = ldg_i32(p.lens + q.s);
+    if (p.cu) c8_fill(p, q, ldg_i32(p.cu + q.s), ldg_i32(p.cu + q.s + 1u), len);
+    else c8_fill(p, q, (int32_t)q.s, (int32_t)q.s + 1, len);
+    return q;
   }
-  q.s = lo;
-  q.row = lo;
-  q.n_new = 1;
-  if (p.cu) {
-    const int32_t c0 = ldg_i32(p.cu + lo), c1 = ldg_i32(p.cu + lo + 1u);
-    q.row = (uint32_t)c0;
-    // rows past n_new are no memory of the caller's
-    q.n_new = c0 < 0 || (uint32_t)c0 > p.n_new || c1 < c0 ? 0 : min(c1 - c0, (int32_t)(p.n_new - (uint32_t)c0));
+  const uint32_t lane = threadIdx.x & 31u;
+  uint32_t lo = 0, n = p.n_seqs;  // the answer is in [lo, lo + n)
+  while (n > 32u) {
+    const uint32_t step = (n + 31u) / 32u;
+    const uint32_t s = lo + lane * step;
+    const bool in = lane * step < n;
+    const bool le = in && c8_base((uint32_t)ldg_i32(p.cu + (in ? s : lo)), s, w, d, x) <= u;
+    const uint32_t k = 31u - (uint32_t)__clz(__ballot_sync(0xffffffffu, le || lane == 0u));
+    lo += k * step;
+    n = min(step, n - k * step);
   }
-  if (q.unit > 0x3fffffffu) q.n_new = 0;  // cu_new not ascending
-  q.len = min(max(0, ldg_i32(p.lens + lo)), 0x7fff0000);  // positions + a tile stay in 32 bits
-  q.start = q.len - q.n_new;
+  const uint32_t s = lo + min(lane, n - 1u);
+  const int32_t c0 = ldg_i32(p.cu + s), c1 = ldg_i32(p.cu + s + 1u), len = ldg_i32(p.lens + s);
+  const uint32_t base = c8_base((uint32_t)c0, s, w, d, x);
+  const uint32_t k = 31u - (uint32_t)__clz(__ballot_sync(0xffffffffu, (lane < n && base <= u) || lane == 0u));
+  q.s = lo + k;
+  q.unit = u - __shfl_sync(0xffffffffu, base, k);
+  c8_fill(p, q, __shfl_sync(0xffffffffu, c0, k), __shfl_sync(0xffffffffu, c1, k), __shfl_sync(0xffffffffu, len, k));
   return q;
 }
 
