@@ -109,18 +109,23 @@ struct Split {
   uint64_t ticket_bytes, bytes;
 };
 
-// Sequences of more than kStepMost rows (new tokens x query heads of a group) go to
-// the prompt kernel, the others to the step kernel.
-constexpr uint32_t kStepMost = 64;
+// Sequences of more than this many rows (new tokens x query heads of a group) go to
+// the prompt kernel, the others to the step kernel.  The prompt kernel is several times
+// faster when its CTAs (256 rows of a KV head) fill the GPU, but does not split keys: below
+// 16 of them it is the slower one (one sequence over 10240 tokens, 4 query heads to each of
+// 8 KV heads, D = 128: 20 new tokens 169 us against the step kernel's 33, 64 new 186 against 90).
+uint32_t step_most(const C8Params& p, const kv_cache8_batch* b) {
+  return (uint64_t)b->n_new * p.G / kvc::kPromptRows * p.H < 16u ? 512u : 64u;
+}
 
 bool has_prompts(const C8Params& p, const kv_cache8_batch* b) {
   if (!b->cu_new || p.D > 128) return false;
   const uint64_t most = b->max_new ? std::min(b->max_new, b->n_new) : b->n_new;
-  return most * p.G > kStepMost;
+  return most * p.G > step_most(p, b);
 }
 // A single sequence's count is the total.
 bool has_steps(const C8Params& p, const kv_cache8_batch* b) {
-  return !has_prompts(p, b) || b->n_seqs > 1 || (uint64_t)b->n_new * p.G <= kStepMost;
+  return !has_prompts(p, b) || b->n_seqs > 1 || (uint64_t)b->n_new * p.G <= step_most(p, b);
 }
 
 // Row tiles of the step kernel and the ranges their keys are split into, from the
@@ -128,8 +133,12 @@ bool has_steps(const C8Params& p, const kv_cache8_batch* b) {
 Split step_split(const C8Params& p, const kv_cache8_batch* b, uint32_t window) {
   Split s;
   const uint32_t tiles1 = (p.G + kvc::kStepRows - 1) / kvc::kStepRows;
-  s.per_seq = !b->cu_new ? tiles1 : has_prompts(p, b) ? kStepMost / kvc::kStepRows : 0u;
-  s.units = s.per_seq ? b->n_seqs * s.per_seq : (uint32_t)((uint64_t)b->n_new * p.G / kvc::kStepRows) + b->n_seqs;
+  s.per_seq = !b->cu_new ? tiles1 : has_prompts(p, b) ? step_most(p, b) / kvc::kStepRows : 0u;
+  s.units = s.per_seq ? b->n_seqs * s.per_seq : 0u;
+  if (b->cu_new) {  // found by cu_new where that leaves fewer units without rows
+    const uint32_t by_cu = (uint32_t)((uint64_t)b->n_new * p.G / kvc::kStepRows) + b->n_seqs;
+    if (!s.per_seq || by_cu < s.units) s.per_seq = 0u, s.units = by_cu;
+  }
   const uint64_t reach = std::min<uint64_t>((uint64_t)b->table_width * p.T, 0x7fff0000u);
   uint64_t keys = b->max_len ? std::min<uint64_t>(b->max_len, reach) : reach;
   if (window) keys = std::min<uint64_t>(keys, (uint64_t)window + kvc::kStepRows + 15u);
@@ -298,7 +307,7 @@ int kv_cache8_attend(kv_cache8_t h, const kv_cache8_layer* layer, const kv_cache
   if (sp.bytes && (!workspace || workspace_bytes < sp.bytes)) return KV_ERR_INVALID_ARG;
   if (prompts) {
     p.n_units = (uint32_t)((uint64_t)p.n_new * p.G / kvc::kPromptRows) + p.n_seqs;
-    p.min_rows = kStepMost + 1;
+    p.min_rows = step_most(p, batch) + 1;
     p.max_rows = 0xffffffffu;
     if ((rc = kvc::launch_c8_prompt(p, stream)) != KV_OK || !steps) return rc;
   }
@@ -309,7 +318,7 @@ int kv_cache8_attend(kv_cache8_t h, const kv_cache8_layer* layer, const kv_cache
   p.step_warps = sp.warps;
   p.rows8 = !p.cu && p.G <= 8 ? 1u : 0u;  // (a hint of few new tokens is not enough: counts are read on the device)
   p.min_rows = 1;
-  p.max_rows = prompts ? kStepMost : 0xffffffffu;
+  p.max_rows = prompts ? step_most(p, batch) : 0xffffffffu;
   p.tickets = static_cast<uint32_t*>(workspace);
   p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.ticket_bytes);
   return kvc::launch_c8_step(p, stream);

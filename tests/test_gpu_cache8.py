@@ -272,6 +272,56 @@ def test_bad_pages(T, op):
     assert errors.tolist() == [0, 1, 1, 1]
 
 
+@pytest.mark.parametrize("D,T,H,G,dtype", [(64, 32, 2, 8, "fp16"), (64, 16, 1, 64, "bf16"), (32, 5, 2, 40, "bf16"),
+                                           (128, 16, 4, 16, "fp16")])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 13), (False, 40)])
+def test_rows_on_both_sides_of_the_prompt_kernel_s_bound(D, T, H, G, dtype, causal, window):
+    """Sequences of a few rows up to thousands in one batch, whichever kernel takes each."""
+    lens = [100, 33, 300, 64, 0, 17, 256]
+    new = [64, 13, 100, 1, 0, 17, 8]
+    su = R.Setup(D=D, H=H, T=T, lens=lens, dtype=dtype, seed=G)
+    su.fill()
+    for hints in (True, False):
+        q, out, lse = _attend(su, lens, new, H * G, causal, window, hints=hints)
+        _check(su, lens, new, q, out, lse, causal, window)
+
+
+@pytest.mark.parametrize("new", [[80, 30, 64], [20, 17, 60]])
+def test_scores_of_every_size_with_many_heads(new):
+    """Page scales far apart and queries of tiny and huge magnitude, in sequences of more than 512 rows."""
+    lens = [90, 200, 64]
+    su = R.Setup(D=64, H=1, T=16, lens=lens, dtype="bf16", seed=5, spread=4.0)
+    su.fill()
+    q = su.queries(sum(new), 32).double()
+    q[:, 0:8] *= 1e-30
+    q[:, 8:16] *= 30.0
+    q[:, 16:24] *= 2.0 ** -7
+    q[:, 24] = 0.0
+    q = q.to(su.dtype)
+    for scale in (None, 0.37):
+        _, out, lse = _attend(su, lens, new, 32, q=q, scale=scale)
+        _check(su, lens, new, q, out, lse, scale=scale)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_nan_reaches_only_the_rows_that_see_it_with_many_heads(D):
+    test_nan_reaches_only_the_rows_that_see_it(D, 32, [40, 64])
+
+
+@pytest.mark.parametrize("T", [16, 24])
+def test_bad_pages_with_many_heads(T):
+    """Prompts of 960 rows whose tables hold no page, or end before the tokens."""
+    lens, new = [60, 60, 60, 300], [60, 60, 60, 60]
+    su = R.Setup(D=64, H=2, T=T, lens=[60, 60, 60, 60], dtype="fp16", seed=2)
+    su.fill()
+    su.tables[1, 1] = su.pages
+    su.tables[2, 0] = -5
+    errors = torch.zeros(4, dtype=torch.int32, device=DEV)
+    q, out, lse = _attend(su, lens, new, 32, errors=errors)
+    _check(su, lens, new, q, out, lse)
+    assert errors.tolist() == [0, 1, 1, 1]
+
+
 def test_rows_past_the_caller_s_count_are_not_touched():
     """cu_new that promises more rows than n_new: the surplus is not read or written."""
     su = R.Setup(D=32, H=1, T=16, lens=[32, 32], dtype="fp16")
