@@ -593,8 +593,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
     mbar_arrive_warp(q_full);
   }
 
-  // Registers: 512 threads start with 128 each; the softmax takes 176 (a row's 128
-  // scores at once), the others keep 80: 256 x 176 + 256 x 80 = 512 x 128.
+  // Registers: 512 threads start with 128 each; the softmax takes 176 (two chunks of 32 scores
+  // and their weights under way), the others keep 80: 256 x 176 + 256 x 80 = 512 x 128.
+  // The split is made for whole warpgroups, each at one place: warps 12 .. 15, of two
+  // roles, are one.
   static_assert(kPromptThreads == 512 && kSoftWarps == 8, "");
   if (warp < kSoftWarps) {
     // ================================================================ softmax
@@ -779,17 +781,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
               __float_as_uint(l == 0.0f ? kNegInf : (m + log2f(l)) * 0.693147180559945309f));
       }
     }
-  } else if (warp < kMmaWarp) {
-    // ================================================================ codes to FP16 tiles
-    regs_dec();
-    if (warp < kSoftWarps + kVWarps)
-      load_tiles<D, PAGED16, false, kVWarps>(p, q, smem, head, lo, hi, n_steps, v_full, v_empty, c_full, stop, nan_seen);
-    else
-      load_tiles<D, PAGED16, true, kKWarps>(p, q, smem, head, lo, hi, n_steps, k_full, k_empty, 0u, stop, nan_seen);
   } else {
-    // ================================================================ products
     regs_dec();
-    if (n_steps > 0) {
+    if (warp < kSoftWarps + kVWarps) {
+    // ================================================================ codes to FP16 tiles
+      load_tiles<D, PAGED16, false, kVWarps>(p, q, smem, head, lo, hi, n_steps, v_full, v_empty, c_full, stop, nan_seen);
+    } else if (warp < kMmaWarp) {
+      load_tiles<D, PAGED16, true, kKWarps>(p, q, smem, head, lo, hi, n_steps, k_full, k_empty, 0u, stop, nan_seen);
+    } else if (n_steps > 0) {
+    // ================================================================ products
     // The whole warp walks, one lane issues: what the instructions take is uniform.
     // (All 512 columns are allocated, so TMEM starts at column 0.)
     const bool one = elect_one();

@@ -161,3 +161,18 @@ def test_reference_codes_match_the_format():
 def test_reference_exponent():
     for a, e in ((0.0, -60), (448.0, 0), (448.0001, 1), (224.0, -1), (1e-30, -60), (3e38, 119), (65504.0, 8)):
         assert R.page_exponent(a) == e
+
+
+# ---- what a warpgroup has to do as one
+def test_the_register_split_is_made_once_for_each_warpgroup():
+    """setmaxnreg: all warps of a warpgroup execute the same instruction, so no two roles of one have calls of their own."""
+    text = open(os.path.join(ROOT, "kv_cache_page_gb300", "csrc", "cache8_prompt.cu")).read()
+    kernel = text[text.index("c8_prompt_kernel(const __grid_constant__"):]
+    for call in ("regs_inc();", "regs_dec();"):
+        assert kernel.count(call) == 1, call
+    # the split falls between warpgroups: warps 0 .. 7 take more, 8 .. 15 keep less, and the shares add up to the launch's
+    warps = {n: int(v) for n, v in re.findall(r"(kSoftWarps|kVWarps|kKWarps) = (\d+)", text)}
+    more, less = (int(re.search(r"setmaxnreg\.%s\.sync\.aligned\.u32 (\d+);" % d, text).group(1)) for d in ("inc", "dec"))
+    soft, rest = warps["kSoftWarps"], warps["kVWarps"] + warps["kKWarps"] + 1
+    assert soft % 4 == 0 and rest % 4 == 0
+    assert 32 * (soft * more + rest * less) <= 32 * (soft + rest) * 128
