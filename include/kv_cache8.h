@@ -145,8 +145,9 @@ int kv_cache8_read(kv_cache8_t cache, const kv_cache8_layer* layer, const kv_cac
  *   scale      0 selects 1 / sqrt(head_dim); otherwise finite and positive
  *   workspace  workspace_bytes >= kv_cache8_attend_workspace(...) bytes of device
  *              memory, 16-byte aligned, ZERO-FILLED before its first use (each
- *              call leaves it fit for the next); calls that may run at the same
- *              time need workspaces of their own.  NULL when 0 bytes are wanted.
+ *              call leaves it fit for the next, whatever batch or cache that is
+ *              for); calls that may run at the same time need workspaces of
+ *              their own.  NULL when 0 bytes are wanted.
  * Products accumulate in FP32; the weights of V are rounded to FP16 (2^-11 of
  * each, below the rounding of the outputs; weights under 2^-25 of the row's largest
  * to 2^-36 of that); maxima, sums and the joining of split ranges are FP32.  The result does not depend on timing. */

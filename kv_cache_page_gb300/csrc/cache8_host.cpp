@@ -106,7 +106,7 @@ uint32_t page_units(const C8Params& p) {
 
 struct Split {
   uint32_t units, per_seq, splits, chunk, warps;
-  uint64_t ticket_bytes, bytes;
+  uint64_t bytes;
 };
 
 // Sequences of more than this many rows (new tokens x query heads of a group) go to
@@ -165,10 +165,11 @@ Split step_split(const C8Params& p, const kv_cache8_batch* b, uint32_t window) {
   }
   chunk = (chunk + 31u) & ~31ull;
   s.splits = (uint32_t)std::min<uint64_t>((keys + chunk - 1) / chunk, kvc::kMaxSplits);
+  // (jobs are below 2 x 456 where there is more than one range, and units at most four times as many)
+  if (all > kvc::kTickets) s.splits = 1u;
   if (window) s.splits = std::min(s.splits, step_split(p, b, 0).splits);  // the workspace is sized without one
   s.chunk = (uint32_t)chunk;
-  s.ticket_bytes = s.splits > 1 ? (all * 4u + 255u) & ~255ull : 0u;
-  s.bytes = s.splits > 1 ? s.ticket_bytes + all * s.splits * (kvc::kStepRows * (p.D + 2ull) * 4u) : 0u;
+  s.bytes = s.splits > 1 ? kvc::kTickets * 4u + all * s.splits * (kvc::kStepRows * (p.D + 2ull) * 4u) : 0u;
   return s;
 }
 
@@ -319,8 +320,10 @@ int kv_cache8_attend(kv_cache8_t h, const kv_cache8_layer* layer, const kv_cache
   p.rows8 = !p.cu && p.G <= 8 ? 1u : 0u;  // (a hint of few new tokens is not enough: counts are read on the device)
   p.min_rows = 1;
   p.max_rows = prompts ? step_most(p, batch) : 0xffffffffu;
-  p.tickets = static_cast<uint32_t*>(workspace);
-  p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sp.ticket_bytes);
+  if (sp.bytes) {
+    p.tickets = static_cast<uint32_t*>(workspace);
+    p.partials = reinterpret_cast<float*>(p.tickets + kvc::kTickets);
+  }
   return kvc::launch_c8_step(p, stream);
 }
 

@@ -14,6 +14,9 @@ constexpr uint32_t kC8Sms = 152;  // SMs of a GB300: what the split rules count 
 constexpr uint32_t kStepRows = 16;
 constexpr uint32_t kMaxSplits = 256;  // ranges of a row tile's keys (the joining CTA holds 8 bytes a range and row)
 constexpr uint32_t kPromptRows = 256;
+// Row tiles (times KV heads) whose keys may be split, of one call.  Their tickets take this much of every
+// workspace whatever the batch, so that what a call leaves behind them is never another call's ticket.
+constexpr uint32_t kTickets = 4096;
 
 struct C8Params {
   // ---- registered geometry ----
@@ -51,7 +54,7 @@ struct C8Params {
   uint32_t both_roles;          // write, read: a warp takes K and V of its page and head
   uint32_t per_seq;             // step: units of a sequence, 0: by cu_new
   uint32_t n_units;             // row tiles (step, prompt) or page units (write, read), an upper bound
-  uint32_t* tickets;            // [n_units][H]
+  uint32_t* tickets;            // [kTickets], of which [n_units][H] are used; 0 between calls
   float* partials;              // [n_units][H][splits][kStepRows][D + 2]
 };
 

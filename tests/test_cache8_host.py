@@ -107,6 +107,23 @@ def test_workspace_sizes():
     assert _workspace(c, _batch(max_len=0))[1] == _workspace(c, _batch(max_len=80 * 16))[1]
 
 
+def test_workspace_tickets_take_the_same_place_for_every_batch():
+    """What is left of a workspace's bytes once the partial results are taken off does not depend on the batch."""
+    left = set()
+    for D, H, HQ in ((128, 8, 32), (64, 1, 7), (256, 4, 4), (32, 2, 128)):
+        c = cache8.Cache8(**_kw(head_dim=D, num_kv_heads=H, num_q_heads=HQ, num_blocks=1 << 20))
+        for n in list(range(1, 130)) + [200, 400, 700]:
+            for cu in (0, 64):
+                for new in ((1,) if not cu else (1, 5, 300, 4000)):
+                    b = _batch(n_seqs=n, n_new=n * new, max_new=new, max_len=65536, table_width=4096, table_stride=4096,
+                               cu_new=cu)
+                    rc, total = _workspace(c, b)
+                    assert rc == 0
+                    if total:
+                        left.add(total % (16 * (D + 2) * 4) - 16384 % (16 * (D + 2) * 4))
+    assert left == {0}
+
+
 def test_null_arguments():
     L, n = cache8.lib(), C.c_uint64()
     c = cache8.Cache8(**_kw())

@@ -1,0 +1,62 @@
+"""The live 8-bit cache on the GPU at the borders of what it admits."""
+import pytest
+import torch
+
+from kv_cache_page_gb300 import cache8
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+class _Random:
+    """A cache of random codes whose pages the sequences of any batch share (attention reads alone)."""
+
+    def __init__(self, *, H, G, D, T, most_len, seed, dtype="bf16"):
+        self.g = torch.Generator(device=DEV).manual_seed(seed)
+        self.H, self.HQ, self.D, self.T, self.pages = H, H * G, D, T, 300
+        self.width = -(-most_len // T)
+        self.dtype = torch.bfloat16 if dtype == "bf16" else torch.float16
+        self.cache = cache8.Cache8(dtype=dtype, head_dim=D, num_kv_heads=H, num_q_heads=self.HQ, block_tokens=T,
+                                   num_blocks=self.pages)
+        codes = [torch.randint(0, 126, (self.pages, T, H, D), generator=self.g, dtype=torch.uint8, device=DEV)
+                 for _ in range(2)]
+        self.layer = cache8.Layer(*codes, *(torch.full((self.pages, H), 2.0 ** -7, device=DEV) for _ in range(2)))
+
+    def batch(self, lens, new=None):
+        n = len(lens)
+        tables = torch.randint(0, self.pages, (n, self.width), generator=self.g, dtype=torch.int32, device=DEV)
+        cu = None
+        if new is not None:
+            cu = torch.tensor([0] + torch.tensor(new).cumsum(0).tolist(), dtype=torch.int32, device=DEV)
+        return cache8.Batch(tables, torch.tensor(lens, dtype=torch.int32, device=DEV), cu,
+                            n_new=sum(new) if new is not None else n, max_new=max(new) if new is not None else 1,
+                            max_len=max(lens))
+
+    def attend(self, batch, workspace):
+        q = torch.randn(batch.n_new, self.HQ, self.D, generator=torch.Generator(device=DEV).manual_seed(batch.n_new),
+                        device=DEV).to(self.dtype)
+        out, lse = torch.full_like(q, 9.0), torch.full((batch.n_new, self.HQ), 9.0, device=DEV)
+        self.cache.attend(self.layer, batch, q, out, lse=lse, workspace=workspace)
+        return out, lse
+
+
+def test_one_workspace_for_batches_of_every_size():
+    """Zero-filled once: sequences come and go, prompts join, and another cache uses it; every call gives what a
+    workspace of its own gives."""
+    a = _Random(H=8, G=4, D=64, T=16, most_len=8192, seed=1)
+    b = _Random(H=2, G=7, D=128, T=16, most_len=8192, seed=2, dtype="fp16")
+    c = _Random(H=1, G=4, D=256, T=5, most_len=1500, seed=3)
+    steps = [(a, [8192 - 7 * s for s in range(n)], None) for n in (4, 8, 9, 64, 9, 33)]
+    steps += [(a, [3000, 900, 8192, 5000, 77], [700, 1, 1, 20, 3]), steps[3]]
+    steps += [(b, [8000, 5000], None), (b, [6000] * 40, None), (c, [1500, 700], [300, 4]), steps[1], steps[5],
+              (b, [8192] * 12, [1, 5] * 6), steps[3]]
+    calls = [(x, x.batch(lens, new)) for x, lens, new in steps]
+    sizes = [x.cache.attend_workspace(batch) for x, batch in calls]
+    assert min(sizes) > 0
+    shared = torch.zeros(max(sizes), dtype=torch.uint8, device=DEV)
+    for i, (x, batch) in enumerate(calls):
+        own = torch.zeros(sizes[i], dtype=torch.uint8, device=DEV)
+        want, got = x.attend(batch, own), x.attend(batch, shared)
+        for w, g in zip(want, got):
+            assert torch.equal(w, g), i
+        assert not bool((want[0] == 9.0).all(-1).any()), i
