@@ -148,9 +148,13 @@ int kv_cache8_read(kv_cache8_t cache, const kv_cache8_layer* layer, const kv_cac
  *              call leaves it fit for the next, whatever batch or cache that is
  *              for); calls that may run at the same time need workspaces of
  *              their own.  NULL when 0 bytes are wanted.
- * Products accumulate in FP32; the weights of V are rounded to FP16 (2^-11 of
- * each, below the rounding of the outputs; weights under 2^-25 of the row's largest
- * to 2^-36 of that); maxima, sums and the joining of split ranges are FP32.  The result does not depend on timing. */
+ * Products accumulate in FP32; maxima, sums and the joining of split ranges are
+ * FP32, and the sum (lse) knows nothing of V.  The weights of V times its pages'
+ * scales are rounded to FP16: by 2^-11 of each at most, as much as the rounding of an
+ * FP16 output; those below 2^-25 of the row's largest weight times the largest scale
+ * of V that it sees, by 2^-36 of that.  (So where a page's scale is 2^25 times
+ * another's, the small page's part of an output is held to 2^-36 of what the large
+ * page could give.)  The result does not depend on timing. */
 int kv_cache8_attend(kv_cache8_t cache, const kv_cache8_layer* layer, const kv_cache8_batch* batch,
                      const kv_cache8_rows* q, const kv_cache8_rows* out, float* lse, float scale,
                      uint32_t window, uint32_t flags, void* workspace, uint64_t workspace_bytes,

@@ -37,6 +37,10 @@ constexpr float kNegInf = -INFINITY;
 // Weights are held as 2^(z - m) * 2^11, m at most kLag below the true maximum (as
 // the step kernel holds them).
 constexpr float kLift = 11.0f, kLag = 4.0f;  // kLift: the logarithm
+// The logarithm of V's scale in a weight's exponent, relative to the row's reference, is held at this at least:
+// such weights, at most 2^(kLag + kFarV), are 0 in FP16 either way, and the sum gets them back whole (of a page of
+// zeros, scale 2^-60, next to one of 2^100 they would leave FP32's range).
+constexpr float kFarV = -40.0f;
 constexpr int kKeys = 128;           // keys of a tile
 constexpr int kSoftWarps = 8, kVWarps = 4, kKWarps = 3, kMmaWarp = kSoftWarps + kKWarps + kVWarps;
 constexpr int kPromptThreads = (kMmaWarp + 1) * 32;
@@ -57,6 +61,12 @@ __device__ __forceinline__ float lg2(float x) {
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// at least kFarV; NaN stays NaN
+__device__ __forceinline__ float far_v(float x) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(kFarV));
   return y;
 }
 
@@ -269,13 +279,14 @@ __device__ __forceinline__ float row_weights(uint32_t s_at, const float* ks, con
       float kk[4], ll[4];
       if (PAGED16) {
         kk[0] = kk[1] = kk[2] = kk[3] = f8[col / 16];
-        ll[0] = ll[1] = ll[2] = ll[3] = l8[col / 16] + lref;
+        ll[0] = ll[1] = ll[2] = ll[3] = far_v(l8[col / 16] + lref);
         // a page that the row sees nothing of: its scale must not matter
         if (MASK && (col >= hi_c || col + 16 <= lo_c)) ll[0] = ll[1] = ll[2] = ll[3] = 0.0f;
       } else {
         const float4 k = *reinterpret_cast<const float4*>(ks + col), l = *reinterpret_cast<const float4*>(lv + col);
         kk[0] = k.x; kk[1] = k.y; kk[2] = k.z; kk[3] = k.w;
-        ll[0] = l.x + lref; ll[1] = l.y + lref; ll[2] = l.z + lref; ll[3] = l.w + lref;
+        ll[0] = far_v(l.x + lref); ll[1] = far_v(l.y + lref);
+        ll[2] = far_v(l.z + lref); ll[3] = far_v(l.w + lref);
       }
       float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll

@@ -2,7 +2,9 @@
 import pytest
 import torch
 
+import cache8_ref as R
 from kv_cache_page_gb300 import cache8
+from test_gpu_cache8 import _attend, _check
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -60,3 +62,29 @@ def test_one_workspace_for_batches_of_every_size():
         for w, g in zip(want, got):
             assert torch.equal(w, g), i
         assert not bool((want[0] == 9.0).all(-1).any()), i
+
+
+def _fill_pages(su, k_of, v_of):
+    """Every sequence's pages from values(n) times a factor of the page: k_of(i), v_of(i) for page i of a sequence."""
+    for s, n in enumerate(su.lens):
+        if n:
+            fk, fv = (torch.tensor([f(t // su.T) for t in range(n)], dtype=torch.float64)[:, None, None]
+                      for f in (k_of, v_of))
+            k, v = (su.values(n).double() * f for f in (fk, fv))
+            su.ref.write(su.tables[s], 0, (k.to(su.dtype), v.to(su.dtype)))
+
+
+V_FACTORS = [[0.0, 1.0, 2.0 ** 70], [1.0, 0.0, 2.0 ** 100], [2.0 ** 119, 0.0, 0.0, 2.0 ** 80], [0.0, 2.0 ** 79], [0.0, 0.0, 2.0 ** 60]]
+
+
+@pytest.mark.parametrize("T", [16, 24])
+@pytest.mark.parametrize("factors", V_FACTORS)
+@pytest.mark.parametrize("new", [None, [3, 9, 1], [80, 30, 64]])
+def test_v_scales_far_apart(T, factors, new):
+    """Zero pages (scale 2^-60) next to pages of very large values: the sum of the weights knows no scale of V."""
+    lens = [90, 200, 64]
+    su = R.Setup(D=64, H=1, T=T, lens=lens, dtype="bf16", seed=T)
+    _fill_pages(su, lambda i: 0.25, lambda i: factors[i % len(factors)])
+    for window in (0, 50):
+        q, out, lse = _attend(su, lens, new, 32, window=window)
+        _check(su, lens, new, q, out, lse, window=window)
