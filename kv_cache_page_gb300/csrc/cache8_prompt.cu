@@ -209,8 +209,9 @@ struct PromptShape {
 // a time, the next on their way: holding all 128 left the compiler too few registers
 // to overlap anything); K's and V's scales, of whole pages per 16 tokens, else per
 // token; rf the row's factor; z = x k rf.  MASK: only
-// columns [lo_c, hi_c) are seen, and of these none whose K scale is 0 (a token
-// without a page).
+// columns [lo_c, hi_c) are seen, and of these none without a page: of whole pages
+// their factor is -1 (a page's own may be 0, where scale and row are tiny), else their
+// K scale is 0.
 template <bool PAGED16, bool MASK>
 __device__ __forceinline__ float row_max(uint32_t s_at, const float* ks, const float (&f8)[8], float rf, int32_t lo_c,
                                          int32_t hi_c) {
@@ -225,7 +226,7 @@ __device__ __forceinline__ float row_max(uint32_t s_at, const float* ks, const f
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         const float f = f8[2 * c + g];
-        const int32_t hg = MASK && f == 0.0f ? -1 : hi_c;
+        const int32_t hg = MASK && f < 0.0f ? -1 : hi_c;
         float y[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -236,7 +237,7 @@ __device__ __forceinline__ float row_max(uint32_t s_at, const float* ks, const f
 #pragma unroll
         for (int i = 0; i < 5; ++i) y[i] = max3(y[3 * i], y[3 * i + 1], y[3 * i + 2]);
         y[0] = fmaxf(max3(y[0], y[1], y[2]), max3(y[3], y[4], y[15]));
-        mt = fmaxf(mt, __fmul_rn(y[0], f));  // (a hole: -inf * 0, which the maximum leaves out)
+        mt = fmaxf(mt, __fmul_rn(y[0], MASK ? fabsf(f) : f));  // (-inf * 0 is NaN, which the maximum leaves out)
       }
     } else {
 #pragma unroll
@@ -301,8 +302,8 @@ __device__ __forceinline__ float row_weights(uint32_t s_at, const float* ks, con
         else
           z = fma2(xx, f, make_float2(ll[e & 3] - base, ll[(e + 1) & 3] - base));
         if (MASK) {
-          z.x = col + e < hi_c && col + e >= lo_c && k0 != 0.0f ? z.x : kNegInf;
-          z.y = col + e + 1 < hi_c && col + e + 1 >= lo_c && k1 != 0.0f ? z.y : kNegInf;
+          z.x = col + e < hi_c && col + e >= lo_c && (PAGED16 ? !(k0 < 0.0f) : k0 != 0.0f) ? z.x : kNegInf;
+          z.y = col + e + 1 < hi_c && col + e + 1 >= lo_c && (PAGED16 ? !(k1 < 0.0f) : k1 != 0.0f) ? z.y : kNegInf;
         }
         const float2 y = make_float2(ex2(z.x), ex2(z.y));
         if (PAGED16) {
@@ -667,7 +668,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
         }
         // columns [lo_c, hi_c) of the tile are seen
         const int32_t hi_c = vis_hi - tok0, lo_c = vis_lo - tok0;
-        // (whole pages) K's scale times the row's factor, V's scale as a logarithm
+        // (whole pages) K's scale times the row's factor, -1 without a page; V's scale as a logarithm
         float f8[8], l8[8];
         if (PAGED16) {
 #pragma unroll
@@ -675,6 +676,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
             const float4 k = *reinterpret_cast<const float4*>(ks + g), v = *reinterpret_cast<const float4*>(vs + kKeys + g);
             f8[g] = __fmul_rn(k.x, rf); f8[g + 1] = __fmul_rn(k.y, rf);
             f8[g + 2] = __fmul_rn(k.z, rf); f8[g + 3] = __fmul_rn(k.w, rf);
+            if (hole) {
+              f8[g] = k.x == 0.0f ? -1.0f : f8[g]; f8[g + 1] = k.y == 0.0f ? -1.0f : f8[g + 1];
+              f8[g + 2] = k.z == 0.0f ? -1.0f : f8[g + 2]; f8[g + 3] = k.w == 0.0f ? -1.0f : f8[g + 3];
+            }
             l8[g] = v.x; l8[g + 1] = v.y; l8[g + 2] = v.z; l8[g + 3] = v.w;
           }
         }

@@ -88,3 +88,20 @@ def test_v_scales_far_apart(T, factors, new):
     for window in (0, 50):
         q, out, lse = _attend(su, lens, new, 32, window=window)
         _check(su, lens, new, q, out, lse, window=window)
+
+
+@pytest.mark.parametrize("T", [16, 24])
+@pytest.mark.parametrize("new", [None, [3, 9, 1], [80, 30, 64]])
+@pytest.mark.parametrize("which", [2, 1])
+def test_zero_keys_under_tiny_queries_are_keys(T, new, which):
+    """Pages of zero keys (scale 2^-60) and query rows of 1e-30: the products of the factors leave FP32's range, the
+    keys still count.  which: one page of `which` holds zeros."""
+    lens = [90, 200, 64]
+    su = R.Setup(D=64, H=1, T=T, lens=lens, dtype="bf16", seed=4)
+    _fill_pages(su, lambda i: 0.0 if i % which == 0 else 1.0, lambda i: 1.0)
+    q = su.queries(sum(new) if new else 3, 32).double()
+    q[:, 8:24] *= 1e-30
+    q = q.to(su.dtype)
+    for window in (0, 50):
+        _, out, lse = _attend(su, lens, new, 32, window=window, q=q)
+        _check(su, lens, new, q, out, lse, window=window)
