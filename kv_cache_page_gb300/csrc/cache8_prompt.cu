@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
   const int32_t first_pos = q.start + (int32_t)(r0 / p.G), last_pos = q.start + (int32_t)((r0 + n_rows - 1u) / p.G);
   const int32_t hi = max(p.causal ? min(q.len, last_pos + 1) : q.len, 0);
   int32_t lo = p.window && first_pos >= 0 ? max(0, first_pos - (int32_t)min(p.window, 0x7fffffffu) + 1) : 0;
-  lo &= ~15;
+  if (PAGED16) lo &= ~15;  // runs of 16 tokens; else the page of a token before may be freed
   const int32_t n_steps = hi > lo ? (hi - lo + kKeys - 1) / kKeys : 0;
 
   // barriers

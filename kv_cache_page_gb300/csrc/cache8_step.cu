@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
   const int32_t first_pos = q.start + (int32_t)(r0 / p.G), last_pos = q.start + (int32_t)((r0 + n_rows - 1u) / p.G);
   const int32_t hi = max(p.causal ? min(q.len, last_pos + 1) : q.len, 0);
   int32_t lo = p.window && first_pos >= 0 ? max(0, first_pos - (int32_t)min(p.window, 0x7fffffffu) + 1) : 0;
-  lo &= ~15;  // tiles start at multiples of 16
+  if (PAGED16) lo &= ~15;  // a page's tiles start at multiples of 16; else the page of a token before may be freed
   const uint32_t keys = hi > lo ? (uint32_t)(hi - lo) : 0u;
   // ranges: p.chunk keys each, longer where p.splits of them would not reach
   uint32_t chunk = p.chunk;

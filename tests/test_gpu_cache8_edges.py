@@ -105,3 +105,20 @@ def test_zero_keys_under_tiny_queries_are_keys(T, new, which):
     for window in (0, 50):
         _, out, lse = _attend(su, lens, new, 32, window=window, q=q)
         _check(su, lens, new, q, out, lse, window=window)
+
+
+@pytest.mark.parametrize("T", [1, 5, 16, 24, 48])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("new", [None, [3, 1, 9, 2], [70, 33, 40, 64]])
+def test_pages_freed_behind_the_window(T, causal, new):
+    """Table entries of pages that no query of the batch sees are not looked at: no error, the same outputs."""
+    lens, window = [300, 121, 90, 177], 20
+    su = R.Setup(D=64, H=1, T=T, lens=lens, dtype="fp16", seed=T)
+    su.fill()
+    for s, n in enumerate(lens):
+        first = n - (new[s] if new else 1) - window + 1
+        su.tables[s, :max(0, first) // T] = -1
+    errors = torch.zeros(4, dtype=torch.int32, device=DEV)
+    q, out, lse = _attend(su, lens, new, 32, causal=causal, window=window, errors=errors)
+    _check(su, lens, new, q, out, lse, causal=causal, window=window)
+    assert errors.tolist() == [0, 0, 0, 0]
