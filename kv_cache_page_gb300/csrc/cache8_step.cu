@@ -38,6 +38,9 @@ constexpr float kNegInf = -INFINITY;
 // 2^-36 of it.  m may lag the true maximum by kLag (fewer rescalings of the sums):
 // 2^(11 + kLag) = 2^15 < 65504.
 constexpr float kLift = 2048.0f, kLag = 4.0f;
+// Sums of weights times V that warps and ranges join are held 2^-24 times as large: with V next to 2^128 they
+// would leave FP32's range before they are normalised (2^20 keys, each weight up to 2^kLag, still fit).
+constexpr float kJoin = 16777216.0f;
 
 // A barrier of the CTA that counts threads, whether or not their warp is
 // converged (__syncthreads() asks for converged warps, and the branches here on
@@ -663,7 +666,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
   // ---- join the warps: every row to the largest maximum among them
   float* s_m = s_row + 16;               // [row][warp] maxima
   float* s_l = s_m + 16 * W;             // [row][warp] sums, at the row's maximum
-  float2* s_fin = reinterpret_cast<float2*>(smem);  // row: maximum and 1 / sum, over Q once no warp needs that
+  float2* s_fin = reinterpret_cast<float2*>(smem);  // row: maximum and kJoin / sum, over Q once no warp needs that
   float* s_o = reinterpret_cast<float*>(smem + S::kQ + S::kSmall);  // [warp][16][D + 4], over the slots
   static_assert((16 + 32 * W) * 4 + 128 <= S::kSmall, "");
   constexpr int OS = D + 4;
@@ -680,7 +683,7 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
 #pragma unroll
     for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_m[row * W + w]);
     const float f = m[r] == kNegInf ? 0.0f : ex2(m[r] - mx);
-    const float fo = m[r] == kNegInf ? 0.0f : f * (vref[r] * (1.0f / kLift));
+    const float fo = m[r] == kNegInf ? 0.0f : f * (vref[r] * (1.0f / (kLift * kJoin)));
     if (holder) s_l[row * W + warp] = l[r] * f;
     float* dst = s_o + (warp * 16 + row) * OS;
     if (N8) {  // tile n: dims 16 n + g, + 8 of the lane's rows
@@ -699,9 +702,9 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
   const uint32_t job = u * p.H + head;
   float* base = p.partials + (uint64_t)job * p.splits * (kStepRows * (D + 2));
   float* mine = base + (uint64_t)split * (kStepRows * (D + 2));
-  // a row's maximum and sum: to the outputs, or to the range's record
+  // a row's maximum and sum: the factor of its outputs, and lse
   auto finish_row = [&](uint32_t row, float mx, float ls) {
-    s_fin[row] = make_float2(mx, ls == 0.0f ? 0.0f : 1.0f / ls);
+    s_fin[row] = make_float2(mx, ls == 0.0f ? 0.0f : kJoin / ls);
     if (p.lse && row < n_rows) {
       const uint32_t rr = r0 + row, tok = rr / p.G, hd = head * p.G + rr - tok * p.G;
       st4(p.lse + ((int64_t)q.row + tok) * p.HQ + hd,

@@ -122,3 +122,18 @@ def test_pages_freed_behind_the_window(T, causal, new):
     q, out, lse = _attend(su, lens, new, 32, causal=causal, window=window, errors=errors)
     _check(su, lens, new, q, out, lse, causal=causal, window=window)
     assert errors.tolist() == [0, 0, 0, 0]
+
+
+@pytest.mark.parametrize("T,G", [(16, 4), (24, 4), (16, 32)])
+@pytest.mark.parametrize("new", [None, [3, 9], [80, 64]])
+def test_values_next_to_the_largest(T, G, new):
+    """V of 2^124: outputs are as large, sums over the keys before they are normalised would be infinite."""
+    lens = [150, 1400]
+    su = R.Setup(D=64, H=1, T=T, lens=lens, dtype="bf16", seed=7, spread=0.0)
+    _fill_pages(su, lambda i: 0.01, lambda i: 2.0 ** 124)
+    for s, n in enumerate(lens):  # one sign, so that they add up
+        for pid in su.tables[s, :-(-n // T)].tolist():
+            su.ref.codes[1][pid] &= 0x7F
+    q, out, lse = _attend(su, lens, new, G)
+    _check(su, lens, new, q, out, lse)
+    assert float(out.max()) > 2.0 ** 123
