@@ -22,6 +22,7 @@ from .codec import KvCodecError  # noqa: F401  (what the calls raise)
 ABI_VERSION = 1
 BAD_PAGE = 1
 CAUSAL = 1
+_MAX_WINDOW = 0xffffffff  # positions are below 2^31: all of any sequence
 EXPORTS = ("kv_cache8_create", "kv_cache8_destroy", "kv_cache8_write", "kv_cache8_read", "kv_cache8_attend",
            "kv_cache8_attend_workspace", "kv_cache8_abi_version")
 _DTYPES = {"fp16": torch.float16, "bf16": torch.bfloat16}
@@ -214,9 +215,9 @@ class Cache8:
                causal: bool = True, window: int = 0, workspace=None, stream=None):
         """Attention of the new tokens' queries (q, out: [n_new, num_q_heads, head_dim])
         over their sequences; lse (float32 [n_new, num_q_heads]): the scores' log-sum-exp.
-        A row that sees no key gets out = 0, lse = -inf.  workspace: a CUDA tensor of
-        ``attend_workspace(batch)`` bytes, zero-filled before its first use, not
-        shared by calls that may run at the same time."""
+        A row that sees no key gets out = 0, lse = -inf.  workspace: a CUDA tensor of at
+        least ``attend_workspace(batch)`` bytes, zero-filled before its first use, then good
+        for any batch or cache, not shared by calls that may run at the same time."""
         qr, outr = self._rows(q, batch, self.num_q_heads, "q"), self._rows(out, batch, self.num_q_heads, "out")
         at = None
         if lse is not None:
@@ -226,10 +227,11 @@ class Cache8:
             at = lse.data_ptr()
         if scale is None:
             scale = 0.0
-        elif not (scale > 0 and math.isfinite(scale)):
-            raise ValueError("scale must be finite and positive")
+        elif not (scale > 0 and math.isfinite(C.c_float(scale).value) and C.c_float(scale).value > 0):
+            raise ValueError("scale must be finite and positive in float32")  # (0 would stand for the default)
         if window < 0:
             raise ValueError("window must not be negative")
+        window = min(window, _MAX_WINDOW)
         ws, nb = None, 0
         if workspace is not None:
             if not workspace.is_cuda or not workspace.is_contiguous():

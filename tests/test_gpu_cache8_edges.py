@@ -1,4 +1,6 @@
 """The live 8-bit cache on the GPU at the borders of what it admits."""
+import math
+
 import pytest
 import torch
 
@@ -137,3 +139,16 @@ def test_values_next_to_the_largest(T, G, new):
     q, out, lse = _attend(su, lens, new, G)
     _check(su, lens, new, q, out, lse)
     assert float(out.max()) > 2.0 ** 123
+
+
+def test_arguments_that_do_not_fit_the_c_types():
+    su = R.Setup(D=64, H=2, T=16, lens=[100], dtype="fp16")
+    su.fill()
+    for scale in (1e-60, 1e-300, 1e60):   # would become 0, which stands for 1 / sqrt(head_dim), or infinite
+        with pytest.raises(ValueError):
+            _attend(su, [100], None, 4, scale=scale)
+    q, out, lse = _attend(su, [100], None, 4)
+    for window in (2 ** 31, 2 ** 32 - 1, 2 ** 32, 2 ** 32 + 5):   # all of the sequence
+        _, o, x = _attend(su, [100], None, 4, window=window, q=q)
+        assert torch.equal(o, out) and torch.equal(x, lse), window
+    assert math.isfinite(float(lse.max()))
