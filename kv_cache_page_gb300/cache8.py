@@ -4,8 +4,8 @@ K and V stay in 8 bits (E4M3 codes in pages, a power-of-two scale for each page
 and head).  ``Cache8.write`` quantises new tokens into their pages,
 ``Cache8.attend`` reads the codes themselves, ``Cache8.read`` gives tokens back in
 16 bits.  Every step runs in the CUDA kernels of ``libkvcodec.so``; this module
-checks the tensors' types, shapes and devices and passes pointers.  Calls enqueue on
-the given stream (default: torch's current stream), allocate nothing and can be
+checks the tensors' types, shapes and devices (one, the current one) and passes pointers.
+Calls enqueue on the given stream (default: torch's current stream), allocate nothing and can be
 captured into a CUDA graph.
 """
 from __future__ import annotations
@@ -71,12 +71,20 @@ def lib():
     return _LIB
 
 
-def _stream(stream):
+def _stream(stream, device):
     """The raw stream: torch's current one by its handle (a Stream object per call costs 3 us)."""
     if stream is None:
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
+        return raw(device) if raw else torch.cuda.current_stream().cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _one_device(tensors, what):
+    """The device index that the tensors share."""
+    device = tensors[0].get_device()
+    if any(t.get_device() != device for t in tensors):
+        raise ValueError(f"the tensors of a {what} must be on one device")
+    return device
 
 
 def _int32(t, name, n=None):
@@ -99,6 +107,7 @@ class Layer:
             if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous float32 CUDA tensor")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device = _one_device((k, v, k_scale, v_scale), "layer")
         self.code_bytes = min(t.untyped_storage().nbytes() - t.storage_offset() for t in (k, v))
         self.scales = min(k_scale.numel(), v_scale.numel())
         self._c = _Layer(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
@@ -131,6 +140,7 @@ class Batch:
                          None if cu_new is None else _int32(cu_new, "cu_new", n + 1),
                          None if errors is None else _int32(errors, "errors", n))
         self._ref = C.addressof(self._c)
+        self.device = _one_device([t for t in (tables, lens, cu_new, errors) if t is not None], "batch")
 
 
 class Cache8:
@@ -176,14 +186,16 @@ class Cache8:
         scales = [torch.zeros(self.num_blocks, self.num_kv_heads, device=device) for _ in range(2)]
         return Layer(*codes, *scales)
 
-    def _layer(self, layer):
+    def _layer(self, layer, batch):
         if layer.code_bytes < self._codes or layer.scales < self._scales:
             raise ValueError("the layer's tensors are smaller than the registered geometry")
+        if layer.device != batch.device or torch.cuda.current_device() != batch.device:
+            raise ValueError("the layer and the batch must be on the current CUDA device")
         return layer._ref
 
     def _rows(self, t, batch, heads, name):
-        if t.dtype is not self.dtype or not t.is_cuda:
-            raise ValueError(f"{name} must be a {self.dtype} CUDA tensor")
+        if t.dtype is not self.dtype or not t.is_cuda or t.get_device() != batch.device:
+            raise ValueError(f"{name} must be a {self.dtype} CUDA tensor on the batch's device")
         row, head, one = t.stride() if t.dim() == 3 else (0, 0, 0)
         if one != 1 or t.shape != (batch.n_new, heads, self.head_dim):
             raise ValueError(f"{name} must be [{batch.n_new}, {heads}, {self.head_dim}] with values side by side")
@@ -194,14 +206,16 @@ class Cache8:
         their pages; a page's scale grows where the new values need it, and its earlier
         codes are rewritten under the grown scale."""
         kr, vr = self._rows(k, batch, self.num_kv_heads, "k"), self._rows(v, batch, self.num_kv_heads, "v")
-        rc = self._write(self._h, self._layer(layer), batch._ref, C.addressof(kr), C.addressof(vr), _stream(stream))
+        rc = self._write(self._h, self._layer(layer, batch), batch._ref, C.addressof(kr), C.addressof(vr),
+                         _stream(stream, batch.device))
         if rc:
             _codec._check(rc, "kv_cache8_write")
 
     def read(self, layer: Layer, batch: Batch, k, v, stream=None):
         """The batch's new tokens back in 16 bits, into k and v."""
         kr, vr = self._rows(k, batch, self.num_kv_heads, "k"), self._rows(v, batch, self.num_kv_heads, "v")
-        rc = self._read(self._h, self._layer(layer), batch._ref, C.addressof(kr), C.addressof(vr), _stream(stream))
+        rc = self._read(self._h, self._layer(layer, batch), batch._ref, C.addressof(kr), C.addressof(vr),
+                        _stream(stream, batch.device))
         if rc:
             _codec._check(rc, "kv_cache8_read")
 
@@ -222,8 +236,9 @@ class Cache8:
         at = None
         if lse is not None:
             if lse.dtype is not torch.float32 or not lse.is_cuda or lse.shape != (batch.n_new, self.num_q_heads) or \
-                    not lse.is_contiguous():
-                raise ValueError(f"lse must be a contiguous float32 CUDA tensor [{batch.n_new}, {self.num_q_heads}]")
+                    not lse.is_contiguous() or lse.get_device() != batch.device:
+                raise ValueError(f"lse must be a contiguous float32 CUDA tensor [{batch.n_new}, {self.num_q_heads}] on "
+                                 "the batch's device")
             at = lse.data_ptr()
         if scale is None:
             scale = 0.0
@@ -234,10 +249,10 @@ class Cache8:
         window = min(window, _MAX_WINDOW)
         ws, nb = None, 0
         if workspace is not None:
-            if not workspace.is_cuda or not workspace.is_contiguous():
-                raise ValueError("workspace must be a contiguous CUDA tensor")
+            if not workspace.is_cuda or not workspace.is_contiguous() or workspace.get_device() != batch.device:
+                raise ValueError("workspace must be a contiguous CUDA tensor on the batch's device")
             ws, nb = workspace.data_ptr(), workspace.nbytes
-        rc = self._attend(self._h, self._layer(layer), batch._ref, C.addressof(qr), C.addressof(outr), at, scale, window,
-                          CAUSAL if causal else 0, ws, nb, _stream(stream))
+        rc = self._attend(self._h, self._layer(layer, batch), batch._ref, C.addressof(qr), C.addressof(outr), at, scale,
+                          window, CAUSAL if causal else 0, ws, nb, _stream(stream, batch.device))
         if rc:
             _codec._check(rc, "kv_cache8_attend")

@@ -162,6 +162,59 @@ def test_python_refusals_on_the_cpu():
     c.close()
 
 
+class _Tensor:
+    """Stands in for a CUDA tensor of some device where there is none: no byte of it is ever touched."""
+    is_cuda = True
+
+    def __init__(self, device, dtype, *shape):
+        t = torch.empty(*shape, dtype=dtype)
+        self.device_index, self.dtype, self.shape, self.t = device, dtype, t.shape, t
+        self.nbytes = t.nbytes
+        for name in ("stride", "dim", "numel", "is_contiguous", "storage_offset", "untyped_storage"):
+            setattr(self, name, getattr(t, name))
+
+    def get_device(self):
+        return self.device_index
+
+    def data_ptr(self):
+        return 4096
+
+
+def _on(device, **other):
+    """The arguments of a step of two sequences on one device, those named by `other` on another."""
+    at = lambda name, dtype, *shape: _Tensor(other.get(name, device), dtype, *shape)  # noqa: E731
+    cache = cache8.Cache8(**_kw())
+    layer = cache8.Layer(*(at(r, torch.uint8, 64 * 16 * 8 * 128) for r in ("k", "v")),
+                         *(at(r, torch.float32, 64, 8) for r in ("k_scale", "v_scale")))
+    batch = cache8.Batch(at("tables", torch.int32, 2, 4), at("lens", torch.int32, 2), at("cu", torch.int32, 3), n_new=2,
+                         errors=at("errors", torch.int32, 2))
+    kv, q, out = (at(r, torch.bfloat16, 2, h, 128) for r, h in (("new", 8), ("q", 32), ("out", 32)))
+    lse, ws = at("lse", torch.float32, 2, 32), at("workspace", torch.uint8, 1 << 24)
+    return {"write": lambda **kw: cache.write(layer, batch, kv, kv, **kw),
+            "read": lambda **kw: cache.read(layer, batch, kv, kv, **kw),
+            "attend": lambda **kw: cache.attend(layer, batch, q, out, lse=lse, workspace=ws, **kw)}
+
+
+@pytest.mark.parametrize("name", ["v", "k_scale", "v_scale", "lens", "cu", "errors"])
+def test_a_layer_and_a_batch_are_on_one_device(name):
+    with pytest.raises(ValueError):
+        _on(1, **{name: 0})
+
+
+@pytest.mark.parametrize("call,names", [("write", ("new",)), ("read", ("new",)), ("attend", ("q", "out", "lse", "workspace"))])
+def test_a_call_is_on_one_device_which_is_the_current_one(monkeypatch, call, names):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for name in names:
+        with pytest.raises(ValueError):
+            _on(1, **{name: 0})[call](stream=64)
+    for name in (dict(k=0, v=0, k_scale=0, v_scale=0), dict(tables=0, lens=0, cu=0, errors=0)):
+        with pytest.raises(ValueError):
+            _on(1, **name)[call](stream=64)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(ValueError):
+        _on(1)[call](stream=64)
+
+
 # ---- the reference itself, against torch's E4M3 conversions
 def test_reference_codes_match_the_format():
     bits = torch.arange(256, dtype=torch.uint8)
