@@ -21,6 +21,7 @@ from .codec import KvCodecError  # noqa: F401  (what the calls raise)
 
 ABI_VERSION = 1
 BAD_PAGE = 1
+STALLED = 2
 CAUSAL = 1
 _MAX_WINDOW = 0xffffffff  # positions are below 2^31: all of any sequence
 EXPORTS = ("kv_cache8_create", "kv_cache8_destroy", "kv_cache8_write", "kv_cache8_read", "kv_cache8_attend",
@@ -121,8 +122,9 @@ class Batch:
     [n_seqs]: tokens held, the new ones among them; cu_new [n_seqs + 1]: running
     sums of the new tokens, ``None`` for one each; n_new: their total.  max_new and
     max_len (0: not known) only choose how work is split.  errors [n_seqs] (int32,
-    zeroed by the caller): BAD_PAGE is or-ed in where a token's page is none.  All
-    are int32 CUDA tensors, read on the device when a call runs."""
+    zeroed by the caller): BAD_PAGE is or-ed in where a token's page is none, STALLED where
+    attention gave up a wait and left the sequence's output unspecified (without errors
+    neither is told).  All are int32 CUDA tensors, read on the device when a call runs."""
 
     def __init__(self, tables, lens, cu_new=None, *, n_new: Optional[int] = None, max_new: int = 0,
                  max_len: int = 0, errors=None):

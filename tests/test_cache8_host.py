@@ -30,6 +30,12 @@ def test_exports_every_declared_symbol():
     assert cache8.lib().kv_cache8_abi_version() == cache8.ABI_VERSION
 
 
+def test_the_binding_names_every_error_bit():
+    text = open(os.path.join(ROOT, "include", "kv_cache8.h")).read()
+    bits = {n: int(v) for n, v in re.findall(r"^#define KV_CACHE8_(BAD_PAGE|STALLED|CAUSAL) (\d+)u", text, re.M)}
+    assert bits == {"BAD_PAGE": cache8.BAD_PAGE, "STALLED": cache8.STALLED, "CAUSAL": cache8.CAUSAL}
+
+
 def test_structure_sizes():
     assert [C.sizeof(x) for x in (cache8._Geometry, cache8._Layer, cache8._Batch, cache8._Rows)] == [64, 32, 64, 24]
 
