@@ -66,7 +66,7 @@ __device__ __forceinline__ bool page_job(const C8Params& p, uint32_t warp, PageJ
 }
 
 // The largest finite magnitude of packed 16-bit values, two running maxima per
-// word; NaN operands are ignored, infinities are not (see finite_max).
+// word; NaN operands are ignored, infinities are not (drop_nonfinite2 takes them out).
 template <int DT>
 __device__ __forceinline__ uint32_t max2(uint32_t m, uint32_t w) {
   w &= 0x7fff7fffu;
@@ -105,6 +105,15 @@ __device__ __forceinline__ uint32_t enc_h4(uint32_t a, uint32_t b) {
   return d;
 }
 
+// The scale that a page held: an ordinary load, because the same kernel stores there
+// (this warp alone, what it makes of the value; so the load needs no other order).
+__device__ __forceinline__ float ld_held_f32(const float* ptr) {
+  KVC_GUARD(ptr, 4, return 0.0f);
+  float v;
+  asm("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(ptr));
+  return v;
+}
+
 // R: 16-byte chunks of new values a lane holds; a page with more new tokens
 // than 32 R chunks is read twice, the second time from L2.
 template <int DT, int D, int R>
@@ -123,7 +132,7 @@ __global__ void __launch_bounds__(kWarps * 32, R == 8 ? 4 : 2) c8_write_kernel(c
     uint8_t* dst = page + (int64_t)first * p.st;
     const int64_t src_step = RPI * rs, dst_step = RPI * p.st;
     float* scale_at = (role ? p.v_scale : p.k_scale) + (int64_t)j.id * p.H + j.head;
-    const float was = j.t0 > 0 ? ldg_f32(scale_at) : 0.0f;
+    const float was = j.t0 > 0 ? ld_held_f32(scale_at) : 0.0f;
 
     uint4 w[R];
     uint32_t m = 0;

@@ -221,6 +221,17 @@ def test_a_call_is_on_one_device_which_is_the_current_one(monkeypatch, call, nam
         _on(1)[call](stream=64)
 
 
+def test_the_write_kernel_reads_what_it_stores_with_ordinary_loads():
+    """Pages and scales change in that kernel: the read-only path (ld.global.nc) promises nothing about them."""
+    text = open(os.path.join(ROOT, "kv_cache_page_gb300", "csrc", "cache8_rw.cu")).read()
+    kernel = text[text.index("c8_write_kernel(const __grid_constant__"):text.index("c8_read_kernel(const __grid_constant__")]
+    read_only = re.findall(r"\b(ldg_\w+|ld_nc\w*|ld_stream\w*|__ldg)(?:<\w+>)?\(([^)]*)\)", kernel)
+    assert read_only and all(at == "at" for _, at in read_only)      # the new values
+    assert kernel.count("const uint16_t* at = src;") == 3
+    assert "*at = c;" in kernel and "uint2 c = *at;" in kernel       # the codes held
+    assert "ld_held_f32(scale_at)" in kernel
+
+
 # ---- the reference itself, against torch's E4M3 conversions
 def test_reference_codes_match_the_format():
     bits = torch.arange(256, dtype=torch.uint8)
