@@ -860,7 +860,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
       *stop = 0u;  // the others have given up or will at their own limit
       mbar_wait(sb, 0, stop);
       *stop = 1u;
-      c8_error(p, q.s, KV_CACHE8_STALLED);
     }
     }
   }
@@ -868,6 +867,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
   tc_fence_before();
   // (counts threads: the roles' loops may leave a warp diverged)
   asm volatile("barrier.sync 0;" ::: "memory");
+  if (tid == 0 && *stop) c8_error(p, q.s, KV_CACHE8_STALLED);  // whichever role gave up
   if (warp == kMmaWarp) {
     __syncwarp();
     tc_fence_after();

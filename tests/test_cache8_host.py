@@ -221,6 +221,16 @@ def test_a_call_is_on_one_device_which_is_the_current_one(monkeypatch, call, nam
         _on(1)[call](stream=64)
 
 
+def test_a_stall_of_any_role_is_reported():
+    """Every role of the prompt kernel may be the one whose wait runs out, the products' warp having finished: the report
+    comes from the mark that they share, after the barrier that all of them reach."""
+    text = open(os.path.join(ROOT, "kv_cache_page_gb300", "csrc", "cache8_prompt.cu")).read()
+    kernel = text[text.index("c8_prompt_kernel(const __grid_constant__"):]
+    report = [m.start() for m in re.finditer("KV_CACHE8_STALLED", kernel)]
+    assert len(report) == 1 and report[0] > kernel.rindex("barrier.sync 0;")
+    assert "if (tid == 0 && *stop)" in kernel
+
+
 def test_the_write_kernel_reads_what_it_stores_with_ordinary_loads():
     """Pages and scales change in that kernel: the read-only path (ld.global.nc) promises nothing about them."""
     text = open(os.path.join(ROOT, "kv_cache_page_gb300", "csrc", "cache8_rw.cu")).read()
