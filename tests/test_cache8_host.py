@@ -265,11 +265,13 @@ def test_the_register_split_is_made_once_for_each_warpgroup():
     """setmaxnreg: all warps of a warpgroup execute the same instruction, so no two roles of one have calls of their own."""
     text = open(os.path.join(ROOT, "kv_cache_page_gb300", "csrc", "cache8_prompt.cu")).read()
     kernel = text[text.index("c8_prompt_kernel(const __grid_constant__"):]
-    for call in ("regs_inc();", "regs_dec();"):
-        assert kernel.count(call) == 1, call
+    # one place for warps 0 .. 7, one for 8 .. 11 (before the branch that V's loaders begin), one for 12 .. 15
+    assert kernel.count("regs_inc();") == 1 and kernel.count("regs_dec();") == 2
+    assert re.search(r"if \(warp < kSoftWarps\) \{[^{}]*regs_inc\(\);", kernel)
+    assert re.search(r"\} else if \(warp < kSoftWarps \+ kVWarps\) \{[^{}]*regs_dec\(\);[^{}]*\} else \{\s*regs_dec\(\);", kernel)
     # the split falls between warpgroups: warps 0 .. 7 take more, 8 .. 15 keep less, and the shares add up to the launch's
     warps = {n: int(v) for n, v in re.findall(r"(kSoftWarps|kVWarps|kKWarps) = (\d+)", text)}
     more, less = (int(re.search(r"setmaxnreg\.%s\.sync\.aligned\.u32 (\d+);" % d, text).group(1)) for d in ("inc", "dec"))
     soft, rest = warps["kSoftWarps"], warps["kVWarps"] + warps["kKWarps"] + 1
-    assert soft % 4 == 0 and rest % 4 == 0
+    assert soft % 4 == 0 and warps["kVWarps"] % 4 == 0 and rest % 4 == 0
     assert 32 * (soft * more + rest * less) <= 32 * (soft + rest) * 128
