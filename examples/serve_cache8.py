@@ -68,7 +68,8 @@ def serve(seqs=8, prompt=700, steps=64, *, kv_heads=8, q_heads=32, head_dim=128,
         graph.replay()
 
     # offload of sequence 0: its tokens back in 16 bits, in whole pages of the codec's layout (an E4M3 value of
-    # a page scale is exact in bf16, and the codec's scale per token and head can only be nearer)
+    # a page scale is exact in bf16; the codec's scale per token and head is another one, so its codes round these
+    # values once more)
     n = prompts[0] + steps
     blocks = -(-n // T)
     pages = torch.zeros(2, blocks, T, kv_heads, head_dim, dtype=dt, device=dev)

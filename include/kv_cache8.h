@@ -57,7 +57,7 @@ extern "C" {
 #define KV_CACHE8_BAD_PAGE 1u /* a token's table entry is no page of the cache, or past the table's row:
                                  the token is not written, reads as zeros, is not attended to */
 #define KV_CACHE8_STALLED 2u  /* a wait inside the attention kernel ran out (of a sequence whose output is then
-                                 unspecified); never seen in a sound run */
+                                 unspecified; untold where errors is NULL); never seen in a sound run */
 
 /* Registered once per cache.  Strides are in bytes (= codes), the value stride
  * is 1, and every stride is a multiple of 16. */

@@ -113,7 +113,8 @@ struct Split {
 // the prompt kernel, the others to the step kernel.  The prompt kernel is several times
 // faster when its CTAs (256 rows of a KV head) fill the GPU, but does not split keys: below
 // 16 of them it is the slower one (one sequence over 10240 tokens, 4 query heads to each of
-// 8 KV heads, D = 128: 20 new tokens 169 us against the step kernel's 33, 64 new 186 against 90).
+// 8 KV heads, D = 128: 20 new tokens 169 us against the step kernel's 31, 64 new 186 against 88).
+// The bound does not know the number of keys: 128 new tokens over 131072 make 16 CTAs, 2.46 ms.
 uint32_t step_most(const C8Params& p, const kv_cache8_batch* b) {
   return (uint64_t)b->n_new * p.G / kvc::kPromptRows * p.H < 16u ? 512u : 64u;
 }
@@ -158,7 +159,8 @@ Split step_split(const C8Params& p, const kv_cache8_batch* b, uint32_t window) {
     // its keys, so it has 384 keys at least; and the lengths may be far below the bound, so the more jobs there
     // are the more ranges each resident CTA gets on average (64 sequences of 100 to 8192 tokens, 8 heads, D = 128:
     // ranges of 1200 keys 72 us, 2300 75, 4096 84, 512 84).  Where there are jobs enough to fill the GPU twice
-    // these are balance enough (256 sequences of 1000 to 2000 tokens: whole 150 us, ranges of 1024 169).
+    // these are balance enough (256 sequences of 1000 to 2000 tokens: whole 150 us, ranges of 1024 169, in one
+    // run; whole 139 now).
     s.warps = 4;
     const uint64_t slots = (uint64_t)kvc::kC8Sms * (p.D == 256 ? 2 : 3);
     chunk = jobs >= 2 * slots ? keys : std::max<uint64_t>(keys * jobs / (2 * slots + 5 * jobs), 384u);

@@ -20,9 +20,9 @@
 // token: as the score product's B operand dims are its inner index (K-major), as the
 // output product's B operand tokens are (MN-major), so V needs no transposition.
 //
-// Measured on a GB300, 2 prompts of 8192 tokens, 32 query heads of 128: 1.12 ms, 0.98 PFLOP/s
-// (a plain matrix product: 1.94).  Of some 4900 clocks a key tile the softmax of a row
-// tile takes 2600, its two products and the waits for them the rest; both row tiles
+// Measured on a GB300, 2 prompts of 8192 tokens, 32 query heads of 128: 1.17 ms, 0.94 PFLOP/s
+// (a plain matrix product: 1.94).  Of some 4850 clocks a key tile the softmax of a row
+// tile takes 2800, its two products and the waits for them the rest; both row tiles
 // overlap.  256 rows a CTA because K and V are converted once for both tiles; 128 keys
 // because scores and outputs of two row tiles then fill the 512 columns of TMEM.
 //
@@ -555,7 +555,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) c8_prompt_kernel(const __gr
   const uint32_t tm = *tm_at;
 
   // ---- Q to shared memory, each softmax warp its own 32 rows; bf16 rows are scaled by
-  // a power of two into FP16's range (exact but for values 2^-39 of the row's largest)
+  // a power of two into FP16's range (exact down to 2^-31 of the row's largest, below that
+  // to 2^-39 of it)
   const uint32_t r = tid;  // row of the CTA, for threads of the softmax
   const bool in = tid < 256u && r < n_rows;
   const uint32_t rr = r0 + (in ? r : 0u), tok_r = rr / p.G, hd = head * p.G + rr - tok_r * p.G;

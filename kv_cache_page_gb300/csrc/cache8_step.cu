@@ -284,8 +284,8 @@ __global__ void __launch_bounds__(W * 32, W == 4 ? (D == 256 ? 2 : 3) : 1)
     cp_commit();
   }
 
-  // Q as FP16 fragments, rows scaled by a power of two into FP16's range (bf16;
-  // exact but for values 2^-39 of the row's largest): lane (g, qd) of k-step
+  // Q as FP16 fragments, rows scaled by a power of two into FP16's range (bf16; exact
+  // down to 2^-31 of the row's largest, below that to 2^-39 of it): lane (g, qd) of k-step
   // 4 c + i holds dims 64 c + 16 qd + 4 i .. + 3 (D = 32: 8 qd + 4 i) of rows g, g + 8.
   uint32_t* s_q = reinterpret_cast<uint32_t*>(smem);
   float* s_row = reinterpret_cast<float*>(smem + S::kQ);  // per row: scale * log2(e) / row scaling
