@@ -1,6 +1,7 @@
 /*
  * kv_cache8.h -- C ABI of the live 8-bit KV cache: writing new tokens into its
- * pages, reading them back, and attention over it.
+ * pages (as they are, or with the position rotation on the way), reading them
+ * back, and attention over it.
  *
  * The page codec of kv_codec.h encodes 16-bit pages for offload.  This is the
  * cache that an engine serves from: K and V stay in 8 bits on the device, new
@@ -59,6 +60,9 @@ extern "C" {
 #define KV_CACHE8_STALLED 2u  /* a wait inside the attention kernel ran out (of a sequence whose output is then
                                  unspecified; untold where errors is NULL); never seen in a sound run */
 
+#define KV_CACHE8_BAD_POSITION 4u /* append: a token's position is past the rotation's table; its key and its
+                                     queries are NaN */
+
 /* Registered once per cache.  Strides are in bytes (= codes), the value stride
  * is 1, and every stride is a multiple of 16. */
 typedef struct kv_cache8_geometry {
@@ -109,6 +113,21 @@ typedef struct kv_cache8_rows {
   int64_t stride_head;
 } kv_cache8_rows;
 
+/* The position rotation of keys and queries.  Row p of two FP32 tables holds the cosines
+ * and sines of position p; the first dim channels of a vector are turned in pairs (a, b),
+ *     a' = a cos - b sin,  b' = b cos + a sin    (FP32, one rounding an operation),
+ * pair i being channels (i, i + dim / 2), or (2 i, 2 i + 1) with KV_CACHE8_NEIGHBOURS. */
+#define KV_CACHE8_NEIGHBOURS 1u
+typedef struct kv_cache8_rotation {
+  uint32_t struct_size;   /* sizeof(kv_cache8_rotation) */
+  uint32_t dim;           /* channels turned: a multiple of 16, at most head_dim */
+  uint32_t positions;     /* rows of the tables */
+  uint32_t flags;         /* KV_CACHE8_NEIGHBOURS */
+  const float* cos;       /* device [positions][dim / 2], 16-byte aligned */
+  const float* sin;
+  int64_t stride;         /* floats between rows, a multiple of 4 */
+} kv_cache8_rotation;
+
 typedef struct kv_cache8_s* kv_cache8_t;
 
 /* Validate a geometry and build the handle (host only).  On error *out is NULL. */
@@ -127,6 +146,16 @@ int kv_cache8_destroy(kv_cache8_t cache);
  * codes past a sequence's length stay as they are. */
 int kv_cache8_write(kv_cache8_t cache, const kv_cache8_layer* layer, const kv_cache8_batch* batch,
                     const kv_cache8_rows* k, const kv_cache8_rows* v, void* stream);
+
+/* kv_cache8_write with the rotation applied on the way: keys are turned by their
+ * positions in FP32 and quantised from there, without a rounding to 16 bits in
+ * between; values are written as they are.  q, q_out ([n_new, num_q_heads, D], both or
+ * neither): the same tokens' queries, turned and rounded once to the dtype; q_out may be
+ * q itself, and overlaps it in no other way; rows without a position become 0.
+ * rotation NULL: kv_cache8_write (q and q_out NULL). */
+int kv_cache8_append(kv_cache8_t cache, const kv_cache8_layer* layer, const kv_cache8_batch* batch,
+                     const kv_cache8_rows* k, const kv_cache8_rows* v, const kv_cache8_rotation* rotation,
+                     const kv_cache8_rows* q, const kv_cache8_rows* q_out, void* stream);
 
 /* The batch's new tokens back in 16 bits: code * scale rounded to nearest even,
  * saturating to the dtype's largest value.  (With lens as new counts this is the

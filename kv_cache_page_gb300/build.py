@@ -20,8 +20,10 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkvcodec.so")
 DEBUG_LIB = os.path.join(PKG, "libkvcodec_debug.so")
 UNITS = ["fp8.cu", "uniform.cu", "turboquant.cu", "int8.cu", "crc.cu", "cache8_rw.cu", "cache8_step.cu", "cache8_prompt.cu",
-         "kv_codec_host.cpp", "cache8_host.cpp"]
-HEADERS = ["kv_internal.h", "device_common.cuh", "crc_common.cuh", "cache8_internal.h", "cache8_common.cuh"]
+         "cache8_append.cu", "cache16_append.cu", "cache16_step.cu", "kv_codec_host.cpp", "cache8_host.cpp",
+         "cache16_host.cpp"]
+HEADERS = ["kv_internal.h", "device_common.cuh", "crc_common.cuh", "cache8_internal.h", "cache8_common.cuh",
+           "cache8_page.cuh", "cache_checks.h", "rotate.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -39,7 +41,7 @@ def _stale(target, deps):
 def _compile(unit, extra, out_dir):
     src = os.path.join(SRC, unit)
     obj = os.path.join(out_dir, unit + ".o")
-    deps = [src] + [os.path.join(ROOT, "include", h) for h in ("kv_codec.h", "kv_cache8.h")] + [os.path.join(SRC, h) for h in HEADERS]
+    deps = [src] + [os.path.join(ROOT, "include", h) for h in ("kv_codec.h", "kv_cache8.h", "kv_cache16.h")] + [os.path.join(SRC, h) for h in HEADERS]
     if _stale(obj, deps + [__file__]):
         cmd = [NVCC] + ARCH + FLAGS + extra + ["-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)

@@ -22,10 +22,12 @@ from .codec import KvCodecError  # noqa: F401  (what the calls raise)
 ABI_VERSION = 1
 BAD_PAGE = 1
 STALLED = 2
+BAD_POSITION = 4
 CAUSAL = 1
+NEIGHBOURS = 1
 _MAX_WINDOW = 0xffffffff  # positions are below 2^31: all of any sequence
-EXPORTS = ("kv_cache8_create", "kv_cache8_destroy", "kv_cache8_write", "kv_cache8_read", "kv_cache8_attend",
-           "kv_cache8_attend_workspace", "kv_cache8_abi_version")
+EXPORTS = ("kv_cache8_create", "kv_cache8_destroy", "kv_cache8_write", "kv_cache8_append", "kv_cache8_read",
+           "kv_cache8_attend", "kv_cache8_attend_workspace", "kv_cache8_abi_version")
 _DTYPES = {"fp16": torch.float16, "bf16": torch.bfloat16}
 
 
@@ -51,6 +53,11 @@ class _Rows(C.Structure):
     _fields_ = [("data", C.c_void_p), ("stride_row", C.c_int64), ("stride_head", C.c_int64)]
 
 
+class _Rotation(C.Structure):
+    _fields_ = [("struct_size", C.c_uint32), ("dim", C.c_uint32), ("positions", C.c_uint32), ("flags", C.c_uint32),
+                ("cos", C.c_void_p), ("sin", C.c_void_p), ("stride", C.c_int64)]
+
+
 _LIB = None
 
 
@@ -62,6 +69,7 @@ def lib():
         L.kv_cache8_create.argtypes = [st(_Geometry), st(vp)]
         L.kv_cache8_destroy.argtypes = [vp]
         L.kv_cache8_write.argtypes = [vp, vp, vp, vp, vp, vp]
+        L.kv_cache8_append.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp]
         L.kv_cache8_read.argtypes = [vp, vp, vp, vp, vp, vp]
         L.kv_cache8_attend.argtypes = [vp, vp, vp, vp, vp, vp, C.c_float, C.c_uint32, C.c_uint32, vp, C.c_uint64, vp]
         L.kv_cache8_attend_workspace.argtypes = [vp, vp, st(C.c_uint64)]
@@ -122,7 +130,8 @@ class Batch:
     [n_seqs]: tokens held, the new ones among them; cu_new [n_seqs + 1]: running
     sums of the new tokens, ``None`` for one each; n_new: their total.  max_new and
     max_len (0: not known) only choose how work is split.  errors [n_seqs] (int32,
-    zeroed by the caller): BAD_PAGE is or-ed in where a token's page is none, STALLED where
+    zeroed by the caller): BAD_PAGE is or-ed in where a token's page is none, BAD_POSITION where an
+    appended token's position is past the rotation's table, STALLED where
     attention gave up a wait and left the sequence's output unspecified (without errors
     neither is told).  All are int32 CUDA tensors, read on the device when a call runs."""
 
@@ -145,7 +154,91 @@ class Batch:
         self.device = _one_device([t for t in (tables, lens, cu_new, errors) if t is not None], "batch")
 
 
-class Cache8:
+class Rotation:
+    """The position rotation of keys and queries, for every layer's ``append``.
+
+    cos, sin: float32 CUDA tensors [positions, dim / 2] with values side by side and rows a
+    multiple of 4 values apart (halves of one [positions, dim] table will do).  The first dim
+    channels of a vector at position p are turned, pair i by the angle of row p's entry i:
+    channels (i, i + dim / 2), or (2 i, 2 i + 1) where interleaved.  dim is a multiple of 16 and at
+    most the cache's head_dim."""
+
+    def __init__(self, cos, sin, *, interleaved: bool = False):
+        for t, name in ((cos, "cos"), (sin, "sin")):
+            if t.dtype != torch.float32 or not t.is_cuda or t.dim() != 2 or t.shape != cos.shape:
+                raise ValueError(f"{name} must be a float32 CUDA tensor [positions, dim / 2]")
+            if t.shape[0] < 1 or t.shape[1] < 1 or (t.shape[1] > 1 and t.stride(1) != 1) or t.stride(0) != cos.stride(0):
+                raise ValueError(f"{name} must have values side by side and rows as far apart as cos")
+        self.cos, self.sin, self.interleaved = cos, sin, interleaved
+        self.dim, self.positions = 2 * cos.shape[1], cos.shape[0]
+        self.device = _one_device((cos, sin), "rotation")
+        self._c = _Rotation(C.sizeof(_Rotation), self.dim, self.positions, NEIGHBOURS if interleaved else 0,
+                            cos.data_ptr(), sin.data_ptr(), cos.stride(0))
+        self._ref = C.addressof(self._c)
+
+    @classmethod
+    def of(cls, dim: int, positions: int, *, theta: float = 1e6, interleaved: bool = False, device="cuda"):
+        """The rotation by angles p * theta^(-2 i / dim), computed in 64 bits, for positions 0 .. positions - 1."""
+        i = torch.arange(dim // 2, dtype=torch.float64, device=device)
+        angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * theta ** (-2.0 * i / dim)
+        return cls(angle.cos().float(), angle.sin().float(), interleaved=interleaved)
+
+
+class _Cache:
+    """What the 8-bit and the 16-bit cache share: rows, and the calls that take them."""
+
+    def _rows(self, t, batch, heads, name):
+        if t.dtype is not self.dtype or not t.is_cuda or t.get_device() != batch.device:
+            raise ValueError(f"{name} must be a {self.dtype} CUDA tensor on the batch's device")
+        row, head, one = t.stride() if t.dim() == 3 else (0, 0, 0)
+        if one != 1 or t.shape != (batch.n_new, heads, self.head_dim):
+            raise ValueError(f"{name} must be [{batch.n_new}, {heads}, {self.head_dim}] with values side by side")
+        return _Rows(t.data_ptr(), row, head)
+
+    def _append_call(self, call, what, layer, batch, k, v, rotation, q, q_out, stream):
+        kr, vr = self._rows(k, batch, self.num_kv_heads, "k"), self._rows(v, batch, self.num_kv_heads, "v")
+        qr = qo = turn = None
+        if rotation is not None:
+            if rotation.device != batch.device:
+                raise ValueError("the rotation must be on the batch's device")
+            turn = rotation._ref
+        if (q is None) != (q_out is None) or (q is not None and turn is None):
+            raise ValueError("q and q_out go together, and with a rotation")
+        if q is not None:
+            qr, qo = self._rows(q, batch, self.num_q_heads, "q"), self._rows(q_out, batch, self.num_q_heads, "q_out")
+        rc = call(self._h, self._layer(layer, batch), batch._ref, C.addressof(kr), C.addressof(vr), turn,
+                  qr and C.addressof(qr), qo and C.addressof(qo), _stream(stream, batch.device))
+        if rc:
+            _codec._check(rc, what)
+
+    def _attend_call(self, call, what, layer, batch, q, out, lse, scale, causal, window, workspace, stream):
+        qr, outr = self._rows(q, batch, self.num_q_heads, "q"), self._rows(out, batch, self.num_q_heads, "out")
+        at = None
+        if lse is not None:
+            if lse.dtype is not torch.float32 or not lse.is_cuda or lse.shape != (batch.n_new, self.num_q_heads) or \
+                    not lse.is_contiguous() or lse.get_device() != batch.device:
+                raise ValueError(f"lse must be a contiguous float32 CUDA tensor [{batch.n_new}, {self.num_q_heads}] on "
+                                 "the batch's device")
+            at = lse.data_ptr()
+        if scale is None:
+            scale = 0.0
+        elif not (scale > 0 and math.isfinite(C.c_float(scale).value) and C.c_float(scale).value > 0):
+            raise ValueError("scale must be finite and positive in float32")  # (0 would stand for the default)
+        if window < 0:
+            raise ValueError("window must not be negative")
+        window = min(window, _MAX_WINDOW)
+        ws, nb = None, 0
+        if workspace is not None:
+            if not workspace.is_cuda or not workspace.is_contiguous() or workspace.get_device() != batch.device:
+                raise ValueError("workspace must be a contiguous CUDA tensor on the batch's device")
+            ws, nb = workspace.data_ptr(), workspace.nbytes
+        rc = call(self._h, self._layer(layer, batch), batch._ref, C.addressof(qr), C.addressof(outr), at, scale,
+                  window, CAUSAL if causal else 0, ws, nb, _stream(stream, batch.device))
+        if rc:
+            _codec._check(rc, what)
+
+
+class Cache8(_Cache):
     """A registered cache geometry (one ``kv_cache8_t`` handle).  strides: (block,
     token, head) in codes of the page layout; default [block, token, head, D]."""
 
@@ -166,6 +259,7 @@ class Cache8:
         self._scales = num_blocks * num_kv_heads
         L = lib()
         self._write, self._read, self._attend = L.kv_cache8_write, L.kv_cache8_read, L.kv_cache8_attend
+        self._append = L.kv_cache8_append
         h = C.c_void_p()
         self._h = None
         _codec._check(lib().kv_cache8_create(C.byref(g), C.byref(h)), "kv_cache8_create")
@@ -195,14 +289,6 @@ class Cache8:
             raise ValueError("the layer and the batch must be on the current CUDA device")
         return layer._ref
 
-    def _rows(self, t, batch, heads, name):
-        if t.dtype is not self.dtype or not t.is_cuda or t.get_device() != batch.device:
-            raise ValueError(f"{name} must be a {self.dtype} CUDA tensor on the batch's device")
-        row, head, one = t.stride() if t.dim() == 3 else (0, 0, 0)
-        if one != 1 or t.shape != (batch.n_new, heads, self.head_dim):
-            raise ValueError(f"{name} must be [{batch.n_new}, {heads}, {self.head_dim}] with values side by side")
-        return _Rows(t.data_ptr(), row, head)
-
     def write(self, layer: Layer, batch: Batch, k, v, stream=None):
         """Quantise the batch's new tokens (k, v: [n_new, num_kv_heads, head_dim]) into
         their pages; a page's scale grows where the new values need it, and its earlier
@@ -212,6 +298,13 @@ class Cache8:
                          _stream(stream, batch.device))
         if rc:
             _codec._check(rc, "kv_cache8_write")
+
+    def append(self, layer: Layer, batch: Batch, k, v, *, rotation: Optional[Rotation], q=None, q_out=None, stream=None):
+        """``write`` with the keys turned by their positions on the way, quantised from float32 (rotation None: as they
+        are).  q, q_out ([n_new, num_q_heads, head_dim], both or neither): the tokens' queries, turned and rounded to the
+        dtype; q_out may be q itself.  Rows without a position get q_out = 0; those past the rotation's table get NaN
+        keys and queries, and BAD_POSITION."""
+        self._append_call(self._append, "kv_cache8_append", layer, batch, k, v, rotation, q, q_out, stream)
 
     def read(self, layer: Layer, batch: Batch, k, v, stream=None):
         """The batch's new tokens back in 16 bits, into k and v."""
@@ -234,27 +327,5 @@ class Cache8:
         A row that sees no key gets out = 0, lse = -inf.  workspace: a CUDA tensor of at
         least ``attend_workspace(batch)`` bytes, zero-filled before its first use, then good
         for any batch or cache, not shared by calls that may run at the same time."""
-        qr, outr = self._rows(q, batch, self.num_q_heads, "q"), self._rows(out, batch, self.num_q_heads, "out")
-        at = None
-        if lse is not None:
-            if lse.dtype is not torch.float32 or not lse.is_cuda or lse.shape != (batch.n_new, self.num_q_heads) or \
-                    not lse.is_contiguous() or lse.get_device() != batch.device:
-                raise ValueError(f"lse must be a contiguous float32 CUDA tensor [{batch.n_new}, {self.num_q_heads}] on "
-                                 "the batch's device")
-            at = lse.data_ptr()
-        if scale is None:
-            scale = 0.0
-        elif not (scale > 0 and math.isfinite(C.c_float(scale).value) and C.c_float(scale).value > 0):
-            raise ValueError("scale must be finite and positive in float32")  # (0 would stand for the default)
-        if window < 0:
-            raise ValueError("window must not be negative")
-        window = min(window, _MAX_WINDOW)
-        ws, nb = None, 0
-        if workspace is not None:
-            if not workspace.is_cuda or not workspace.is_contiguous() or workspace.get_device() != batch.device:
-                raise ValueError("workspace must be a contiguous CUDA tensor on the batch's device")
-            ws, nb = workspace.data_ptr(), workspace.nbytes
-        rc = self._attend(self._h, self._layer(layer, batch), batch._ref, C.addressof(qr), C.addressof(outr), at, scale,
-                          window, CAUSAL if causal else 0, ws, nb, _stream(stream, batch.device))
-        if rc:
-            _codec._check(rc, "kv_cache8_attend")
+        self._attend_call(self._attend, "kv_cache8_attend", layer, batch, q, out, lse, scale, causal, window, workspace,
+                          stream)

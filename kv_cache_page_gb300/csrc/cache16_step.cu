@@ -1,0 +1,705 @@
+// cache16_step.cu -- attention of few query rows over the 16-bit pages: single tokens,
+// drafted tokens, short chunks.
+//
+//   z_rj = scale (q_r . k_j),  out_r = sum_j 2^(z_rj - m_r) v_j / l_r
+//
+// Bound by reading K and V once (4 D bytes a token and KV head).  A row tile is the G query
+// heads of a KV head times the new tokens, 8 or 16 rows at a time; a job is a row tile of a
+// sequence and a KV head, its keys in steps of 16 or 32 tokens.  The lengths are on the
+// device, so the split is made there: every CTA adds up the steps of all sequences, takes
+// an equal share of the row of all jobs' steps (the last of one job, some whole ones, the
+// first of another), and finds where that begins.  No CTA is idle while another has two
+// shares, whatever the lengths, and no sum needs the host to know them.
+//
+// In a CTA the warps take a job's steps in turn, each on its own: asynchronous copies into
+// slots of its own, stages ahead, without barriers; they join at the job's end.  A job that
+// lies in several shares leaves a partial result in each, and the CTA that finishes last
+// joins them in the order of the keys, so the result does not depend on timing.
+//
+// Both products have the tokens (scores) and the dims (outputs) as their 16 rows and 8 query
+// rows as their columns: K's tile is the operand as it lies, V's as ldmatrix transposes it,
+// and the weights pass through a transposition in registers.  A weight is split into two
+// 16-bit terms (the second product is made twice): with one, BF16 weights alone would be as
+// coarse as the output's rounding.
+#include "cache8_common.cuh"
+
+namespace kvc {
+
+#ifdef KVC_BOUNDS_CHECK
+inline void dbg_ranges(DbgRanges& r, const C16Params& p) {
+  const uint64_t last = (uint64_t)p.sb * (p.num_blocks - 1u) + (uint64_t)p.st * (p.T - 1u) +
+                        (uint64_t)p.sh * (p.H - 1u) + 2u * p.D;
+  dbg_add(r, p.k, dbg_slot_bytes(last));
+  dbg_add(r, p.v, dbg_slot_bytes(last));
+  dbg_add(r, p.tables, 4ull * ((uint64_t)p.table_stride * (p.n_seqs - 1u) + p.table_width));
+  dbg_add(r, p.lens, 4ull * p.n_seqs);
+  if (p.cu) dbg_add(r, p.cu, 4ull * (p.n_seqs + 1u));
+  if (p.errors) dbg_add(r, p.errors, 4ull * p.n_seqs);
+  dbg_rows(r, p.a, p.a_row, p.a_head, p, p.HQ);
+  dbg_rows(r, p.b, p.b_row, p.b_head, p, p.HQ);
+  if (p.lse) dbg_add(r, p.lse, 4ull * p.n_new * p.HQ);
+  dbg_add(r, p.tickets, 4ull * kC16Ctas);
+  dbg_add(r, p.partials, 4ull * kC16Ctas * 2u * kStepRows * (p.D + 2u));
+}
+#endif
+
+namespace {
+
+constexpr float kNegInf = -INFINITY;
+// m may lag the true maximum by kLag (fewer rescalings of the sums).
+constexpr float kLag = 4.0f;
+// Weights are held as 2^(z - m + bias).  FP16: largest 2^11 .. 2^15, so that 2^-25, half of the smallest FP16, is 2^-36 of the
+// largest.  BF16: 2^-24 .. 2^-20, so that sums over 2^20 keys of V next to 2^128 stay in FP32's range.
+template <int DT>
+constexpr float kBias = DT == 0 ? 11.0f : -24.0f;
+
+// A barrier of the CTA that counts threads, whether or not their warp is converged.
+__device__ __forceinline__ void cta_sync() { asm volatile("barrier.sync 0;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int DT>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (DT == 0)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t smem) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t smem) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem)
+               : "memory");
+}
+// Transpose of an 8 x 8 tile of 16-bit values, two values of a row to a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Copy 16 bytes to a shared slot; zeros when !ok.
+__device__ __forceinline__ void cp16z(uint32_t smem, const void* src, bool ok) {
+#ifdef KVC_BOUNDS_CHECK
+  if (ok && !dbg_ok(src, 16)) ok = false;
+#endif
+  const uint32_t n = ok ? 16u : 0u;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp16(uint32_t smem, const void* src) {
+  KVC_GUARD(src, 16, return);
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// loads of what other CTAs of this launch have stored (L2)
+__device__ __forceinline__ float2 ld_join2(const float* ptr) {
+  KVC_GUARD(ptr, 8, return make_float2(0.f, 0.f));
+  return __ldcg(reinterpret_cast<const float2*>(ptr));
+}
+__device__ __forceinline__ float4 ld_join4(const float* ptr) {
+  KVC_GUARD(ptr, 16, return make_float4(0.f, 0.f, 0.f, 0.f));
+  return __ldcg(reinterpret_cast<const float4*>(ptr));
+}
+
+template <int D>
+struct Shape16 {
+  static constexpr int TS = D >= 128 ? 16 : 32;  // tokens of a step
+  static constexpr int HT = TS / 16;
+  static constexpr int C = D / 8;                // 16-byte chunks of a row
+  static constexpr int RPI = 32 / C;             // rows that a warp's copy instruction covers
+  static constexpr int kTile = 16 * D * 2;       // 16 tokens of K, or of V
+  static constexpr int kStage = 2 * HT * kTile;  // K tiles, then V tiles
+  static constexpr int NS = D == 32 ? 4 : 3;
+  static constexpr int kQ = 16 * D * 2;
+  static constexpr int kSmall = 2048;
+  static constexpr int kOut = D + 4;             // floats of a row in the join of the warps
+};
+template <int D>
+constexpr int smem16(int warps) {
+  using S = Shape16<D>;
+  return S::kQ + S::kSmall + warps * S::NS * S::kStage;
+}
+
+// 8 consecutive rows of one chunk lie in 8 different bank groups: chunk c of row t is at c ^ swz(t).
+template <int D>
+__device__ __forceinline__ uint32_t swz(uint32_t t) {
+  return D == 32 ? (t >> 1) & 3u : t & 7u;
+}
+
+// A sequence of the batch, and how many steps its jobs have.
+struct Seq16 {
+  C8Seq q;
+  int32_t lo, hi;   // keys that some row sees; lo at a 16-token tile where pages are whole tiles
+  bool past;        // tokens lie past the table's row
+  uint32_t steps;   // of a job
+  uint64_t all;     // of all jobs
+};
+template <int TS, bool PAGED16>
+__device__ __forceinline__ Seq16 seq16(const C16Params& p, uint32_t s) {
+  Seq16 x;
+  x.q.s = s;
+  x.q.unit = 0;
+  const int32_t len = ldg_i32(p.lens + s);
+  if (p.cu) c8_fill(p, x.q, ldg_i32(p.cu + s), ldg_i32(p.cu + s + 1u), len);
+  else c8_fill(p, x.q, (int32_t)s, (int32_t)s + 1, len);
+  const uint64_t reach = (uint64_t)p.table_width * p.T;
+  x.past = (uint64_t)x.q.len > reach;
+  x.hi = x.past ? (int32_t)reach : x.q.len;
+  x.lo = p.window && x.q.start >= 0 ? max(0, x.q.start - (int32_t)min(p.window, 0x7fffffffu) + 1) : 0;
+  if (PAGED16) x.lo &= ~15;
+  x.steps = x.hi > x.lo ? ((uint32_t)(x.hi - x.lo) + TS - 1u) / TS : 1u;  // (rows that see nothing are a step)
+  const uint32_t tiles = ((uint32_t)x.q.n_new * p.G + p.tile_rows - 1u) / p.tile_rows;
+  x.all = (uint64_t)x.steps * tiles * p.H;
+  return x;
+}
+
+// PAGED16: pages are whole 16-token tiles, so a tile lies in one page; otherwise every token's page is
+// looked up by itself.  NT: 8-row column blocks of a row tile.
+template <int DT, int D, bool PAGED16, int NT>
+__global__ void __launch_bounds__(128) c16_step_kernel(const __grid_constant__ C16Params p) {
+  using S = Shape16<D>;
+  constexpr int NS = S::NS, TS = S::TS, HT = S::HT, TR = 8 * NT, KS = D / 16;
+  constexpr uint32_t kFull = TS == 32 ? 0xffffffffu : 0xffffu;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, threads = blockDim.x, W = threads >> 5;
+  const uint32_t g = lane >> 2, qd = lane & 3u;
+  const uint32_t sm_q = (uint32_t)__cvta_generic_to_shared(smem);
+  float* s_m = reinterpret_cast<float*>(smem + S::kQ);             // [row][warp] maxima
+  float* s_l = s_m + 16 * 8;                                       // [row][warp] sums, at the row's maximum
+  float2* s_fin = reinterpret_cast<float2*>(s_l + 16 * 8);         // row: maximum, 1 / sum
+  unsigned long long* s_tot = reinterpret_cast<unsigned long long*>(s_fin + 16);  // [8] warps' steps, then where to begin
+  uint32_t* s_last = reinterpret_cast<uint32_t*>(s_tot + 10);
+  static_assert(16 * 8 * 8 + 16 * 8 + 10 * 8 + 4 <= S::kSmall, "");
+  uint8_t* slots = smem + S::kQ + S::kSmall;
+  float* s_o = reinterpret_cast<float*>(slots);                    // [warp][TR][kOut], over the slots
+  float2* s_ml = reinterpret_cast<float2*>(slots);                 // [partial][TR], over the slots
+  static_assert((int)kC16Ctas * 16 * 8 <= 4 * S::NS * S::kStage && 16 * S::kOut * 4 <= S::NS * S::kStage, "");
+  const uint32_t my_slots = sm_q + S::kQ + S::kSmall + warp * (NS * S::kStage);
+
+  // ---- this CTA's share of all steps
+  uint64_t at, end, share;  // steps, counted over all jobs
+  uint32_t s;
+  uint64_t base;            // where sequence s begins
+  {
+    const uint32_t per = (p.n_seqs + threads - 1u) / threads, i0 = min(tid * per, p.n_seqs), i1 = min(i0 + per, p.n_seqs);
+    unsigned long long mine = 0;
+    for (uint32_t i = i0; i < i1; ++i) mine += seq16<TS, PAGED16>(p, i).all;
+    unsigned long long inc = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= (uint32_t)d) inc += y;
+    }
+    if (lane == 31u) s_tot[warp] = inc;
+    cta_sync();
+    unsigned long long before = 0, total = 0;
+    for (uint32_t w = 0; w < W; ++w) {
+      before += w < warp ? s_tot[w] : 0ull;
+      total += s_tot[w];
+    }
+    share = max((total + gridDim.x - 1u) / gridDim.x, (unsigned long long)p.share);
+    at = (uint64_t)blockIdx.x * share;
+    if (at >= total) return;
+    end = min(at + share, (uint64_t)total);
+    unsigned long long pre = before + inc - mine;
+    if (pre <= at && at < pre + mine) {
+      uint32_t i = i0;
+      for (;; ++i) {
+        const uint64_t n = seq16<TS, PAGED16>(p, i).all;
+        if (at < pre + n) break;
+        pre += n;
+      }
+      s_tot[8] = pre;
+      s_tot[9] = i;
+    }
+    cta_sync();
+    base = s_tot[8];
+    s = (uint32_t)s_tot[9];
+  }
+
+  // what of a tile's copies and fragments belongs to this lane (byte offsets within a tile, chunks swizzled)
+  const uint32_t c_row = lane / S::C, c_chunk = lane % S::C;
+  const uint32_t c_dst = c_row * (D * 2) + ((c_chunk ^ swz<D>(c_row)) << 4);
+  const uint32_t k_at = (lane & 15u) * (D * 2) + (((lane >> 4) ^ swz<D>(lane & 15u)) << 4);
+  const uint32_t v_row = (lane & 7u) + ((lane >> 4) << 3);
+  const uint32_t v_at = v_row * (D * 2) + ((((lane >> 3) & 1u) ^ swz<D>(v_row)) << 4);
+
+  Seq16 x = seq16<TS, PAGED16>(p, s);
+  while (at < end) {
+    while (at >= base + x.all) {  // (a sequence without new tokens has no steps)
+      base += x.all;
+      x = seq16<TS, PAGED16>(p, ++s);
+    }
+    const uint64_t job = (at - base) / x.steps;
+    const uint32_t step0 = (uint32_t)(at - base - job * x.steps);
+    const uint32_t n_steps = (uint32_t)min((uint64_t)(x.steps - step0), end - at);
+    const uint32_t tile = (uint32_t)(job / p.H), head = (uint32_t)(job - (uint64_t)tile * p.H);
+    const uint64_t job0 = base + job * x.steps;
+    const uint32_t cta0 = (uint32_t)(job0 / share), n_parts = (uint32_t)((job0 + x.steps - 1u) / share) - cta0 + 1u;
+    at += n_steps;
+
+    const uint32_t r0 = tile * TR, n_rows = min((uint32_t)TR, (uint32_t)x.q.n_new * p.G - r0);
+    const int32_t first_pos = x.q.start + (int32_t)(r0 / p.G), last_pos = x.q.start + (int32_t)((r0 + n_rows - 1u) / p.G);
+    // keys that some row of the tile sees, and the steps that hold them
+    const int32_t t_hi = last_pos < 0 ? 0 : p.causal ? min(x.hi, last_pos + 1) : x.hi;
+    const int32_t t_lo = p.window && first_pos >= 0 ? max(0, first_pos - (int32_t)min(p.window, 0x7fffffffu) + 1) : 0;
+    const int32_t x_lo = max((int32_t)step0, t_lo > x.lo ? (t_lo - x.lo) / TS : 0);
+    const int32_t x_hi = min((int32_t)(step0 + n_steps), t_hi > x.lo ? (t_hi - x.lo + TS - 1) / TS : 0);
+    const bool several = first_pos != last_pos;  // rows of several positions: they do not all see the same keys
+    const int32_t* table = p.tables + (int64_t)x.q.s * p.table_stride;
+    bool bad = x.past && tid == 0u;
+
+    // raw table entry of this lane's token of step t; -2 past the keys
+    auto entry_of = [&](int32_t t) -> int32_t {
+      const int32_t tok = x.lo + TS * t + (int32_t)(lane % TS);
+      return t < x_hi && tok < t_hi ? ldg_i32(table + c8_div_t(p, (uint32_t)tok)) : -2;
+    };
+    const uint8_t* k_src = p.k + (int64_t)head * p.sh + c_chunk * 16 + (PAGED16 ? (int64_t)c_row * p.st : 0);
+    const uint8_t* v_src = p.v + (int64_t)head * p.sh + c_chunk * 16 + (PAGED16 ? (int64_t)c_row * p.st : 0);
+    // Start the copies of step t.  Tokens that no row sees, and those without a page, become zeros.  Returns the
+    // tokens that are there, a bit each.
+    auto issue = [&](int32_t t, int stage, int32_t entry) -> uint32_t {
+      const uint32_t dst = my_slots + stage * S::kStage + c_dst;
+      const int32_t tok = x.lo + TS * t + (int32_t)(lane % TS);
+      const bool in = tok >= t_lo && tok < t_hi, page = (uint32_t)entry < p.num_blocks;
+      bad |= in && !page;
+      const uint32_t there = __ballot_sync(0xffffffffu, in && page) & kFull;
+      const uint32_t in_page = (uint32_t)tok - c8_div_t(p, (uint32_t)tok) * p.T;
+      const int64_t off = (int64_t)entry * p.sb + (int64_t)in_page * p.st;
+#pragma unroll
+      for (int h = 0; h < HT; ++h) {
+        const uint32_t bits = HT == 1 ? there : (there >> (16 * h)) & 0xffffu;
+        const int64_t tile_off = __shfl_sync(0xffffffffu, off, 16 * h);
+        if (PAGED16 && bits == 0xffffu) {
+          const uint8_t *ks = k_src + tile_off, *vs = v_src + tile_off;
+#pragma unroll
+          for (int i = 0; i < 16 / S::RPI; ++i) {
+            const uint32_t to = (dst ^ (swz<D>(S::RPI * i) << 4)) + h * S::kTile + i * S::RPI * (D * 2);
+            cp16(to, ks);
+            cp16(to + HT * S::kTile, vs);
+            ks += S::RPI * p.st;
+            vs += S::RPI * p.st;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16 / S::RPI; ++i) {
+            const uint32_t to = (dst ^ (swz<D>(S::RPI * i) << 4)) + h * S::kTile + i * S::RPI * (D * 2);
+            const uint32_t row = c_row + S::RPI * i;
+            const bool ok = (bits >> row) & 1u;
+            const int64_t o = PAGED16 ? tile_off + (int64_t)(S::RPI * i) * p.st : __shfl_sync(0xffffffffu, off, 16 * h + row);
+            cp16z(to, ok ? k_src + o : p.k, ok);
+            cp16z(to + HT * S::kTile, ok ? v_src + o : p.v, ok);
+          }
+        }
+      }
+      return there;
+    };
+
+    cta_sync();  // the job before is done with shared memory
+    uint32_t there[NS];  // of the stages in flight, the oldest first
+    int32_t entry;
+    {
+      int32_t e[NS - 1];
+#pragma unroll
+      for (int i = 0; i < NS - 1; ++i) e[i] = entry_of(x_lo + (int32_t)(warp + i * W));
+      entry = entry_of(x_lo + (int32_t)(warp + (NS - 1) * W));
+      for (uint32_t i = tid; i < TR * S::C; i += threads) {
+        const uint32_t r = i / S::C, c = i % S::C, rr = r0 + min(r, n_rows - 1u), tok = rr / p.G;
+        const uint16_t* src = p.a + ((int64_t)x.q.row + tok) * p.a_row + (int64_t)(head * p.G + rr - tok * p.G) * p.a_head + c * 8;
+        cp16z(sm_q + r * (D * 2) + ((c ^ swz<D>(r)) << 4), src, r < n_rows);
+      }
+      cp_commit();
+#pragma unroll
+      for (int i = 0; i < NS - 1; ++i) {
+        const int32_t t = x_lo + (int32_t)(warp + i * W);
+        there[i] = t < x_hi ? issue(t, i, e[i]) : 0u;
+        cp_commit();
+      }
+    }
+    cp_wait<NS - 1>();  // the queries
+    cta_sync();
+    uint32_t qf[NT][KS][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < KS / 2; ++k) {
+        const uint32_t row = 8u * n + (lane & 7u);
+        uint32_t w[4];
+        ldsm4(w, (sm_q + row * (D * 2) + (((lane >> 3) ^ swz<D>(row)) << 4)) ^ (k << 6));
+        qf[n][2 * k][0] = w[0];
+        qf[n][2 * k][1] = w[1];
+        qf[n][2 * k + 1][0] = w[2];
+        qf[n][2 * k + 1][1] = w[3];
+      }
+    // steps between these need no mask by rows
+    const int32_t full_hi = !several ? 0x7fffffff : first_pos < 0 ? 0 : p.causal ? first_pos + 1 : 0x7fffffff;
+    const int32_t full_lo = several && p.window ? (int32_t)max((int64_t)0, (int64_t)last_pos - p.window + 1) : 0;
+
+    float o[KS][NT][4];
+#pragma unroll
+    for (int i = 0; i < KS; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.0f;
+    float m[NT][2], l[NT][2];  // of rows 8 n + 2 qd, + 1
+#pragma unroll
+    for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = kNegInf, l[n][0] = l[n][1] = 0.0f;
+
+    int stage = 0;
+    for (int32_t t = x_lo + (int32_t)warp; t < x_hi; t += (int32_t)W) {
+      {
+        const int32_t tn = t + (int32_t)((NS - 1) * W);
+        __syncwarp();  // every lane is done with the stage that is refilled
+        there[NS - 1] = 0u;
+        if (tn < x_hi) {
+          const int32_t e = entry;
+          entry = entry_of(tn + (int32_t)W);
+          there[NS - 1] = issue(tn, stage == 0 ? NS - 1 : stage - 1, e);
+        }
+        cp_commit();
+        cp_wait<NS - 1>();
+        __syncwarp();  // the other lanes' copies
+      }
+      const uint32_t bits = there[0];
+#pragma unroll
+      for (int i = 0; i < NS - 1; ++i) there[i] = there[i + 1];
+      const uint32_t sk = my_slots + stage * S::kStage + k_at, sv = my_slots + stage * S::kStage + HT * S::kTile + v_at;
+      stage = stage == NS - 1 ? 0 : stage + 1;
+      const int32_t tok0 = x.lo + TS * t;
+
+      // scores of tokens 16 h + g, + 8 and rows 8 n + 2 qd, + 1
+      float z[HT][NT][4];
+#pragma unroll
+      for (int h = 0; h < HT; ++h) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) z[h][n][0] = z[h][n][1] = z[h][n][2] = z[h][n][3] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          uint32_t a[4];
+          ldsm4(a, (sk ^ (k << 5)) + h * S::kTile);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma16816<DT>(z[h][n], a, qf[n][k][0], qf[n][k][1]);
+        }
+      }
+      const bool by_row = tok0 + TS > full_hi || tok0 < full_lo;
+#pragma unroll
+      for (int h = 0; h < HT; ++h)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[h][n][e] *= p.scale_log2;
+      if (by_row || bits != kFull) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            // keys that the row sees
+            int32_t hi = 0x7fffffff, lo = 0;
+            if (by_row) {
+              const int32_t pos = x.q.start + (int32_t)((r0 + 8u * n + 2u * qd + r) / p.G);
+              if (p.causal) hi = pos + 1;
+              if (p.window) lo = (int32_t)max((int64_t)0, (int64_t)pos - p.window + 1);
+              if (pos < 0) hi = 0;
+            }
+#pragma unroll
+            for (int h = 0; h < HT; ++h)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t i = 16u * h + 8u * e + g;
+                const int32_t tok = tok0 + (int32_t)i;
+                if (!((bits >> i) & 1u) || tok >= hi || tok < lo) z[h][n][2 * e + r] = kNegInf;
+              }
+          }
+      }
+      // running maxima; the sums are rescaled only where a maximum grew by more than kLag
+      bool grow = false;
+#pragma unroll
+      for (int h = 0; h < HT; ++h)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) grow |= z[h][n][e] > m[n][e & 1] + kLag;  // -inf + kLag = -inf: any finite score
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float mx = kNegInf;
+#pragma unroll
+            for (int h = 0; h < HT; ++h) mx = fmaxf(mx, fmaxf(z[h][n][r], z[h][n][2 + r]));
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            const float mn = fmaxf(mx, m[n][r]);
+            const float f = m[n][r] == kNegInf ? 0.0f : ex2(m[n][r] - mn);
+            m[n][r] = mn;
+            l[n][r] *= f;
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+              o[i][n][r] *= f;
+              o[i][n][2 + r] *= f;
+            }
+          }
+      }
+      // weights, split in two terms and transposed: row g, tokens 2 qd, + 1 (+ 8 e)
+      uint32_t wh[HT][NT][2], wl[HT][NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float b0 = m[n][0] == kNegInf ? 0.0f : m[n][0] - kBias<DT>;
+        const float b1 = m[n][1] == kNegInf ? 0.0f : m[n][1] - kBias<DT>;
+#pragma unroll
+        for (int h = 0; h < HT; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float p0 = ex2(z[h][n][2 * e] - b0), p1 = ex2(z[h][n][2 * e + 1] - b1);
+            l[n][0] += p0;
+            l[n][1] += p1;
+            const uint32_t w = pack2<DT>(p0, p1);
+            wh[h][n][e] = transpose8(w);
+            wl[h][n][e] = transpose8(pack2<DT>(p0 - lo_f32<DT>(w), p1 - hi_f32<DT>(w)));
+          }
+      }
+      // V: dims 16 i + g, + 8 of tokens 2 qd, + 1, + 8, + 9
+      uint32_t odd = 0;
+#pragma unroll
+      for (int h = 0; h < HT; ++h)
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          uint32_t a[4];
+          ldsm4_t(a, (sv ^ (i << 5)) + h * S::kTile);
+          if (by_row) {
+            // an infinity or a NaN that some row does not see must not reach it through 0 times it: such values
+            // become 0 here, and NaN is put below where they are seen
+            constexpr uint32_t E = DT == 0 ? 0x7c00u : 0x7f80u;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t lo = (a[k] & E) == E ? 0xffffu : 0u, hi = (a[k] & (E << 16)) == (E << 16) ? 0xffff0000u : 0u;
+              odd |= lo | hi;
+              a[k] &= ~(lo | hi);
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma16816<DT>(o[i][n], a, wh[h][n][0], wh[h][n][1]);
+            mma16816<DT>(o[i][n], a, wl[h][n][0], wl[h][n][1]);
+          }
+        }
+      if (by_row && __any_sync(0xffffffffu, odd != 0u)) {
+        // rows x dims where a visible token's value is one: count them with the same product
+        constexpr uint32_t E = DT == 0 ? 0x7c00u : 0x7f80u, one = DT == 0 ? 0x3c00u : 0x3f80u;
+#pragma unroll
+        for (int h = 0; h < HT; ++h) {
+          uint32_t seen[NT][2];
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              seen[n][e] = transpose8((z[h][n][2 * e] == kNegInf ? 0u : one) | (z[h][n][2 * e + 1] == kNegInf ? 0u : one << 16));
+#pragma unroll
+          for (int i = 0; i < KS; ++i) {
+            uint32_t a[4];
+            ldsm4_t(a, (sv ^ (i << 5)) + h * S::kTile);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              a[k] = ((a[k] & E) == E ? one : 0u) | ((a[k] & (E << 16)) == (E << 16) ? one << 16 : 0u);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              float cnt[4] = {0.f, 0.f, 0.f, 0.f};
+              mma16816<DT>(cnt, a, seen[n][0], seen[n][1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (cnt[e] > 0.0f) o[i][n][e] = __int_as_float(0x7fffffff);
+            }
+          }
+        }
+      }
+    }
+    cp_wait<0>();
+    if (bad) c8_error(p, x.q.s, KV_CACHE8_BAD_PAGE);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int d = 4; d < 32; d *= 2) l[n][r] += __shfl_xor_sync(0xffffffffu, l[n][r], d);
+
+    // ---- join the warps: every row to the largest maximum among them
+    if (g == 0u) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        s_m[(8 * n + 2 * qd) * W + warp] = m[n][0];
+        s_m[(8 * n + 2 * qd + 1) * W + warp] = m[n][1];
+      }
+    }
+    cta_sync();
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t row = 8u * n + 2u * qd + r;
+        float mx = kNegInf;
+        for (uint32_t w = 0; w < W; ++w) mx = fmaxf(mx, s_m[row * W + w]);
+        const float f = m[n][r] == kNegInf ? 0.0f : ex2(m[n][r] - mx);
+        if (g == 0u) s_l[row * W + warp] = l[n][r] * f;
+        float* dst = s_o + (warp * TR + row) * S::kOut;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          dst[16 * i + g] = o[i][n][r] * f;
+          dst[16 * i + 8 + g] = o[i][n][2 + r] * f;
+        }
+      }
+    cta_sync();
+
+    const uint64_t part_floats = TR * (D + 2);
+    // partials of a job that several CTAs hold: the first CTA's is its second one (the job begins in its share),
+    // every other's its first
+    auto part_of = [&](uint32_t k) { return p.partials + (2ull * (cta0 + k) + (k == 0u ? 1u : 0u)) * part_floats; };
+    float* mine = part_of(blockIdx.x - cta0);
+    // a row's maximum and sum: the factor of its outputs, and lse
+    auto finish_row = [&](uint32_t row, float mx, float ls) {
+      s_fin[row] = make_float2(mx, ls == 0.0f ? 0.0f : 1.0f / ls);
+      if (p.lse && row < n_rows) {
+        const uint32_t rr = r0 + row, tok = rr / p.G, hd = head * p.G + rr - tok * p.G;
+        st4(p.lse + ((int64_t)x.q.row + tok) * p.HQ + hd,
+            __float_as_uint(ls == 0.0f ? kNegInf : (mx - kBias<DT> + log2f(ls)) * 0.693147180559945309f));
+      }
+    };
+    auto finish_out = [&](uint32_t r, uint32_t d4, float4 y) {
+      const float inv = s_fin[r].y;
+      const uint32_t rr = r0 + r, tok = rr / p.G, hd = head * p.G + rr - tok * p.G;
+      st8(p.b + ((int64_t)x.q.row + tok) * p.b_row + (int64_t)hd * p.b_head + d4 * 4,
+          inv == 0.0f ? make_uint2(0, 0)
+                      : make_uint2(pack2<DT>(y.x * inv, y.y * inv), pack2<DT>(y.z * inv, y.w * inv)));
+    };
+    if (tid < n_rows) {
+      float mx = kNegInf, ls = 0.0f;
+      for (uint32_t w = 0; w < W; ++w) {
+        mx = fmaxf(mx, s_m[tid * W + w]);
+        ls += s_l[tid * W + w];
+      }
+      if (n_parts > 1u) st8(mine + TR * D + 2 * tid, make_uint2(__float_as_uint(mx), __float_as_uint(ls)));
+      else finish_row(tid, mx, ls);
+    }
+    if (n_parts == 1u) cta_sync();
+    for (uint32_t c4 = tid; c4 < n_rows * (D / 4); c4 += threads) {
+      const uint32_t r = c4 / (D / 4), d4 = c4 % (D / 4);
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (uint32_t w = 0; w < W; ++w) {
+        const float4 a = *reinterpret_cast<const float4*>(s_o + (w * TR + r) * S::kOut + d4 * 4);
+        y.x += a.x; y.y += a.y; y.z += a.z; y.w += a.w;
+      }
+      if (n_parts > 1u)
+        st16(mine + c4 * 4, make_uint4(__float_as_uint(y.x), __float_as_uint(y.y), __float_as_uint(y.z), __float_as_uint(y.w)));
+      else finish_out(r, d4, y);
+    }
+    if (n_parts == 1u) continue;
+
+    // ---- the CTA that finishes last joins the job's partial results
+    cta_sync();
+    if (tid == 0) {
+      uint32_t last = 0;
+      KVC_GUARD(p.tickets + cta0, 4, last = 2);
+      if (last == 0) {
+        __threadfence();
+        last = atomicAdd(p.tickets + cta0, 1u) == n_parts - 1u ? 1u : 0u;
+        if (last) p.tickets[cta0] = 0;  // as the next call finds it
+        __threadfence();
+      }
+      *s_last = last;
+    }
+    cta_sync();
+    if (*s_last != 1u) continue;
+    for (uint32_t k = tid; k < n_parts * TR; k += threads)
+      s_ml[k] = k % TR < n_rows ? ld_join2(part_of(k / TR) + TR * D + 2 * (k % TR)) : make_float2(kNegInf, 0.0f);
+    cta_sync();
+    if (tid < 8u * TR) {  // 8 threads a row
+      const uint32_t row = tid >> 3, part = tid & 7u;
+      float mx = kNegInf, ls = 0.0f;
+      for (uint32_t k = part; k < n_parts; k += 8) mx = fmaxf(mx, s_ml[k * TR + row].x);
+#pragma unroll
+      for (int d = 1; d < 8; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+      for (uint32_t k = part; k < n_parts; k += 8) {
+        const float2 ml = s_ml[k * TR + row];
+        const float f = ml.x == kNegInf ? 0.0f : ex2(ml.x - mx);
+        ls += ml.y * f;
+        s_ml[k * TR + row].x = f;
+      }
+#pragma unroll
+      for (int d = 1; d < 8; d *= 2) ls += __shfl_xor_sync(0xffffffffu, ls, d);
+      if (part == 0) finish_row(row, mx, ls);
+    }
+    cta_sync();
+    // four dims a thread, all partials in order, 16 loads in flight
+    for (uint32_t c4 = tid; c4 < n_rows * (D / 4); c4 += threads) {
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (uint32_t k0 = 0; k0 < n_parts; k0 += 16) {
+        float4 a[16];
+#pragma unroll
+        for (uint32_t k = 0; k < 16; ++k)
+          if (k0 + k < n_parts) a[k] = ld_join4(part_of(k0 + k) + c4 * 4);
+#pragma unroll
+        for (uint32_t k = 0; k < 16; ++k)
+          if (k0 + k < n_parts) {
+            const float f = s_ml[(k0 + k) * TR + c4 / (D / 4)].x;
+            y.x += a[k].x * f;
+            y.y += a[k].y * f;
+            y.z += a[k].z * f;
+            y.w += a[k].w * f;
+          }
+      }
+      finish_out(c4 / (D / 4), c4 % (D / 4), y);
+    }
+  }
+}
+
+template <int DT, int D, bool PAGED16, int NT>
+int step_launch(const C16Params& p, uint32_t ctas, uint32_t warps, void* stream) {
+  const int bytes = smem16<D>((int)warps);
+  const auto kernel = c16_step_kernel<DT, D, PAGED16, NT>;
+  static std::atomic<uint64_t> done{0};
+  if (!allow_smem(kernel, smem16<D>(4), done)) return KV_ERR_CUDA;
+  return dbg_launch(
+      stream,
+      [&] {
+        kernel<<<ctas, warps * 32, bytes, (cudaStream_t)stream>>>(p);
+        return cudaGetLastError();
+      },
+      p);
+}
+
+template <int DT, int D>
+int step_d(const C16Params& p, uint32_t ctas, uint32_t warps, void* stream) {
+  if (p.T % 16 == 0)
+    return p.tile_rows == 8u ? step_launch<DT, D, true, 1>(p, ctas, warps, stream) : step_launch<DT, D, true, 2>(p, ctas, warps, stream);
+  return p.tile_rows == 8u ? step_launch<DT, D, false, 1>(p, ctas, warps, stream) : step_launch<DT, D, false, 2>(p, ctas, warps, stream);
+}
+
+}  // namespace
+
+int launch_c16_attend(const C16Params& p, uint32_t ctas, uint32_t warps, void* stream) {
+  KVC_C8_DISPATCH(step_d, p, ctas, warps, stream);
+}
+
+}  // namespace kvc

@@ -9,6 +9,7 @@
 #include <new>
 
 #include "cache8_internal.h"
+#include "cache_checks.h"
 
 struct kv_cache8_s {
   kvc::C8Params p;  // geometry part filled at create
@@ -16,21 +17,13 @@ struct kv_cache8_s {
 
 namespace {
 
+using kvc::accessible;
 using kvc::C8Params;
-
-// Whether the kernels can reach ptr (pageable host memory is refused, as for
-// the codec's buffers).
-int accessible(const void* ptr) {
-  if (!ptr) return KV_OK;
-  cudaPointerAttributes a;
-  if (cudaPointerGetAttributes(&a, ptr) != cudaSuccess) {
-    cudaGetLastError();
-    return KV_ERR_CUDA;
-  }
-  return a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged ? KV_OK : KV_ERR_NOT_ACCESSIBLE;
-}
-
-bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+using kvc::check_batch_fields;
+using kvc::check_out;
+using kvc::misaligned;
+using kvc::set_batch;
+using kvc::set_rows;
 
 int set_layer(C8Params& p, const kv_cache8_layer* y) {
   if (!y || !y->k || !y->v || !y->k_scale || !y->v_scale) return KV_ERR_INVALID_ARG;
@@ -45,57 +38,6 @@ int set_layer(C8Params& p, const kv_cache8_layer* y) {
   p.k_scale = y->k_scale;
   p.v_scale = y->v_scale;
   return KV_OK;
-}
-
-int check_batch_fields(const C8Params& p, const kv_cache8_batch* b) {
-  if (!b) return KV_ERR_INVALID_ARG;
-  if (b->struct_size != sizeof(kv_cache8_batch)) return KV_ERR_ABI;
-  if (b->n_seqs > KV_CACHE8_MAX_SEQS || b->n_new > 0x7fffffffu / p.G) return KV_ERR_INVALID_ARG;
-  if (!b->cu_new && b->n_new != b->n_seqs) return KV_ERR_INVALID_ARG;
-  if (b->n_seqs == 0 && b->n_new != 0) return KV_ERR_INVALID_ARG;
-  return KV_OK;
-}
-
-int set_batch(C8Params& p, const kv_cache8_batch* b) {
-  int rc = check_batch_fields(p, b);
-  if (rc != KV_OK) return rc;
-  if (!b->lens || (!b->tables && b->table_width) || b->table_stride < 0) return KV_ERR_INVALID_ARG;
-  if (b->n_seqs > 1 && b->table_stride < (int64_t)b->table_width) return KV_ERR_INVALID_ARG;
-  if (misaligned(b->tables, 4) || misaligned(b->lens, 4) || misaligned(b->cu_new, 4) || misaligned(b->errors, 4))
-    return KV_ERR_MISALIGNED;
-  for (const void* x : {(const void*)b->tables, (const void*)b->lens, (const void*)b->cu_new, (const void*)b->errors})
-    if ((rc = accessible(x)) != KV_OK) return rc;
-  p.n_seqs = b->n_seqs;
-  p.n_new = b->n_new;
-  p.table_width = b->table_width;
-  p.table_stride = b->table_stride;
-  p.tables = b->tables;
-  p.lens = b->lens;
-  p.cu = b->cu_new;
-  p.errors = b->errors;
-  return KV_OK;
-}
-
-int set_rows(const kv_cache8_rows* r, uint16_t*& data, int64_t& row, int64_t& head) {
-  if (!r || !r->data) return KV_ERR_INVALID_ARG;
-  if (misaligned(r->data, 16) || ((r->stride_row | r->stride_head) & 7)) return KV_ERR_MISALIGNED;
-  if (r->stride_row < 0 || r->stride_head < 0) return KV_ERR_LAYOUT_MISMATCH;
-  data = static_cast<uint16_t*>(r->data);
-  row = r->stride_row;
-  head = r->stride_head;
-  return accessible(r->data);
-}
-
-// Outputs: rows and heads must not overlap.
-int check_out(const C8Params& p, const kv_cache8_rows* r, uint32_t heads) {
-  const int64_t D = p.D;
-  const bool rows = p.n_new <= 1, one = heads <= 1;
-  if (!one && r->stride_head < D) return KV_ERR_LAYOUT_MISMATCH;
-  if (!rows && r->stride_row < D) return KV_ERR_LAYOUT_MISMATCH;
-  if (rows || one) return KV_OK;
-  const bool fits = r->stride_row >= r->stride_head * (int64_t)(heads - 1) + D ||
-                    r->stride_head >= r->stride_row * (int64_t)(p.n_new - 1) + D;
-  return fits ? KV_OK : KV_ERR_LAYOUT_MISMATCH;
 }
 
 // Pages that a sequence's new tokens touch number at most floor(c / T) + 2;
@@ -182,7 +124,7 @@ extern "C" {
 uint32_t kv_cache8_abi_version(void) { return KV_CACHE8_ABI_VERSION; }
 
 static_assert(sizeof(kv_cache8_geometry) == 64 && sizeof(kv_cache8_batch) == 64 && sizeof(kv_cache8_rows) == 24 &&
-                  sizeof(kv_cache8_layer) == 32,
+                  sizeof(kv_cache8_layer) == 32 && sizeof(kv_cache8_rotation) == 40,
               "public structures");
 
 int kv_cache8_create(const kv_cache8_geometry* g, kv_cache8_t* out) {
@@ -190,50 +132,16 @@ int kv_cache8_create(const kv_cache8_geometry* g, kv_cache8_t* out) {
   *out = nullptr;
   if (!g) return KV_ERR_INVALID_ARG;
   if (g->abi_version != KV_CACHE8_ABI_VERSION || g->struct_size != sizeof(kv_cache8_geometry)) return KV_ERR_ABI;
-  if (g->dtype != KV_DT_FP16 && g->dtype != KV_DT_BF16) return KV_ERR_INVALID_ARG;
-  const uint32_t D = g->head_dim;
-  if (D != 32 && D != 64 && D != 128 && D != 256) return KV_ERR_UNSUPPORTED_HEAD_DIM;
-  if (g->num_kv_heads == 0 || g->num_kv_heads > 4096 || g->num_q_heads == 0 ||
-      g->num_q_heads % g->num_kv_heads || g->num_q_heads / g->num_kv_heads > 64)
-    return KV_ERR_INVALID_ARG;
-  if (g->block_tokens == 0 || g->block_tokens > 32768 || g->num_blocks == 0 || g->num_blocks > 0x7fffffffull ||
-      g->reserved)
-    return KV_ERR_INVALID_ARG;
-  if (g->stride_block <= 0 || g->stride_token <= 0 || g->stride_head <= 0) return KV_ERR_LAYOUT_MISMATCH;
-  if ((g->stride_block | g->stride_token | g->stride_head) & 15) return KV_ERR_MISALIGNED;
-  // the smaller of the three strides steps over a value row, each next one over the extent of those before
-  struct {
-    uint64_t stride, n;
-  } d[3] = {{(uint64_t)g->stride_head, g->num_kv_heads},
-            {(uint64_t)g->stride_token, g->block_tokens},
-            {(uint64_t)g->stride_block, g->num_blocks}};
-  std::sort(d, d + 3, [](const auto& a, const auto& b) { return a.stride != b.stride ? a.stride < b.stride : a.n < b.n; });
-  uint64_t span = D;
-  for (const auto& x : d) {
-    if (x.n <= 1) continue;
-    if (x.stride < span || x.stride > (uint64_t(1) << 62) / (x.n - 1)) return KV_ERR_LAYOUT_MISMATCH;
-    span += x.stride * (x.n - 1);
-    if (span > (uint64_t(1) << 62)) return KV_ERR_LAYOUT_MISMATCH;
-  }
+  if (g->reserved) return KV_ERR_INVALID_ARG;
+  C8Params p;
+  std::memset(&p, 0, sizeof(p));
+  const int rc = kvc::set_pages(p, g->dtype, g->head_dim, g->num_kv_heads, g->num_q_heads, g->block_tokens, g->num_blocks,
+                                g->stride_block, g->stride_token, g->stride_head, 1);
+  if (rc != KV_OK) return rc;
   kv_cache8_s* h = new (std::nothrow) kv_cache8_s;
   if (!h) return KV_ERR_INVALID_ARG;
-  std::memset(h, 0, sizeof(*h));
-  C8Params& p = h->p;
-  p.dtype = g->dtype;
-  p.D = D;
-  p.H = g->num_kv_heads;
-  p.HQ = g->num_q_heads;
-  p.G = p.HQ / p.H;
-  p.T = g->block_tokens;
-  p.num_blocks = (uint32_t)g->num_blocks;
-  p.sb = g->stride_block;
-  p.st = g->stride_token;
-  p.sh = g->stride_head;
-  p.st2 = 2 * p.st;
-  p.stv = (int64_t)(512 / D) * p.st;
-  // n / T for n < 2^31 by the round-up method (Granlund and Montgomery, PLDI 1994)
-  while ((1u << p.t_shift) < p.T) ++p.t_shift;
-  p.t_magic = (uint32_t)((((uint64_t(1) << p.t_shift) - p.T) << 32) / p.T + 1);
+  p.stv = (int64_t)(512 / p.D) * p.st;
+  h->p = p;
   *out = h;
   return KV_OK;
 }
@@ -256,6 +164,25 @@ int kv_cache8_write(kv_cache8_t h, const kv_cache8_layer* layer, const kv_cache8
     return rc;
   p.n_units = page_units(p);
   return kvc::launch_c8_write(p, stream);
+}
+
+int kv_cache8_append(kv_cache8_t h, const kv_cache8_layer* layer, const kv_cache8_batch* batch,
+                     const kv_cache8_rows* k, const kv_cache8_rows* v, const kv_cache8_rotation* rotation,
+                     const kv_cache8_rows* q, const kv_cache8_rows* q_out, void* stream) {
+  if (!h) return KV_ERR_INVALID_ARG;
+  if (!rotation) return q || q_out ? KV_ERR_INVALID_ARG : kv_cache8_write(h, layer, batch, k, v, stream);
+  kvc::AppendParams p;
+  std::memset(&p, 0, sizeof(p));
+  static_cast<C8Params&>(p) = h->p;
+  int rc = check_batch_fields(p, batch);
+  if (rc != KV_OK) return rc;
+  if (batch->n_new == 0) return KV_OK;
+  if ((rc = set_batch(p, batch)) != KV_OK || (rc = set_layer(p, layer)) != KV_OK ||
+      (rc = set_rows(k, p.a, p.a_row, p.a_head)) != KV_OK || (rc = set_rows(v, p.b, p.b_row, p.b_head)) != KV_OK ||
+      (rc = kvc::set_rotation(p, rotation)) != KV_OK || (rc = kvc::set_queries(p, q, q_out)) != KV_OK)
+    return rc;
+  p.n_units = page_units(p);
+  return kvc::launch_c8_append(p, stream);
 }
 
 int kv_cache8_read(kv_cache8_t h, const kv_cache8_layer* layer, const kv_cache8_batch* batch,

@@ -1,5 +1,6 @@
-// cache8_internal.h -- launch parameters of the live 8-bit KV cache, shared by
-// the host library and the kernels.
+// cache8_internal.h -- launch parameters of the live 8-bit KV cache, and of the
+// live 16-bit cache that shares its batches and rows; for the host library and
+// the kernels.
 #pragma once
 #include <stdint.h>
 
@@ -17,6 +18,7 @@ constexpr uint32_t kPromptRows = 256;
 // Row tiles (times KV heads) whose keys may be split, of one call.  Their tickets take this much of every
 // workspace whatever the batch, so that what a call leaves behind them is never another call's ticket.
 constexpr uint32_t kTickets = 4096;
+constexpr uint32_t kC16Ctas = 2u * kC8Sms;  // CTAs of 16-bit attention at most: two an SM
 
 struct C8Params {
   // ---- registered geometry ----
@@ -58,6 +60,28 @@ struct C8Params {
   float* partials;              // [n_units][H][splits][kStepRows][D + 2]
 };
 
+// Appending with the position rotation, to 8-bit and (k, v: 16-bit pages, strides in bytes) 16-bit pages.
+struct AppendParams : C8Params {
+  const float* cos;             // [positions][R / 2]
+  const float* sin;
+  int64_t rot_stride;           // floats between positions
+  uint32_t R;                   // channels turned, a multiple of 16; 0: none
+  uint32_t positions;
+  uint32_t neighbours;          // pairs (2 i, 2 i + 1), else (i, i + R / 2)
+  const uint16_t* q;            // may be NULL, or q_out itself
+  uint16_t* q_out;
+  int64_t q_row, q_head, q_out_row, q_out_head;
+};
+
+// Attention over 16-bit pages (strides in bytes, scales NULL).
+struct C16Params : C8Params {
+  uint32_t tile_rows;           // rows of a tile: 8 where one token's query heads fit, else 16
+  uint32_t share;               // steps of a CTA at least
+};
+
+int launch_c8_append(const AppendParams& p, void* stream);
+int launch_c16_append(const AppendParams& p, void* stream);
+int launch_c16_attend(const C16Params& p, uint32_t ctas, uint32_t warps, void* stream);
 int launch_c8_write(const C8Params& p, void* stream);
 int launch_c8_read(const C8Params& p, void* stream);
 int launch_c8_step(const C8Params& p, void* stream);

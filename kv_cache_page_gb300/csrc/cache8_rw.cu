@@ -13,57 +13,13 @@
 // GPU all the same; and conversions, which stay in FP16 where that is exact.
 // Measured on a GB300, 4 x 8192 tokens of 8 heads of 128 in FP16: written and read
 // back in 37 us (5.4 and 5.5 TB/s of 3 bytes a value; a plain copy 6.7).
-#include "cache8_common.cuh"
+#include "cache8_page.cuh"
 
 namespace kvc {
 namespace {
 
 
-constexpr int kExpMin = -60, kExpMax = 119;
 constexpr int kWarps = 8;
-
-// The smallest 2^e with amax <= 448 * 2^e.  448 = 1.75 * 2^8: with amax = f 2^k,
-// 1 <= f < 2, e is k - 8 for f <= 1.75, else k - 7.
-__device__ __forceinline__ float page_scale(float amax) {
-  const uint32_t b = __float_as_uint(amax);
-  const int k = (int)(b >> 23) - 127;
-  int e = k - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
-  e = min(max(e, kExpMin), kExpMax);  // amax = 0 and FP32 subnormals have k = -127
-  return __uint_as_float((uint32_t)(e + 127) << 23);
-}
-
-// Where a warp works: role, head, page and the range of its tokens.
-struct PageJob {
-  C8Seq q;
-  uint32_t role, roles, head;  // first role and how many
-  int32_t page;       // index within the sequence
-  int32_t t0, t1;     // tokens of the page that are new
-  int32_t id;         // page id, -1: none
-  int64_t row0;       // row of token 0 of the page (negative where it has none)
-};
-
-__device__ __forceinline__ bool page_job(const C8Params& p, uint32_t warp, PageJob& j) {
-  const uint32_t per = p.both_roles ? p.H : 2u * p.H;
-  const uint32_t u = warp / per, r = warp - u * per;
-  if (u >= p.n_units) return false;
-  j.role = r >= p.H ? 1u : 0u;
-  j.roles = p.both_roles ? 2u : 1u;
-  j.head = r - j.role * p.H;
-  j.q = c8_find(p, u, 1u, p.T, 2u, p.cu ? 0u : 1u);
-  const int32_t T = (int32_t)p.T;
-  j.page = (int32_t)(c8_div_t(p, (uint32_t)max(j.q.start, 0)) + j.q.unit);
-  const int64_t first = (int64_t)j.page * T;
-  j.t0 = (int32_t)max((int64_t)max(j.q.start, 0) - first, (int64_t)0);
-  j.t1 = (int32_t)min((int64_t)j.q.len - first, (int64_t)T);
-  j.row0 = (int64_t)j.q.row + (first - j.q.start);
-  j.id = -1;
-  if (j.t0 < j.t1 && j.q.n_new > 0) {
-    j.id = c8_page(p, j.q.s, (uint32_t)j.page);
-    if (j.id < 0 && r == 0u && (threadIdx.x & 31u) == 0u) c8_error(p, j.q.s, KV_CACHE8_BAD_PAGE);
-    return true;
-  }
-  return j.q.n_new > 0;
-}
 
 // The largest finite magnitude of packed 16-bit values, two running maxima per
 // word; NaN operands are ignored, infinities are not (drop_nonfinite2 takes them out).
@@ -103,15 +59,6 @@ __device__ __forceinline__ uint32_t enc_h4(uint32_t a, uint32_t b) {
       : "=r"(d)
       : "r"(a), "r"(b));
   return d;
-}
-
-// The scale that a page held: an ordinary load, because the same kernel stores there
-// (this warp alone, what it makes of the value; so the load needs no other order).
-__device__ __forceinline__ float ld_held_f32(const float* ptr) {
-  KVC_GUARD(ptr, 4, return 0.0f);
-  float v;
-  asm("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(ptr));
-  return v;
 }
 
 // R: 16-byte chunks of new values a lane holds; a page with more new tokens
