@@ -137,7 +137,7 @@ int kv_cache16_attend(kv_cache16_t h, const kv_cache16_layer* layer, const kv_ca
   if (window) keys = std::min<uint64_t>(keys, (uint64_t)window + (batch->max_new ? batch->max_new : p.n_new) + 15u);
   const uint64_t tiles = !p.cu ? (uint64_t)p.n_seqs * ((p.G + p.tile_rows - 1u) / p.tile_rows)
                                : (uint64_t)p.n_new * p.G / p.tile_rows + p.n_seqs;
-  const uint64_t steps = tiles * p.H * ((keys + tokens - 1u) / tokens + 1u);
+  const uint64_t steps = tiles * p.H * ((keys + tokens - 1u) / tokens + 12u);
   const uint32_t per_sm = p.D == 256u ? 1u : 2u;
   p.share = 16u;
   const uint64_t ctas = std::min<uint64_t>((uint64_t)kvc::kC8Sms * per_sm, (steps + p.share - 1u) / p.share);

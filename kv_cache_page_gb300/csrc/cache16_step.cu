@@ -105,14 +105,15 @@ __device__ __forceinline__ void cp16z(uint32_t smem, const void* src, bool ok) {
   const uint32_t n = ok ? 16u : 0u;
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(src), "r"(n) : "memory");
 }
-__device__ __forceinline__ void cp16(uint32_t smem, const void* src) {
-  KVC_GUARD(src, 16, return);
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(src) : "memory");
-}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void cp16(uint32_t smem, const void* src) {
+  KVC_GUARD(src, 16, return);
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(src) : "memory");
 }
 
 // loads of what other CTAs of this launch have stored (L2)
@@ -127,27 +128,25 @@ __device__ __forceinline__ float4 ld_join4(const float* ptr) {
 
 template <int D>
 struct Shape16 {
-  static constexpr int TS = D >= 128 ? 16 : 32;  // tokens of a step
+  static constexpr int TS = D >= 128 ? 16 : 32;    // tokens of a step
   static constexpr int HT = TS / 16;
-  static constexpr int C = D / 8;                // 16-byte chunks of a row
-  static constexpr int RPI = 32 / C;             // rows that a warp's copy instruction covers
-  static constexpr int kTile = 16 * D * 2;       // 16 tokens of K, or of V
-  static constexpr int kStage = 2 * HT * kTile;  // K tiles, then V tiles
+  static constexpr int C = D / 8;                  // 16-byte chunks of a row
+  static constexpr int RPI = 32 / C;               // rows that a warp's copy instruction covers
+  // Rows lie an odd number of chunks apart: 8 rows' chunks of one column are in 8 different bank groups.
+  static constexpr int kPitch = D * 2 + 16;
+  static constexpr int kStage = 2 * TS * kPitch;   // K's rows, then V's
   static constexpr int NS = D == 32 ? 4 : 3;
-  static constexpr int kQ = 16 * D * 2;
+  static constexpr int kQ = 16 * kPitch;
   static constexpr int kSmall = 2048;
-  static constexpr int kOut = D + 4;             // floats of a row in the join of the warps
+  static constexpr int kOut = D + 4;               // floats of a row in the join of the warps
+  static constexpr int kWarps = D == 256 ? 4 : 8;  // the most whose slots fit
+  // What a job costs its CTA besides its steps (finding it, its first copies, the join), in steps: some 5 us.
+  static constexpr uint32_t kStart = D == 256 ? 8 : D == 32 ? 16 : 12;
 };
 template <int D>
 constexpr int smem16(int warps) {
   using S = Shape16<D>;
   return S::kQ + S::kSmall + warps * S::NS * S::kStage;
-}
-
-// 8 consecutive rows of one chunk lie in 8 different bank groups: chunk c of row t is at c ^ swz(t).
-template <int D>
-__device__ __forceinline__ uint32_t swz(uint32_t t) {
-  return D == 32 ? (t >> 1) & 3u : t & 7u;
 }
 
 // A sequence of the batch, and how many steps its jobs have.
@@ -156,9 +155,15 @@ struct Seq16 {
   int32_t lo, hi;   // keys that some row sees; lo at a 16-token tile where pages are whole tiles
   bool past;        // tokens lie past the table's row
   uint32_t steps;   // of a job
-  uint64_t all;     // of all jobs
+  uint64_t all;     // of all jobs, each with kStart besides
 };
-template <int TS, bool PAGED16>
+// a / b, where both fit 32 bits as they mostly do without the long division
+__device__ __forceinline__ uint64_t div64(uint64_t a, uint64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
+template <int D, bool PAGED16>
 __device__ __forceinline__ Seq16 seq16(const C16Params& p, uint32_t s) {
   Seq16 x;
   x.q.s = s;
@@ -171,16 +176,17 @@ __device__ __forceinline__ Seq16 seq16(const C16Params& p, uint32_t s) {
   x.hi = x.past ? (int32_t)reach : x.q.len;
   x.lo = p.window && x.q.start >= 0 ? max(0, x.q.start - (int32_t)min(p.window, 0x7fffffffu) + 1) : 0;
   if (PAGED16) x.lo &= ~15;
+  constexpr int TS = Shape16<D>::TS;
   x.steps = x.hi > x.lo ? ((uint32_t)(x.hi - x.lo) + TS - 1u) / TS : 1u;  // (rows that see nothing are a step)
   const uint32_t tiles = ((uint32_t)x.q.n_new * p.G + p.tile_rows - 1u) / p.tile_rows;
-  x.all = (uint64_t)x.steps * tiles * p.H;
+  x.all = (uint64_t)(x.steps + Shape16<D>::kStart) * tiles * p.H;
   return x;
 }
 
 // PAGED16: pages are whole 16-token tiles, so a tile lies in one page; otherwise every token's page is
 // looked up by itself.  NT: 8-row column blocks of a row tile.
 template <int DT, int D, bool PAGED16, int NT>
-__global__ void __launch_bounds__(128) c16_step_kernel(const __grid_constant__ C16Params p) {
+__global__ void __launch_bounds__(Shape16<D>::kWarps * 32, 1) c16_step_kernel(const __grid_constant__ C16Params p) {
   using S = Shape16<D>;
   constexpr int NS = S::NS, TS = S::TS, HT = S::HT, TR = 8 * NT, KS = D / 16;
   constexpr uint32_t kFull = TS == 32 ? 0xffffffffu : 0xffffu;
@@ -201,13 +207,14 @@ __global__ void __launch_bounds__(128) c16_step_kernel(const __grid_constant__ C
   const uint32_t my_slots = sm_q + S::kQ + S::kSmall + warp * (NS * S::kStage);
 
   // ---- this CTA's share of all steps
-  uint64_t at, end, share;  // steps, counted over all jobs
+  // Counted over all jobs one after the other, kStart for each before its steps.
+  uint64_t at, end, share;
   uint32_t s;
-  uint64_t base;            // where sequence s begins
+  uint64_t base;  // where sequence s begins
   {
     const uint32_t per = (p.n_seqs + threads - 1u) / threads, i0 = min(tid * per, p.n_seqs), i1 = min(i0 + per, p.n_seqs);
     unsigned long long mine = 0;
-    for (uint32_t i = i0; i < i1; ++i) mine += seq16<TS, PAGED16>(p, i).all;
+    for (uint32_t i = i0; i < i1; ++i) mine += seq16<D, PAGED16>(p, i).all;
     unsigned long long inc = mine;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -221,7 +228,7 @@ __global__ void __launch_bounds__(128) c16_step_kernel(const __grid_constant__ C
       before += w < warp ? s_tot[w] : 0ull;
       total += s_tot[w];
     }
-    share = max((total + gridDim.x - 1u) / gridDim.x, (unsigned long long)p.share);
+    share = max((unsigned long long)div64(total + gridDim.x - 1u, gridDim.x), (unsigned long long)p.share);
     at = (uint64_t)blockIdx.x * share;
     if (at >= total) return;
     end = min(at + share, (uint64_t)total);
@@ -229,7 +236,7 @@ __global__ void __launch_bounds__(128) c16_step_kernel(const __grid_constant__ C
     if (pre <= at && at < pre + mine) {
       uint32_t i = i0;
       for (;; ++i) {
-        const uint64_t n = seq16<TS, PAGED16>(p, i).all;
+        const uint64_t n = seq16<D, PAGED16>(p, i).all;
         if (at < pre + n) break;
         pre += n;
       }
@@ -241,26 +248,27 @@ __global__ void __launch_bounds__(128) c16_step_kernel(const __grid_constant__ C
     s = (uint32_t)s_tot[9];
   }
 
-  // what of a tile's copies and fragments belongs to this lane (byte offsets within a tile, chunks swizzled)
+  // this lane's place in the copies and the fragments of a tile
   const uint32_t c_row = lane / S::C, c_chunk = lane % S::C;
-  const uint32_t c_dst = c_row * (D * 2) + ((c_chunk ^ swz<D>(c_row)) << 4);
-  const uint32_t k_at = (lane & 15u) * (D * 2) + (((lane >> 4) ^ swz<D>(lane & 15u)) << 4);
-  const uint32_t v_row = (lane & 7u) + ((lane >> 4) << 3);
-  const uint32_t v_at = v_row * (D * 2) + ((((lane >> 3) & 1u) ^ swz<D>(v_row)) << 4);
+  const uint32_t c_dst = my_slots + c_row * S::kPitch + c_chunk * 16;
+  const uint32_t k_at = my_slots + (lane & 15u) * S::kPitch + ((lane >> 4) << 4);
+  const uint32_t v_at = my_slots + (TS + (lane & 7u) + ((lane >> 4) << 3)) * S::kPitch + (((lane >> 3) & 1u) << 4);
 
-  Seq16 x = seq16<TS, PAGED16>(p, s);
+  Seq16 x = seq16<D, PAGED16>(p, s);
   while (at < end) {
     while (at >= base + x.all) {  // (a sequence without new tokens has no steps)
       base += x.all;
-      x = seq16<TS, PAGED16>(p, ++s);
+      x = seq16<D, PAGED16>(p, ++s);
     }
-    const uint64_t job = (at - base) / x.steps;
-    const uint32_t step0 = (uint32_t)(at - base - job * x.steps);
-    const uint32_t n_steps = (uint32_t)min((uint64_t)(x.steps - step0), end - at);
-    const uint32_t tile = (uint32_t)(job / p.H), head = (uint32_t)(job - (uint64_t)tile * p.H);
-    const uint64_t job0 = base + job * x.steps;
-    const uint32_t cta0 = (uint32_t)(job0 / share), n_parts = (uint32_t)((job0 + x.steps - 1u) / share) - cta0 + 1u;
-    at += n_steps;
+    const uint32_t len = x.steps + S::kStart;
+    const uint64_t job = div64(at - base, len), job0 = base + job * len;
+    const uint32_t from = (uint32_t)(at - job0), to = (uint32_t)min((uint64_t)len, end - job0);
+    at = job0 + to;
+    // the steps of [from, to), kStart of which are none
+    const uint32_t step0 = max(from, S::kStart) - S::kStart, n_steps = max(to, S::kStart) - S::kStart - step0;
+    if (n_steps == 0u) continue;  // the CTA after this one begins the job
+    const uint32_t tile = (uint32_t)div64(job, p.H), head = (uint32_t)(job - (uint64_t)tile * p.H);
+    const uint32_t cta0 = (uint32_t)div64(job0 + S::kStart, share), n_parts = (uint32_t)div64(job0 + len - 1u, share) - cta0 + 1u;
 
     const uint32_t r0 = tile * TR, n_rows = min((uint32_t)TR, (uint32_t)x.q.n_new * p.G - r0);
     const int32_t first_pos = x.q.start + (int32_t)(r0 / p.G), last_pos = x.q.start + (int32_t)((r0 + n_rows - 1u) / p.G);
@@ -283,7 +291,7 @@ __global__ void __launch_bounds__(128) c16_step_kernel(const __grid_constant__ C
     // Start the copies of step t.  Tokens that no row sees, and those without a page, become zeros.  Returns the
     // tokens that are there, a bit each.
     auto issue = [&](int32_t t, int stage, int32_t entry) -> uint32_t {
-      const uint32_t dst = my_slots + stage * S::kStage + c_dst;
+      const uint32_t dst = c_dst + stage * S::kStage;
       const int32_t tok = x.lo + TS * t + (int32_t)(lane % TS);
       const bool in = tok >= t_lo && tok < t_hi, page = (uint32_t)entry < p.num_blocks;
       bad |= in && !page;
@@ -298,21 +306,19 @@ __global__ void __launch_bounds__(128) c16_step_kernel(const __grid_constant__ C
           const uint8_t *ks = k_src + tile_off, *vs = v_src + tile_off;
 #pragma unroll
           for (int i = 0; i < 16 / S::RPI; ++i) {
-            const uint32_t to = (dst ^ (swz<D>(S::RPI * i) << 4)) + h * S::kTile + i * S::RPI * (D * 2);
-            cp16(to, ks);
-            cp16(to + HT * S::kTile, vs);
+            cp16(dst + (16 * h + i * S::RPI) * S::kPitch, ks);
+            cp16(dst + (TS + 16 * h + i * S::RPI) * S::kPitch, vs);
             ks += S::RPI * p.st;
             vs += S::RPI * p.st;
           }
         } else {
-#pragma unroll
+#pragma unroll 4
           for (int i = 0; i < 16 / S::RPI; ++i) {
-            const uint32_t to = (dst ^ (swz<D>(S::RPI * i) << 4)) + h * S::kTile + i * S::RPI * (D * 2);
             const uint32_t row = c_row + S::RPI * i;
             const bool ok = (bits >> row) & 1u;
             const int64_t o = PAGED16 ? tile_off + (int64_t)(S::RPI * i) * p.st : __shfl_sync(0xffffffffu, off, 16 * h + row);
-            cp16z(to, ok ? k_src + o : p.k, ok);
-            cp16z(to + HT * S::kTile, ok ? v_src + o : p.v, ok);
+            cp16z(dst + (16 * h + i * S::RPI) * S::kPitch, ok ? k_src + o : p.k, ok);
+            cp16z(dst + (TS + 16 * h + i * S::RPI) * S::kPitch, ok ? v_src + o : p.v, ok);
           }
         }
       }
@@ -327,10 +333,10 @@ __global__ void __launch_bounds__(128) c16_step_kernel(const __grid_constant__ C
 #pragma unroll
       for (int i = 0; i < NS - 1; ++i) e[i] = entry_of(x_lo + (int32_t)(warp + i * W));
       entry = entry_of(x_lo + (int32_t)(warp + (NS - 1) * W));
-      for (uint32_t i = tid; i < TR * S::C; i += threads) {
-        const uint32_t r = i / S::C, c = i % S::C, rr = r0 + min(r, n_rows - 1u), tok = rr / p.G;
+      for (uint32_t i = tid; i < TR * (D / 8); i += threads) {
+        const uint32_t r = i / (D / 8), c = i % (D / 8), rr = r0 + min(r, n_rows - 1u), tok = rr / p.G;
         const uint16_t* src = p.a + ((int64_t)x.q.row + tok) * p.a_row + (int64_t)(head * p.G + rr - tok * p.G) * p.a_head + c * 8;
-        cp16z(sm_q + r * (D * 2) + ((c ^ swz<D>(r)) << 4), src, r < n_rows);
+        cp16z(sm_q + r * S::kPitch + c * 16, src, r < n_rows);
       }
       cp_commit();
 #pragma unroll
@@ -342,19 +348,16 @@ __global__ void __launch_bounds__(128) c16_step_kernel(const __grid_constant__ C
     }
     cp_wait<NS - 1>();  // the queries
     cta_sync();
-    uint32_t qf[NT][KS][2];
+    // the queries' fragments: in registers, or (where the sums leave no room) read again at each step
+    constexpr bool kHeld = D < 256;
+    const uint32_t q_at = sm_q + (lane & 7u) * S::kPitch + ((lane >> 3) << 4);
+    uint32_t qf[kHeld ? NT : 1][kHeld ? KS / 2 : 1][4];
+    if constexpr (kHeld) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int k = 0; k < KS / 2; ++k) {
-        const uint32_t row = 8u * n + (lane & 7u);
-        uint32_t w[4];
-        ldsm4(w, (sm_q + row * (D * 2) + (((lane >> 3) ^ swz<D>(row)) << 4)) ^ (k << 6));
-        qf[n][2 * k][0] = w[0];
-        qf[n][2 * k][1] = w[1];
-        qf[n][2 * k + 1][0] = w[2];
-        qf[n][2 * k + 1][1] = w[3];
-      }
+        for (int k = 0; k < KS / 2; ++k) ldsm4(qf[n][k], q_at + n * 8 * S::kPitch + k * 64);
+    }
     // steps between these need no mask by rows
     const int32_t full_hi = !several ? 0x7fffffff : first_pos < 0 ? 0 : p.causal ? first_pos + 1 : 0x7fffffff;
     const int32_t full_lo = several && p.window ? (int32_t)max((int64_t)0, (int64_t)last_pos - p.window + 1) : 0;
@@ -384,33 +387,46 @@ __global__ void __launch_bounds__(128) c16_step_kernel(const __grid_constant__ C
         __syncwarp();  // the other lanes' copies
       }
       const uint32_t bits = there[0];
+      const uint32_t sk = k_at + stage * S::kStage, sv = v_at + stage * S::kStage;
 #pragma unroll
       for (int i = 0; i < NS - 1; ++i) there[i] = there[i + 1];
-      const uint32_t sk = my_slots + stage * S::kStage + k_at, sv = my_slots + stage * S::kStage + HT * S::kTile + v_at;
       stage = stage == NS - 1 ? 0 : stage + 1;
       const int32_t tok0 = x.lo + TS * t;
 
       // scores of tokens 16 h + g, + 8 and rows 8 n + 2 qd, + 1
+      constexpr int Z = HT * NT == 1 ? 2 : 1;  // chains of products that do not wait for each other
       float z[HT][NT][4];
 #pragma unroll
       for (int h = 0; h < HT; ++h) {
+        float y[Z][NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) z[h][n][0] = z[h][n][1] = z[h][n][2] = z[h][n][3] = 0.0f;
+        for (int c = 0; c < Z; ++c)
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          uint32_t a[4];
-          ldsm4(a, (sk ^ (k << 5)) + h * S::kTile);
+          for (int n = 0; n < NT; ++n) y[c][n][0] = y[c][n][1] = y[c][n][2] = y[c][n][3] = 0.0f;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma16816<DT>(z[h][n], a, qf[n][k][0], qf[n][k][1]);
+        for (int k = 0; k < KS / 2; ++k) {
+          uint32_t a[4], b[4], w[NT][4];
+          ldsm4(a, sk + h * 16 * S::kPitch + k * 64);
+          ldsm4(b, sk + h * 16 * S::kPitch + k * 64 + 32);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if constexpr (kHeld) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) w[n][i] = qf[n][k][i];
+            } else {
+              ldsm4(w[n], q_at + n * 8 * S::kPitch + k * 64);
+            }
+            mma16816<DT>(y[0][n], a, w[n][0], w[n][1]);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma16816<DT>(y[Z - 1][n], b, w[n][2], w[n][3]);
         }
-      }
-      const bool by_row = tok0 + TS > full_hi || tok0 < full_lo;
-#pragma unroll
-      for (int h = 0; h < HT; ++h)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) z[h][n][e] *= p.scale_log2;
+          for (int e = 0; e < 4; ++e) z[h][n][e] = (Z == 2 ? y[0][n][e] + y[Z - 1][n][e] : y[0][n][e]) * p.scale_log2;
+      }
+      const bool by_row = tok0 + TS > full_hi || tok0 < full_lo;
       if (by_row || bits != kFull) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -482,33 +498,34 @@ __global__ void __launch_bounds__(128) c16_step_kernel(const __grid_constant__ C
           }
       }
       // V: dims 16 i + g, + 8 of tokens 2 qd, + 1, + 8, + 9
-      uint32_t odd = 0;
-#pragma unroll
-      for (int h = 0; h < HT; ++h)
-#pragma unroll
-        for (int i = 0; i < KS; ++i) {
+      constexpr uint32_t E = DT == 0 ? 0x7c00u : 0x7f80u, one = DT == 0 ? 0x3c00u : 0x3f80u;
+      bool odd = false;
+      if (by_row) {
+        // an infinity or a NaN that some row does not see must not reach it through 0 times it
+#pragma unroll 1
+        for (int i = 0; i < HT * KS; ++i) {
           uint32_t a[4];
-          ldsm4_t(a, (sv ^ (i << 5)) + h * S::kTile);
-          if (by_row) {
-            // an infinity or a NaN that some row does not see must not reach it through 0 times it: such values
-            // become 0 here, and NaN is put below where they are seen
-            constexpr uint32_t E = DT == 0 ? 0x7c00u : 0x7f80u;
+          ldsm4_t(a, sv + (i / KS) * 16 * S::kPitch + (i % KS) * 32);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t lo = (a[k] & E) == E ? 0xffffu : 0u, hi = (a[k] & (E << 16)) == (E << 16) ? 0xffff0000u : 0u;
-              odd |= lo | hi;
-              a[k] &= ~(lo | hi);
+          for (int k = 0; k < 4; ++k) odd |= (a[k] & E) == E || (a[k] & (E << 16)) == (E << 16);
+        }
+        odd = __any_sync(0xffffffffu, odd);
+      }
+      if (!odd) {
+#pragma unroll
+        for (int h = 0; h < HT; ++h)
+#pragma unroll
+          for (int i = 0; i < KS; ++i) {
+            uint32_t a[4];
+            ldsm4_t(a, sv + h * 16 * S::kPitch + i * 32);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma16816<DT>(o[i][n], a, wh[h][n][0], wh[h][n][1]);
+              mma16816<DT>(o[i][n], a, wl[h][n][0], wl[h][n][1]);
             }
           }
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma16816<DT>(o[i][n], a, wh[h][n][0], wh[h][n][1]);
-            mma16816<DT>(o[i][n], a, wl[h][n][0], wl[h][n][1]);
-          }
-        }
-      if (by_row && __any_sync(0xffffffffu, odd != 0u)) {
-        // rows x dims where a visible token's value is one: count them with the same product
-        constexpr uint32_t E = DT == 0 ? 0x7c00u : 0x7f80u, one = DT == 0 ? 0x3c00u : 0x3f80u;
+      } else {
+        // such values become 0, and NaN is put where they are seen: rows x dims with one, counted by the same product
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
           uint32_t seen[NT][2];
@@ -519,15 +536,20 @@ __global__ void __launch_bounds__(128) c16_step_kernel(const __grid_constant__ C
               seen[n][e] = transpose8((z[h][n][2 * e] == kNegInf ? 0u : one) | (z[h][n][2 * e + 1] == kNegInf ? 0u : one << 16));
 #pragma unroll
           for (int i = 0; i < KS; ++i) {
-            uint32_t a[4];
-            ldsm4_t(a, (sv ^ (i << 5)) + h * S::kTile);
+            uint32_t a[4], b[4];
+            ldsm4_t(a, sv + h * 16 * S::kPitch + i * 32);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              a[k] = ((a[k] & E) == E ? one : 0u) | ((a[k] & (E << 16)) == (E << 16) ? one << 16 : 0u);
+            for (int k = 0; k < 4; ++k) {
+              const bool lo = (a[k] & E) == E, hi = (a[k] & (E << 16)) == (E << 16);
+              b[k] = (lo ? one : 0u) | (hi ? one << 16 : 0u);
+              a[k] &= (lo ? 0u : 0xffffu) | (hi ? 0u : 0xffff0000u);
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
+              mma16816<DT>(o[i][n], a, wh[h][n][0], wh[h][n][1]);
+              mma16816<DT>(o[i][n], a, wl[h][n][0], wl[h][n][1]);
               float cnt[4] = {0.f, 0.f, 0.f, 0.f};
-              mma16816<DT>(cnt, a, seen[n][0], seen[n][1]);
+              mma16816<DT>(cnt, b, seen[n][0], seen[n][1]);
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 if (cnt[e] > 0.0f) o[i][n][e] = __int_as_float(0x7fffffff);
@@ -622,10 +644,10 @@ __global__ void __launch_bounds__(128) c16_step_kernel(const __grid_constant__ C
       uint32_t last = 0;
       KVC_GUARD(p.tickets + cta0, 4, last = 2);
       if (last == 0) {
-        __threadfence();
-        last = atomicAdd(p.tickets + cta0, 1u) == n_parts - 1u ? 1u : 0u;
+        // releases this CTA's partial (the barrier above put it before), acquires the others'
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(last) : "l"(p.tickets + cta0) : "memory");
+        last = last == n_parts - 1u ? 1u : 0u;
         if (last) p.tickets[cta0] = 0;  // as the next call finds it
-        __threadfence();
       }
       *s_last = last;
     }
@@ -676,14 +698,13 @@ __global__ void __launch_bounds__(128) c16_step_kernel(const __grid_constant__ C
 
 template <int DT, int D, bool PAGED16, int NT>
 int step_launch(const C16Params& p, uint32_t ctas, uint32_t warps, void* stream) {
-  const int bytes = smem16<D>((int)warps);
   const auto kernel = c16_step_kernel<DT, D, PAGED16, NT>;
   static std::atomic<uint64_t> done{0};
-  if (!allow_smem(kernel, smem16<D>(4), done)) return KV_ERR_CUDA;
+  if (!allow_smem(kernel, smem16<D>(Shape16<D>::kWarps), done)) return KV_ERR_CUDA;
   return dbg_launch(
       stream,
       [&] {
-        kernel<<<ctas, warps * 32, bytes, (cudaStream_t)stream>>>(p);
+        kernel<<<ctas, warps * 32, smem16<D>((int)warps), (cudaStream_t)stream>>>(p);
         return cudaGetLastError();
       },
       p);
