@@ -12,6 +12,7 @@ namespace kvc {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr uint32_t kQueries = 4;     // iterations of a queries' warp: 128 bytes of loads in flight a lane
 constexpr uint32_t kIterations = 2;  // of K and V each: 128 bytes of loads in flight a lane
 
 struct Append16 : AppendParams {
@@ -40,7 +41,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) c16_append_kernel(const __grid
   constexpr uint32_t U = D / 16, C = D / 8, I = kIterations;
   const uint32_t lane = threadIdx.x & 31u;
   if (blockIdx.x >= p.kv_blocks)
-    return append_queries<DT, D>(p, p.qm, (blockIdx.x - p.kv_blocks) * kWarps + (threadIdx.x >> 5));
+    return append_queries<DT, D, kQueries>(p, p.qm, (blockIdx.x - p.kv_blocks) * kWarps + (threadIdx.x >> 5));
   const RowMap& m = p.kv;
   const uint32_t warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (warp >= m.warps) return;
@@ -102,7 +103,7 @@ int append_d(const AppendParams& p, void* stream) {
   Append16 a;
   static_cast<AppendParams&>(a) = p;
   a.kv = row_map(p.n_new, p.H * (D / 16), kIterations);
-  a.qm = row_map(p.q ? p.n_new : 0u, p.HQ * (D / 16), kQueryIterations);
+  a.qm = row_map(p.q ? p.n_new : 0u, p.HQ * (D / 16), kQueries);
   if (a.kv.warps == 0xffffffffu || a.qm.warps == 0xffffffffu) return KV_ERR_INVALID_ARG;
   a.kv_blocks = (a.kv.warps + kWarps - 1u) / kWarps;
   const uint64_t grid = a.kv_blocks + (uint64_t)((a.qm.warps + kWarps - 1u) / kWarps);

@@ -1,5 +1,4 @@
-// cache16_host.cpp -- the C ABI of the live 16-bit KV cache: validation, and the size of
-// attention's grid.
+// cache16_host.cpp -- the C ABI of the live 16-bit KV cache: validation.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -127,21 +126,18 @@ int kv_cache16_attend(kv_cache16_t h, const kv_cache16_layer* layer, const kv_ca
   p.window = window;
   p.causal = flags & KV_CACHE8_CAUSAL;
   p.tile_rows = tile_rows(p, batch);
+  while ((1u << p.g_shift) < p.G) ++p.g_shift;  // as for n / T
+  p.g_magic = (uint32_t)((((uint64_t(1) << p.g_shift) - p.G) << 32) / p.G + 1);
   p.tickets = static_cast<uint32_t*>(workspace);
   p.partials = reinterpret_cast<float*>(p.tickets + kvc::kTickets);
 
-  // The most steps that the batch may have by its host fields; the device finds how many it has.
-  const uint32_t tokens = p.D >= 128u ? 16u : 32u;
+  // the most jobs and keys that the batch may have
   const uint64_t reach = std::min<uint64_t>((uint64_t)p.table_width * p.T, 0x7fff0000u);
   uint64_t keys = batch->max_len ? std::min<uint64_t>(batch->max_len, reach) : reach;
-  if (window) keys = std::min<uint64_t>(keys, (uint64_t)window + (batch->max_new ? batch->max_new : p.n_new) + 15u);
+  if (window) keys = std::min<uint64_t>(keys, (uint64_t)window + (batch->max_new ? batch->max_new : p.n_new));
   const uint64_t tiles = !p.cu ? (uint64_t)p.n_seqs * ((p.G + p.tile_rows - 1u) / p.tile_rows)
                                : (uint64_t)p.n_new * p.G / p.tile_rows + p.n_seqs;
-  const uint64_t steps = tiles * p.H * ((keys + tokens - 1u) / tokens + 12u);
-  const uint32_t per_sm = p.D == 256u ? 1u : 2u;
-  p.share = 16u;
-  const uint64_t ctas = std::min<uint64_t>((uint64_t)kvc::kC8Sms * per_sm, (steps + p.share - 1u) / p.share);
-  return kvc::launch_c16_attend(p, (uint32_t)ctas, 4u, stream);
+  return kvc::launch_c16_attend(p, tiles * p.H, keys, stream);
 }
 
 }  // extern "C"

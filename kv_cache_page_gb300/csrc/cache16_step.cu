@@ -21,6 +21,8 @@
 // and the weights pass through a transposition in registers.  A weight is split into two
 // 16-bit terms (the second product is made twice): with one, BF16 weights alone would be as
 // coarse as the output's rounding.
+#include <algorithm>
+
 #include "cache8_common.cuh"
 
 namespace kvc {
@@ -38,7 +40,7 @@ inline void dbg_ranges(DbgRanges& r, const C16Params& p) {
   dbg_rows(r, p.a, p.a_row, p.a_head, p, p.HQ);
   dbg_rows(r, p.b, p.b_row, p.b_head, p, p.HQ);
   if (p.lse) dbg_add(r, p.lse, 4ull * p.n_new * p.HQ);
-  dbg_add(r, p.tickets, 4ull * kC16Ctas);
+  dbg_add(r, p.tickets, 4ull * 3u * kC16Ctas);
   dbg_add(r, p.partials, 4ull * kC16Ctas * 2u * kStepRows * (p.D + 2u));
 }
 #endif
@@ -117,14 +119,24 @@ __device__ __forceinline__ void cp16(uint32_t smem, const void* src) {
 }
 
 // loads of what other CTAs of this launch have stored (L2)
-__device__ __forceinline__ float2 ld_join2(const float* ptr) {
-  KVC_GUARD(ptr, 8, return make_float2(0.f, 0.f));
-  return __ldcg(reinterpret_cast<const float2*>(ptr));
-}
 __device__ __forceinline__ float4 ld_join4(const float* ptr) {
   KVC_GUARD(ptr, 16, return make_float4(0.f, 0.f, 0.f, 0.f));
   return __ldcg(reinterpret_cast<const float4*>(ptr));
 }
+__device__ __forceinline__ float2 ld_join2(const float* ptr) {
+  KVC_GUARD(ptr, 8, return make_float2(0.f, 0.f));
+  return __ldcg(reinterpret_cast<const float2*>(ptr));
+}
+
+// Warps of a CTA, two of which share an SM (one for D = 256): the start of a job and the joins of one hide behind
+// the other.  CTAs of 8 warps, one an SM: 64 uneven sequences 103 us against 101, 48 with one KV head 27 against 25.
+constexpr int kWarps = 4, kThreads16 = 32 * kWarps;
+// What a job costs its CTA besides its steps (its first copies, the joins), in steps: some 5 us.  Shares that did not
+// count it left CTAs with many short jobs three times as long as the others.  Of 8, 12, 16, 20, 24: 48 sequences with
+// one KV head 26.6, 26.5, 24.6, 24.6, 24.6 us, 64 uneven ones 102, 100, 101, 102, 102.
+constexpr uint32_t kStart = 16;
+constexpr uint32_t kLeast = kStart + 4;  // of a share
+constexpr uint32_t kFlat = 12;  // partials that are joined at once
 
 template <int D>
 struct Shape16 {
@@ -137,16 +149,13 @@ struct Shape16 {
   static constexpr int kStage = 2 * TS * kPitch;   // K's rows, then V's
   static constexpr int NS = D == 32 ? 4 : 3;
   static constexpr int kQ = 16 * kPitch;
-  static constexpr int kSmall = 2048;
+  static constexpr int kSmall = 1024;
   static constexpr int kOut = D + 4;               // floats of a row in the join of the warps
-  static constexpr int kWarps = D == 256 ? 4 : 8;  // the most whose slots fit
-  // What a job costs its CTA besides its steps (finding it, its first copies, the join), in steps: some 5 us.
-  static constexpr uint32_t kStart = D == 256 ? 8 : D == 32 ? 16 : 12;
+  static constexpr int kSmem = kQ + kSmall + kWarps * NS * kStage;
 };
-template <int D>
-constexpr int smem16(int warps) {
-  using S = Shape16<D>;
-  return S::kQ + S::kSmall + warps * S::NS * S::kStage;
+// n / G for n < 2^31
+__device__ __forceinline__ uint32_t div_g(const C16Params& p, uint32_t n) {
+  return (__umulhi(p.g_magic, n) + n) >> p.g_shift;
 }
 
 // A sequence of the batch, and how many steps its jobs have.
@@ -157,13 +166,21 @@ struct Seq16 {
   uint32_t steps;   // of a job
   uint64_t all;     // of all jobs, each with kStart besides
 };
-// a / b, where both fit 32 bits as they mostly do without the long division
+// a / b.  Small ones (as they mostly are) by an FP32 quotient, which is off by one at most, and its remainder: the long
+// divisions, several in a row at each start of a CTA, took it most of a microsecond.
 __device__ __forceinline__ uint64_t div64(uint64_t a, uint64_t b) {
-  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  if (((a | b) >> 22) == 0) {
+    const int32_t x = (int32_t)a, y = (int32_t)b;
+    int32_t q = (int32_t)__fdividef((float)x, (float)y);
+    const int32_t r = x - q * y;
+    if (r < 0) --q;
+    if (r >= y) ++q;
+    return (uint64_t)q;
+  }
   return a / b;
 }
 
-template <int D, bool PAGED16>
+template <int D, bool PAGED16, int TR>
 __device__ __forceinline__ Seq16 seq16(const C16Params& p, uint32_t s) {
   Seq16 x;
   x.q.s = s;
@@ -178,32 +195,33 @@ __device__ __forceinline__ Seq16 seq16(const C16Params& p, uint32_t s) {
   if (PAGED16) x.lo &= ~15;
   constexpr int TS = Shape16<D>::TS;
   x.steps = x.hi > x.lo ? ((uint32_t)(x.hi - x.lo) + TS - 1u) / TS : 1u;  // (rows that see nothing are a step)
-  const uint32_t tiles = ((uint32_t)x.q.n_new * p.G + p.tile_rows - 1u) / p.tile_rows;
-  x.all = (uint64_t)(x.steps + Shape16<D>::kStart) * tiles * p.H;
+  const uint32_t tiles = ((uint32_t)x.q.n_new * p.G + TR - 1u) / TR;
+  x.all = (uint64_t)(x.steps + kStart) * tiles * p.H;
   return x;
 }
 
 // PAGED16: pages are whole 16-token tiles, so a tile lies in one page; otherwise every token's page is
 // looked up by itself.  NT: 8-row column blocks of a row tile.
 template <int DT, int D, bool PAGED16, int NT>
-__global__ void __launch_bounds__(Shape16<D>::kWarps * 32, 1) c16_step_kernel(const __grid_constant__ C16Params p) {
+__global__ void __launch_bounds__(kThreads16) c16_step_kernel(const __grid_constant__ C16Params p) {
   using S = Shape16<D>;
   constexpr int NS = S::NS, TS = S::TS, HT = S::HT, TR = 8 * NT, KS = D / 16;
   constexpr uint32_t kFull = TS == 32 ? 0xffffffffu : 0xffffu;
   extern __shared__ __align__(1024) uint8_t smem[];
-  const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5, threads = blockDim.x, W = threads >> 5;
+  const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
+  constexpr uint32_t threads = kThreads16, W = kWarps;
   const uint32_t g = lane >> 2, qd = lane & 3u;
   const uint32_t sm_q = (uint32_t)__cvta_generic_to_shared(smem);
   float* s_m = reinterpret_cast<float*>(smem + S::kQ);             // [row][warp] maxima
-  float* s_l = s_m + 16 * 8;                                       // [row][warp] sums, at the row's maximum
-  float2* s_fin = reinterpret_cast<float2*>(s_l + 16 * 8);         // row: maximum, 1 / sum
-  unsigned long long* s_tot = reinterpret_cast<unsigned long long*>(s_fin + 16);  // [8] warps' steps, then where to begin
-  uint32_t* s_last = reinterpret_cast<uint32_t*>(s_tot + 10);
-  static_assert(16 * 8 * 8 + 16 * 8 + 10 * 8 + 4 <= S::kSmall, "");
+  float* s_l = s_m + 16 * kWarps;                                       // [row][warp] sums, at the row's maximum
+  float2* s_fin = reinterpret_cast<float2*>(s_l + 16 * kWarps);         // row: maximum, 1 / sum
+  unsigned long long* s_tot = reinterpret_cast<unsigned long long*>(s_fin + 16);  // warps' steps, then where to begin
+  uint32_t* s_last = reinterpret_cast<uint32_t*>(s_tot + kWarps + 2);
+  static_assert(16 * kWarps * 8 + 16 * 8 + (kWarps + 2) * 8 + 4 <= S::kSmall, "");
   uint8_t* slots = smem + S::kQ + S::kSmall;
   float* s_o = reinterpret_cast<float*>(slots);                    // [warp][TR][kOut], over the slots
   float2* s_ml = reinterpret_cast<float2*>(slots);                 // [partial][TR], over the slots
-  static_assert((int)kC16Ctas * 16 * 8 <= 4 * S::NS * S::kStage && 16 * S::kOut * 4 <= S::NS * S::kStage, "");
+  static_assert((int)kC16Ctas * 16 * 8 <= kWarps * S::NS * S::kStage && 16 * S::kOut * 4 <= S::NS * S::kStage, "");
   const uint32_t my_slots = sm_q + S::kQ + S::kSmall + warp * (NS * S::kStage);
 
   // ---- this CTA's share of all steps
@@ -214,7 +232,7 @@ __global__ void __launch_bounds__(Shape16<D>::kWarps * 32, 1) c16_step_kernel(co
   {
     const uint32_t per = (p.n_seqs + threads - 1u) / threads, i0 = min(tid * per, p.n_seqs), i1 = min(i0 + per, p.n_seqs);
     unsigned long long mine = 0;
-    for (uint32_t i = i0; i < i1; ++i) mine += seq16<D, PAGED16>(p, i).all;
+    for (uint32_t i = i0; i < i1; ++i) mine += seq16<D, PAGED16, TR>(p, i).all;
     unsigned long long inc = mine;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -228,7 +246,7 @@ __global__ void __launch_bounds__(Shape16<D>::kWarps * 32, 1) c16_step_kernel(co
       before += w < warp ? s_tot[w] : 0ull;
       total += s_tot[w];
     }
-    share = max((unsigned long long)div64(total + gridDim.x - 1u, gridDim.x), (unsigned long long)p.share);
+    share = max((unsigned long long)div64(total + gridDim.x - 1u, gridDim.x), (unsigned long long)kLeast);
     at = (uint64_t)blockIdx.x * share;
     if (at >= total) return;
     end = min(at + share, (uint64_t)total);
@@ -236,16 +254,16 @@ __global__ void __launch_bounds__(Shape16<D>::kWarps * 32, 1) c16_step_kernel(co
     if (pre <= at && at < pre + mine) {
       uint32_t i = i0;
       for (;; ++i) {
-        const uint64_t n = seq16<D, PAGED16>(p, i).all;
+        const uint64_t n = seq16<D, PAGED16, TR>(p, i).all;
         if (at < pre + n) break;
         pre += n;
       }
-      s_tot[8] = pre;
-      s_tot[9] = i;
+      s_tot[kWarps] = pre;
+      s_tot[kWarps + 1] = i;
     }
     cta_sync();
-    base = s_tot[8];
-    s = (uint32_t)s_tot[9];
+    base = s_tot[kWarps];
+    s = (uint32_t)s_tot[kWarps + 1];
   }
 
   // this lane's place in the copies and the fragments of a tile
@@ -254,24 +272,34 @@ __global__ void __launch_bounds__(Shape16<D>::kWarps * 32, 1) c16_step_kernel(co
   const uint32_t k_at = my_slots + (lane & 15u) * S::kPitch + ((lane >> 4) << 4);
   const uint32_t v_at = my_slots + (TS + (lane & 7u) + ((lane >> 4) << 3)) * S::kPitch + (((lane >> 3) & 1u) << 4);
 
-  Seq16 x = seq16<D, PAGED16>(p, s);
-  while (at < end) {
-    while (at >= base + x.all) {  // (a sequence without new tokens has no steps)
-      base += x.all;
-      x = seq16<D, PAGED16>(p, ++s);
+  Seq16 x = seq16<D, PAGED16, TR>(p, s);
+  const uint64_t begin = at;
+  const uint64_t job = div64(at - base, x.steps + kStart);
+  uint64_t job0 = base + job * (x.steps + kStart);  // where the job begins
+  uint32_t tile = job < p.H ? 0u : (uint32_t)div64(job, p.H), head = (uint32_t)(job - (uint64_t)tile * p.H);
+  for (bool first = true; at < end; first = false) {
+    if (!first) {  // the next job: at is where it begins
+      job0 = at;
+      if (++head == p.H) head = 0, ++tile;
+      while (at >= base + x.all) {  // the next sequence (one without new tokens has no jobs)
+        base += x.all;
+        x = seq16<D, PAGED16, TR>(p, ++s);
+        head = tile = 0;
+      }
     }
-    const uint32_t len = x.steps + S::kStart;
-    const uint64_t job = div64(at - base, len), job0 = base + job * len;
+    const uint32_t len = x.steps + kStart;
     const uint32_t from = (uint32_t)(at - job0), to = (uint32_t)min((uint64_t)len, end - job0);
     at = job0 + to;
     // the steps of [from, to), kStart of which are none
-    const uint32_t step0 = max(from, S::kStart) - S::kStart, n_steps = max(to, S::kStart) - S::kStart - step0;
+    const uint32_t step0 = max(from, kStart) - kStart, n_steps = max(to, kStart) - kStart - step0;
     if (n_steps == 0u) continue;  // the CTA after this one begins the job
-    const uint32_t tile = (uint32_t)div64(job, p.H), head = (uint32_t)(job - (uint64_t)tile * p.H);
-    const uint32_t cta0 = (uint32_t)div64(job0 + S::kStart, share), n_parts = (uint32_t)div64(job0 + len - 1u, share) - cta0 + 1u;
+    // the CTAs that hold parts of the job: the one whose share has its first step, and those up to its last
+    uint32_t cta0 = blockIdx.x, n_parts = 1u;
+    if (job0 + kStart < begin) cta0 = (uint32_t)div64(job0 + kStart, share);
+    if (cta0 != blockIdx.x || job0 + len > end) n_parts = (uint32_t)div64(job0 + len - 1u, share) - cta0 + 1u;
 
     const uint32_t r0 = tile * TR, n_rows = min((uint32_t)TR, (uint32_t)x.q.n_new * p.G - r0);
-    const int32_t first_pos = x.q.start + (int32_t)(r0 / p.G), last_pos = x.q.start + (int32_t)((r0 + n_rows - 1u) / p.G);
+    const int32_t first_pos = x.q.start + (int32_t)div_g(p, r0), last_pos = x.q.start + (int32_t)div_g(p, r0 + n_rows - 1u);
     // keys that some row of the tile sees, and the steps that hold them
     const int32_t t_hi = last_pos < 0 ? 0 : p.causal ? min(x.hi, last_pos + 1) : x.hi;
     const int32_t t_lo = p.window && first_pos >= 0 ? max(0, first_pos - (int32_t)min(p.window, 0x7fffffffu) + 1) : 0;
@@ -334,7 +362,7 @@ __global__ void __launch_bounds__(Shape16<D>::kWarps * 32, 1) c16_step_kernel(co
       for (int i = 0; i < NS - 1; ++i) e[i] = entry_of(x_lo + (int32_t)(warp + i * W));
       entry = entry_of(x_lo + (int32_t)(warp + (NS - 1) * W));
       for (uint32_t i = tid; i < TR * (D / 8); i += threads) {
-        const uint32_t r = i / (D / 8), c = i % (D / 8), rr = r0 + min(r, n_rows - 1u), tok = rr / p.G;
+        const uint32_t r = i / (D / 8), c = i % (D / 8), rr = r0 + min(r, n_rows - 1u), tok = div_g(p, rr);
         const uint16_t* src = p.a + ((int64_t)x.q.row + tok) * p.a_row + (int64_t)(head * p.G + rr - tok * p.G) * p.a_head + c * 8;
         cp16z(sm_q + r * S::kPitch + c * 16, src, r < n_rows);
       }
@@ -435,7 +463,7 @@ __global__ void __launch_bounds__(Shape16<D>::kWarps * 32, 1) c16_step_kernel(co
             // keys that the row sees
             int32_t hi = 0x7fffffff, lo = 0;
             if (by_row) {
-              const int32_t pos = x.q.start + (int32_t)((r0 + 8u * n + 2u * qd + r) / p.G);
+              const int32_t pos = x.q.start + (int32_t)div_g(p, r0 + 8u * n + 2u * qd + r);
               if (p.causal) hi = pos + 1;
               if (p.window) lo = (int32_t)max((int64_t)0, (int64_t)pos - p.window + 1);
               if (pos < 0) hi = 0;
@@ -603,14 +631,14 @@ __global__ void __launch_bounds__(Shape16<D>::kWarps * 32, 1) c16_step_kernel(co
     auto finish_row = [&](uint32_t row, float mx, float ls) {
       s_fin[row] = make_float2(mx, ls == 0.0f ? 0.0f : 1.0f / ls);
       if (p.lse && row < n_rows) {
-        const uint32_t rr = r0 + row, tok = rr / p.G, hd = head * p.G + rr - tok * p.G;
+        const uint32_t rr = r0 + row, tok = div_g(p, rr), hd = head * p.G + rr - tok * p.G;
         st4(p.lse + ((int64_t)x.q.row + tok) * p.HQ + hd,
             __float_as_uint(ls == 0.0f ? kNegInf : (mx - kBias<DT> + log2f(ls)) * 0.693147180559945309f));
       }
     };
     auto finish_out = [&](uint32_t r, uint32_t d4, float4 y) {
       const float inv = s_fin[r].y;
-      const uint32_t rr = r0 + r, tok = rr / p.G, hd = head * p.G + rr - tok * p.G;
+      const uint32_t rr = r0 + r, tok = div_g(p, rr), hd = head * p.G + rr - tok * p.G;
       st8(p.b + ((int64_t)x.q.row + tok) * p.b_row + (int64_t)hd * p.b_head + d4 * 4,
           inv == 0.0f ? make_uint2(0, 0)
                       : make_uint2(pack2<DT>(y.x * inv, y.y * inv), pack2<DT>(y.z * inv, y.w * inv)));
@@ -639,88 +667,139 @@ __global__ void __launch_bounds__(Shape16<D>::kWarps * 32, 1) c16_step_kernel(co
     if (n_parts == 1u) continue;
 
     // ---- the CTA that finishes last joins the job's partial results
-    cta_sync();
-    if (tid == 0) {
-      uint32_t last = 0;
-      KVC_GUARD(p.tickets + cta0, 4, last = 2);
-      if (last == 0) {
-        // releases this CTA's partial (the barrier above put it before), acquires the others'
-        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(last) : "l"(p.tickets + cta0) : "memory");
-        last = last == n_parts - 1u ? 1u : 0u;
-        if (last) p.tickets[cta0] = 0;  // as the next call finds it
+    // Whether this CTA is the last of n at a ticket.
+    auto last_of = [&](uint32_t* ticket, uint32_t n) -> bool {
+      cta_sync();
+      if (tid == 0) {
+        uint32_t last = 0;
+        KVC_GUARD(ticket, 4, last = 2);
+        if (last == 0) {
+          // releases what this CTA stored (the barrier above put it before), acquires what the others did
+          asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(last) : "l"(ticket) : "memory");
+          last = last == n - 1u ? 1u : 0u;
+          if (last) *ticket = 0;  // as the next call finds it
+        }
+        *s_last = last;
       }
-      *s_last = last;
-    }
-    cta_sync();
-    if (*s_last != 1u) continue;
-    for (uint32_t k = tid; k < n_parts * TR; k += threads)
-      s_ml[k] = k % TR < n_rows ? ld_join2(part_of(k / TR) + TR * D + 2 * (k % TR)) : make_float2(kNegInf, 0.0f);
-    cta_sync();
-    if (tid < 8u * TR) {  // 8 threads a row
-      const uint32_t row = tid >> 3, part = tid & 7u;
-      float mx = kNegInf, ls = 0.0f;
-      for (uint32_t k = part; k < n_parts; k += 8) mx = fmaxf(mx, s_ml[k * TR + row].x);
+      cta_sync();
+      return *s_last == 1u;
+    };
+    // Join partials first, first + stride, ... (n of them) in this order: a row's outputs and lse, or (!whole) a partial
+    // in place of the first.
+    auto join = [&](uint32_t first, uint32_t stride, uint32_t n, bool whole) {
+      // four dims a thread at each of its places; kU partials' loads at each place are in flight
+      constexpr uint32_t kP = TR * D / 4 > threads ? TR * D / 4 / threads : 1, kU = (NT == 2 || D == 256 ? 8 : 16) / kP;
+      float4 a[kP][kU], y[kP];
+      auto load = [&](uint32_t k0) {
 #pragma unroll
-      for (int d = 1; d < 8; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-      for (uint32_t k = part; k < n_parts; k += 8) {
-        const float2 ml = s_ml[k * TR + row];
-        const float f = ml.x == kNegInf ? 0.0f : ex2(ml.x - mx);
-        ls += ml.y * f;
-        s_ml[k * TR + row].x = f;
+        for (uint32_t i = 0; i < kP; ++i)
+#pragma unroll
+          for (uint32_t k = 0; k < kU; ++k) {
+            const uint32_t c4 = tid + i * threads;
+            if (k0 + k < n && c4 < n_rows * (D / 4)) a[i][k] = ld_join4(part_of(first + (k0 + k) * stride) + c4 * 4);
+          }
+      };
+      load(0);  // on their way while the factors are found
+      for (uint32_t k = tid; k < n * TR; k += threads)
+        s_ml[k] = k % TR < n_rows ? ld_join2(part_of(first + k / TR * stride) + TR * D + 2 * (k % TR)) : make_float2(kNegInf, 0.0f);
+      cta_sync();
+      for (uint32_t i = tid; i < 8u * TR; i += threads) {  // 8 threads a row
+        const uint32_t row = i >> 3, part = i & 7u;
+        float mx = kNegInf, ls = 0.0f;
+        for (uint32_t k = part; k < n; k += 8) mx = fmaxf(mx, s_ml[k * TR + row].x);
+#pragma unroll
+        for (int d = 1; d < 8; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        for (uint32_t k = part; k < n; k += 8) {
+          const float2 ml = s_ml[k * TR + row];
+          const float f = ml.x == kNegInf ? 0.0f : ex2(ml.x - mx);
+          ls += ml.y * f;
+          s_ml[k * TR + row].x = f;
+        }
+#pragma unroll
+        for (int d = 1; d < 8; d *= 2) ls += __shfl_xor_sync(0xffffffffu, ls, d);
+        if (part == 0) {
+          if (whole) finish_row(row, mx, ls);
+          else if (row < n_rows) st8(part_of(first) + TR * D + 2 * row, make_uint2(__float_as_uint(mx), __float_as_uint(ls)));
+        }
       }
+      cta_sync();
 #pragma unroll
-      for (int d = 1; d < 8; d *= 2) ls += __shfl_xor_sync(0xffffffffu, ls, d);
-      if (part == 0) finish_row(row, mx, ls);
-    }
-    cta_sync();
-    // four dims a thread, all partials in order, 16 loads in flight
-    for (uint32_t c4 = tid; c4 < n_rows * (D / 4); c4 += threads) {
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (uint32_t k0 = 0; k0 < n_parts; k0 += 16) {
-        float4 a[16];
+      for (uint32_t i = 0; i < kP; ++i) y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (uint32_t k0 = 0; k0 < n; k0 += kU) {
+        if (k0) load(k0);
 #pragma unroll
-        for (uint32_t k = 0; k < 16; ++k)
-          if (k0 + k < n_parts) a[k] = ld_join4(part_of(k0 + k) + c4 * 4);
+        for (uint32_t i = 0; i < kP; ++i)
 #pragma unroll
-        for (uint32_t k = 0; k < 16; ++k)
-          if (k0 + k < n_parts) {
-            const float f = s_ml[(k0 + k) * TR + c4 / (D / 4)].x;
-            y.x += a[k].x * f;
-            y.y += a[k].y * f;
-            y.z += a[k].z * f;
-            y.w += a[k].w * f;
+          for (uint32_t k = 0; k < kU; ++k) {
+            const uint32_t c4 = tid + i * threads;
+            if (k0 + k < n && c4 < n_rows * (D / 4)) {
+              const float f = s_ml[(k0 + k) * TR + c4 / (D / 4)].x;
+              y[i].x += a[i][k].x * f;
+              y[i].y += a[i][k].y * f;
+              y[i].z += a[i][k].z * f;
+              y[i].w += a[i][k].w * f;
+            }
           }
       }
-      finish_out(c4 / (D / 4), c4 % (D / 4), y);
+#pragma unroll
+      for (uint32_t i = 0; i < kP; ++i) {
+        const uint32_t c4 = tid + i * threads;
+        if (c4 < n_rows * (D / 4)) {
+          if (whole) finish_out(c4 / (D / 4), c4 % (D / 4), y[i]);
+          else st16(part_of(first) + c4 * 4, make_uint4(__float_as_uint(y[i].x), __float_as_uint(y[i].y), __float_as_uint(y[i].z),
+                                                        __float_as_uint(y[i].w)));
+        }
+      }
+    };
+    // Many partials are joined in groups of about their number's square root, each by its last CTA, then the groups.
+    // (A group's tickets go by its first CTA: one job at most begins in a CTA's share, and one at most goes on into it.)
+    uint32_t first_part = 0, stride = 1, n = n_parts, *ticket = p.tickets + cta0;
+    const uint32_t group = n_parts <= kFlat ? n_parts : (uint32_t)sqrtf((float)n_parts) + 1u;
+    if (group < n_parts) {
+      first_part = (blockIdx.x - cta0) / group * group;
+      n = min(group, n_parts - first_part);
+      ticket += first_part + (first_part ? kC16Ctas : 0u);
+    }
+    bool whole = group == n_parts;
+#pragma unroll 1
+    while (last_of(ticket, n)) {
+      join(first_part, stride, n, whole);
+      if (whole) break;
+      first_part = 0, stride = group, n = (n_parts + group - 1u) / group, whole = true;
+      ticket = p.tickets + 2u * kC16Ctas + cta0;
     }
   }
 }
 
 template <int DT, int D, bool PAGED16, int NT>
-int step_launch(const C16Params& p, uint32_t ctas, uint32_t warps, void* stream) {
+int step_launch(const C16Params& p, uint32_t ctas, void* stream) {
   const auto kernel = c16_step_kernel<DT, D, PAGED16, NT>;
   static std::atomic<uint64_t> done{0};
-  if (!allow_smem(kernel, smem16<D>(Shape16<D>::kWarps), done)) return KV_ERR_CUDA;
+  if (!allow_smem(kernel, Shape16<D>::kSmem, done)) return KV_ERR_CUDA;
   return dbg_launch(
       stream,
       [&] {
-        kernel<<<ctas, warps * 32, smem16<D>((int)warps), (cudaStream_t)stream>>>(p);
+        kernel<<<ctas, kThreads16, Shape16<D>::kSmem, (cudaStream_t)stream>>>(p);
         return cudaGetLastError();
       },
       p);
 }
 
 template <int DT, int D>
-int step_d(const C16Params& p, uint32_t ctas, uint32_t warps, void* stream) {
+int step_d(const C16Params& p, uint32_t ctas, void* stream) {
   if (p.T % 16 == 0)
-    return p.tile_rows == 8u ? step_launch<DT, D, true, 1>(p, ctas, warps, stream) : step_launch<DT, D, true, 2>(p, ctas, warps, stream);
-  return p.tile_rows == 8u ? step_launch<DT, D, false, 1>(p, ctas, warps, stream) : step_launch<DT, D, false, 2>(p, ctas, warps, stream);
+    return p.tile_rows == 8u ? step_launch<DT, D, true, 1>(p, ctas, stream) : step_launch<DT, D, true, 2>(p, ctas, stream);
+  return p.tile_rows == 8u ? step_launch<DT, D, false, 1>(p, ctas, stream) : step_launch<DT, D, false, 2>(p, ctas, stream);
 }
 
 }  // namespace
 
-int launch_c16_attend(const C16Params& p, uint32_t ctas, uint32_t warps, void* stream) {
-  KVC_C8_DISPATCH(step_d, p, ctas, warps, stream);
+// Two CTAs an SM (one for D = 256), fewer where the batch cannot have as many shares: host fields only, the device finds
+// how many steps there are.
+int launch_c16_attend(const C16Params& p, uint64_t jobs, uint64_t keys, void* stream) {
+  const uint64_t steps = jobs * (keys / (p.D >= 128u ? 16u : 32u) + 2u + kStart);
+  const uint32_t ctas = (uint32_t)std::min<uint64_t>(p.D == 256u ? kC8Sms : kC16Ctas, (steps + kLeast - 1u) / kLeast);
+  KVC_C8_DISPATCH(step_d, p, ctas, stream);
 }
 
 }  // namespace kvc

@@ -16,6 +16,7 @@ namespace kvc {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr uint32_t kQueries = 8;  // iterations of a queries' warp: 256 bytes of loads in flight a lane, at 16 warps an SM
 
 struct Append8 : AppendParams {
   RowMap qm;
@@ -29,18 +30,21 @@ inline void dbg_ranges(DbgRanges& r, const Append8& p) {
 }
 #endif
 
+// Ask for the line that holds ptr (a hint).
+__device__ __forceinline__ void prefetch_line(const void* ptr) {
+  KVC_GUARD(ptr, 1, return);
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(ptr));
+}
+
 template <int DT, int D>
 __global__ void __launch_bounds__(kWarps * 32, 2) c8_append_kernel(const __grid_constant__ Append8 p) {
   constexpr int LPR = D / 16, RPI = 32 / LPR, R = 4;  // lanes of a token's row, rows a warp holds at once, times R
   if (blockIdx.x >= p.page_blocks)
-    return append_queries<DT, D>(p, p.qm, (blockIdx.x - p.page_blocks) * kWarps + (threadIdx.x >> 5));
+    return append_queries<DT, D, kQueries>(p, p.qm, (blockIdx.x - p.page_blocks) * kWarps + (threadIdx.x >> 5));
   const uint32_t lane = threadIdx.x & 31u;
   PageJob j;
-  if (!page_job(p, blockIdx.x * kWarps + (threadIdx.x >> 5), j)) return;
-  if (j.t0 < j.t1 && j.head == 0u && j.role == 0u && lane == 0u &&
-      (uint64_t)j.page * p.T + (uint32_t)j.t1 > p.positions)
-    c8_error(p, j.q.s, KV_CACHE8_BAD_POSITION);
-  if (j.id < 0 || j.t0 >= j.t1) return;
+  if (!page_find(p, blockIdx.x * kWarps + (threadIdx.x >> 5), j) || j.t0 >= j.t1) return;
+  j.id = c8_page(p, j.q.s, (uint32_t)j.page);  // (not looked at before the new values have been asked for)
   const int sub = lane / LPR, first = j.t0 + sub;
   const int32_t pos0 = j.page * (int32_t)p.T;
 #pragma unroll 1
@@ -49,9 +53,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2) c8_append_kernel(const __grid_
     const RotUnit r = rot_unit<D>(turn ? p.R : 0u, turn && p.neighbours, lane % LPR);
     const int64_t rs = role ? p.b_row : p.a_row;
     const uint16_t* src = (role ? p.b : p.a) + (int64_t)j.head * (role ? p.b_head : p.a_head) + j.row0 * rs;
-    uint8_t* page = (role ? p.v : p.k) + (int64_t)j.id * p.sb + (int64_t)j.head * p.sh;
-    float* scale_at = (role ? p.v_scale : p.k_scale) + (int64_t)j.id * p.H + j.head;
-    const float was = j.t0 > 0 ? ld_held_f32(scale_at) : 0.0f;
     float x[R][16];
     // rows t, t + RPI, ... of the page, turned; zeros past its new tokens
     auto rows_at = [&](int t) {
@@ -69,10 +70,22 @@ __global__ void __launch_bounds__(kWarps * 32, 2) c8_append_kernel(const __grid_
         if (turn && t + i * RPI < j.t1) rot_turn(r, rot_angles(p, r, pos0 + t + i * RPI), x[i]);
       }
     };
+    rows_at(first);
+    if (j.id < 0 || (role == j.role && pos0 + j.t1 > (int32_t)p.positions)) {
+      if (j.head == 0u && j.role == 0u && lane == 0u && role == 0u)
+        c8_error(p, j.q.s, (j.id < 0 ? KV_CACHE8_BAD_PAGE : 0u) |
+                               ((uint32_t)(pos0 + j.t1) > p.positions ? KV_CACHE8_BAD_POSITION : 0u));
+      if (j.id < 0) return;
+    }
+    uint8_t* page = (role ? p.v : p.k) + (int64_t)j.id * p.sb + (int64_t)j.head * p.sh;
+    float* scale_at = (role ? p.v_scale : p.k_scale) + (int64_t)j.id * p.H + j.head;
+    const float was = j.t0 > 0 ? ld_held_f32(scale_at) : 0.0f;
+    // the codes held, in case the scale grows
+    if (lane < (uint32_t)min(j.t0, 32)) prefetch_line(page + (int64_t)lane * p.st);
     // the largest magnitude; NaN are ignored, infinities are not
     float amax = 0.0f;
     for (int t = first; t - sub < j.t1; t += R * RPI) {
-      rows_at(t);
+      if (t != first) rows_at(t);
 #pragma unroll
       for (int i = 0; i < R; ++i)
 #pragma unroll
@@ -142,7 +155,7 @@ int append_d(const AppendParams& p, void* stream) {
   // K and V in one warp where that leaves 32 warps an SM, as in the plain write
   a.both_roles = (uint64_t)p.H * p.n_units >= 32ull * kC8Sms ? 1u : 0u;
   const uint64_t warps = (a.both_roles ? 1ull : 2ull) * p.H * p.n_units;
-  a.qm = row_map(p.q ? p.n_new : 0u, p.HQ * (D / 16), kQueryIterations);
+  a.qm = row_map(p.q ? p.n_new : 0u, p.HQ * (D / 16), kQueries);
   const uint64_t pages = (warps + kWarps - 1u) / kWarps;
   const uint64_t grid = pages + (a.qm.warps + (uint64_t)kWarps - 1u) / kWarps;
   if (a.qm.warps == 0xffffffffu || grid > 0x7fffffffull || warps > 0xffffffffull) return KV_ERR_INVALID_ARG;

@@ -76,12 +76,12 @@ struct AppendParams : C8Params {
 // Attention over 16-bit pages (strides in bytes, scales NULL).
 struct C16Params : C8Params {
   uint32_t tile_rows;           // rows of a tile: 8 where one token's query heads fit, else 16
-  uint32_t share;               // steps of a CTA at least
+  uint32_t g_magic, g_shift;    // n / G = (umulhi(g_magic, n) + n) >> g_shift, n < 2^31
 };
 
 int launch_c8_append(const AppendParams& p, void* stream);
 int launch_c16_append(const AppendParams& p, void* stream);
-int launch_c16_attend(const C16Params& p, uint32_t ctas, uint32_t warps, void* stream);
+int launch_c16_attend(const C16Params& p, uint64_t jobs, uint64_t keys, void* stream);  // at most so many
 int launch_c8_write(const C8Params& p, void* stream);
 int launch_c8_read(const C8Params& p, void* stream);
 int launch_c8_step(const C8Params& p, void* stream);

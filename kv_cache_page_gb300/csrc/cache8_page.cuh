@@ -27,7 +27,8 @@ struct PageJob {
   int64_t row0;       // row of token 0 of the page (negative where it has none)
 };
 
-__device__ __forceinline__ bool page_job(const C8Params& p, uint32_t warp, PageJob& j) {
+// All but the page id; false where the warp has no work.
+__device__ __forceinline__ bool page_find(const C8Params& p, uint32_t warp, PageJob& j) {
   const uint32_t per = p.both_roles ? p.H : 2u * p.H;
   const uint32_t u = warp / per, r = warp - u * per;
   if (u >= p.n_units) return false;
@@ -42,12 +43,16 @@ __device__ __forceinline__ bool page_job(const C8Params& p, uint32_t warp, PageJ
   j.t1 = (int32_t)min((int64_t)j.q.len - first, (int64_t)T);
   j.row0 = (int64_t)j.q.row + (first - j.q.start);
   j.id = -1;
-  if (j.t0 < j.t1 && j.q.n_new > 0) {
-    j.id = c8_page(p, j.q.s, (uint32_t)j.page);
-    if (j.id < 0 && r == 0u && (threadIdx.x & 31u) == 0u) c8_error(p, j.q.s, KV_CACHE8_BAD_PAGE);
-    return true;
-  }
   return j.q.n_new > 0;
+}
+
+__device__ __forceinline__ bool page_job(const C8Params& p, uint32_t warp, PageJob& j) {
+  if (!page_find(p, warp, j)) return false;
+  if (j.t0 < j.t1) {
+    j.id = c8_page(p, j.q.s, (uint32_t)j.page);
+    if (j.id < 0 && j.role == 0u && j.head == 0u && (threadIdx.x & 31u) == 0u) c8_error(p, j.q.s, KV_CACHE8_BAD_PAGE);
+  }
+  return true;
 }
 
 // The scale that a page held: an ordinary load, because the same kernel stores there

@@ -171,13 +171,11 @@ __device__ __forceinline__ RowPlace row_place(const C8Params& p, uint32_t row0, 
 }
 
 // ---------------------------------------------------------------- queries
-constexpr uint32_t kQueryIterations = 4;  // 128 bytes of loads in flight a lane
-
 // Warp `warp` of the queries' part of an append: rows turned from q to q_out (which may be q: a lane loads, with
-// ordinary loads, what it alone stores).  Rows without a position become 0.
-template <int DT, int D>
+// ordinary loads, what it alone stores), I units of 32 bytes in flight a lane.  Rows without a position become 0.
+template <int DT, int D, uint32_t I>
 __device__ __forceinline__ void append_queries(const AppendParams& p, const RowMap& m, uint32_t warp) {
-  constexpr uint32_t U = D / 16, I = kQueryIterations;
+  constexpr uint32_t U = D / 16;
   if (warp >= m.warps) return;
   const uint32_t lane = threadIdx.x & 31u, per = 32u >> m.log2;
   const uint32_t group = warp / m.slabs, slab = warp - group * m.slabs;
