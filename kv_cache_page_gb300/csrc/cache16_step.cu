@@ -164,7 +164,8 @@ struct Seq16 {
   int32_t lo, hi;   // keys that some row sees; lo at a 16-token tile where pages are whole tiles
   bool past;        // tokens lie past the table's row
   uint32_t steps;   // of a job
-  uint64_t all;     // of all jobs, each with kStart besides
+  uint32_t len;     // of a job in the row of all jobs: its parts, or its steps and kStart
+  uint32_t jobs;
 };
 // a / b.  Small ones (as they mostly are) by an FP32 quotient, which is off by one at most, and its remainder: the long
 // divisions, several in a row at each start of a CTA, took it most of a microsecond.
@@ -180,8 +181,9 @@ __device__ __forceinline__ uint64_t div64(uint64_t a, uint64_t b) {
   return a / b;
 }
 
+// most: the most steps of a part where jobs are split evenly, 0 where shares go over the jobs.
 template <int D, bool PAGED16, int TR>
-__device__ __forceinline__ Seq16 seq16(const C16Params& p, uint32_t s) {
+__device__ __forceinline__ Seq16 seq16(const C16Params& p, uint32_t s, uint32_t most) {
   Seq16 x;
   x.q.s = s;
   x.q.unit = 0;
@@ -195,8 +197,8 @@ __device__ __forceinline__ Seq16 seq16(const C16Params& p, uint32_t s) {
   if (PAGED16) x.lo &= ~15;
   constexpr int TS = Shape16<D>::TS;
   x.steps = x.hi > x.lo ? ((uint32_t)(x.hi - x.lo) + TS - 1u) / TS : 1u;  // (rows that see nothing are a step)
-  const uint32_t tiles = ((uint32_t)x.q.n_new * p.G + TR - 1u) / TR;
-  x.all = (uint64_t)(x.steps + kStart) * tiles * p.H;
+  x.jobs = ((uint32_t)x.q.n_new * p.G + TR - 1u) / TR * p.H;
+  x.len = most ? (uint32_t)div64(x.steps + most - 1u, most) : x.steps + kStart;
   return x;
 }
 
@@ -216,23 +218,49 @@ __global__ void __launch_bounds__(kThreads16) c16_step_kernel(const __grid_const
   float* s_l = s_m + 16 * kWarps;                                       // [row][warp] sums, at the row's maximum
   float2* s_fin = reinterpret_cast<float2*>(s_l + 16 * kWarps);         // row: maximum, 1 / sum
   unsigned long long* s_tot = reinterpret_cast<unsigned long long*>(s_fin + 16);  // warps' steps, then where to begin
-  uint32_t* s_last = reinterpret_cast<uint32_t*>(s_tot + kWarps + 2);
-  static_assert(16 * kWarps * 8 + 16 * 8 + (kWarps + 2) * 8 + 4 <= S::kSmall, "");
+  uint32_t* s_last = reinterpret_cast<uint32_t*>(s_tot + 2 * kWarps);
+  static_assert(16 * kWarps * 8 + 16 * 8 + 2 * kWarps * 8 + 4 <= S::kSmall, "");
   uint8_t* slots = smem + S::kQ + S::kSmall;
   float* s_o = reinterpret_cast<float*>(slots);                    // [warp][TR][kOut], over the slots
   float2* s_ml = reinterpret_cast<float2*>(slots);                 // [partial][TR], over the slots
   static_assert((int)kC16Ctas * 16 * 8 <= kWarps * S::NS * S::kStage && 16 * S::kOut * 4 <= S::NS * S::kStage, "");
   const uint32_t my_slots = sm_q + S::kQ + S::kSmall + warp * (NS * S::kStage);
 
-  // ---- this CTA's share of all steps
-  // Counted over all jobs one after the other, kStart for each before its steps.
+  // ---- this CTA's share
+  // All jobs one after the other.  Few jobs: each is split into even parts of `most` steps at most, a part to a CTA.  Else
+  // equal shares of the row go over the jobs' ends, each job counted as its steps and kStart.
   uint64_t at, end, share;
-  uint32_t s;
+  uint32_t s, most = 0;
   uint64_t base;  // where sequence s begins
   {
     const uint32_t per = (p.n_seqs + threads - 1u) / threads, i0 = min(tid * per, p.n_seqs), i1 = min(i0 + per, p.n_seqs);
+    if (p.even) {
+      unsigned long long steps = 0, jobs = 0;
+      for (uint32_t i = i0; i < i1; ++i) {
+        const Seq16 y = seq16<D, PAGED16, TR>(p, i, 0u);
+        steps += (unsigned long long)y.steps * y.jobs;
+        jobs += y.jobs;
+      }
+#pragma unroll
+      for (int d = 16; d; d /= 2) {
+        steps += __shfl_xor_sync(0xffffffffu, steps, d);
+        jobs += __shfl_xor_sync(0xffffffffu, jobs, d);
+      }
+      if (lane == 0u) s_tot[warp] = steps, s_tot[kWarps + warp] = jobs;
+      cta_sync();
+      steps = jobs = 0;
+#pragma unroll
+      for (uint32_t w = 0; w < W; ++w) steps += s_tot[w], jobs += s_tot[kWarps + w];
+      cta_sync();
+      // the parts of all jobs number steps / most, and one more at most for each job
+      if (2u * jobs <= gridDim.x)
+        most = max((uint32_t)div64(steps + gridDim.x - jobs - 1u, gridDim.x - jobs), kLeast - kStart);
+    }
     unsigned long long mine = 0;
-    for (uint32_t i = i0; i < i1; ++i) mine += seq16<D, PAGED16, TR>(p, i).all;
+    for (uint32_t i = i0; i < i1; ++i) {
+      const Seq16 y = seq16<D, PAGED16, TR>(p, i, most);
+      mine += (unsigned long long)y.len * y.jobs;
+    }
     unsigned long long inc = mine;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -242,11 +270,12 @@ __global__ void __launch_bounds__(kThreads16) c16_step_kernel(const __grid_const
     if (lane == 31u) s_tot[warp] = inc;
     cta_sync();
     unsigned long long before = 0, total = 0;
+#pragma unroll
     for (uint32_t w = 0; w < W; ++w) {
       before += w < warp ? s_tot[w] : 0ull;
       total += s_tot[w];
     }
-    share = max((unsigned long long)div64(total + gridDim.x - 1u, gridDim.x), (unsigned long long)kLeast);
+    share = most ? 1ull : max((unsigned long long)div64(total + gridDim.x - 1u, gridDim.x), (unsigned long long)kLeast);
     at = (uint64_t)blockIdx.x * share;
     if (at >= total) return;
     end = min(at + share, (uint64_t)total);
@@ -254,7 +283,8 @@ __global__ void __launch_bounds__(kThreads16) c16_step_kernel(const __grid_const
     if (pre <= at && at < pre + mine) {
       uint32_t i = i0;
       for (;; ++i) {
-        const uint64_t n = seq16<D, PAGED16, TR>(p, i).all;
+        const Seq16 y = seq16<D, PAGED16, TR>(p, i, most);
+        const unsigned long long n = (unsigned long long)y.len * y.jobs;
         if (at < pre + n) break;
         pre += n;
       }
@@ -272,31 +302,41 @@ __global__ void __launch_bounds__(kThreads16) c16_step_kernel(const __grid_const
   const uint32_t k_at = my_slots + (lane & 15u) * S::kPitch + ((lane >> 4) << 4);
   const uint32_t v_at = my_slots + (TS + (lane & 7u) + ((lane >> 4) << 3)) * S::kPitch + (((lane >> 3) & 1u) << 4);
 
-  Seq16 x = seq16<D, PAGED16, TR>(p, s);
+  Seq16 x = seq16<D, PAGED16, TR>(p, s, most);
   const uint64_t begin = at;
-  const uint64_t job = div64(at - base, x.steps + kStart);
-  uint64_t job0 = base + job * (x.steps + kStart);  // where the job begins
+  const uint64_t job = div64(at - base, x.len);
+  uint64_t job0 = base + job * x.len;  // where the job begins
   uint32_t tile = job < p.H ? 0u : (uint32_t)div64(job, p.H), head = (uint32_t)(job - (uint64_t)tile * p.H);
   for (bool first = true; at < end; first = false) {
     if (!first) {  // the next job: at is where it begins
       job0 = at;
       if (++head == p.H) head = 0, ++tile;
-      while (at >= base + x.all) {  // the next sequence (one without new tokens has no jobs)
-        base += x.all;
-        x = seq16<D, PAGED16, TR>(p, ++s);
+      while (at >= base + (uint64_t)x.len * x.jobs) {  // the next sequence (one without new tokens has no jobs)
+        base += (uint64_t)x.len * x.jobs;
+        x = seq16<D, PAGED16, TR>(p, ++s, most);
         head = tile = 0;
       }
     }
-    const uint32_t len = x.steps + kStart;
-    const uint32_t from = (uint32_t)(at - job0), to = (uint32_t)min((uint64_t)len, end - job0);
+    const uint32_t from = (uint32_t)(at - job0), to = (uint32_t)min((uint64_t)x.len, end - job0);
     at = job0 + to;
-    // the steps of [from, to), kStart of which are none
-    const uint32_t step0 = max(from, kStart) - kStart, n_steps = max(to, kStart) - kStart - step0;
-    if (n_steps == 0u) continue;  // the CTA after this one begins the job
-    // the CTAs that hold parts of the job: the one whose share has its first step, and those up to its last
-    uint32_t cta0 = blockIdx.x, n_parts = 1u;
-    if (job0 + kStart < begin) cta0 = (uint32_t)div64(job0 + kStart, share);
-    if (cta0 != blockIdx.x || job0 + len > end) n_parts = (uint32_t)div64(job0 + len - 1u, share) - cta0 + 1u;
+    // the steps of this part, the CTA of the job's first part, and how many there are
+    uint32_t step0, n_steps, cta0 = blockIdx.x, n_parts = 1u;
+    if (most) {
+      const uint32_t size = x.len == 1u ? x.steps : (uint32_t)div64(x.steps + x.len - 1u, x.len);
+      step0 = from * size;
+      if (step0 >= x.steps) break;  // (even parts may be one fewer)
+      n_steps = min(size, x.steps - step0);
+      cta0 = blockIdx.x - from;
+      n_parts = x.len == 1u ? 1u : (uint32_t)div64(x.steps + size - 1u, size);
+    } else {
+      // the steps of [from, to), kStart of which are none; a job's parts are with the CTA whose share has its first step and
+      // those up to its last
+      step0 = max(from, kStart) - kStart;
+      n_steps = max(to, kStart) - kStart - step0;
+      if (n_steps == 0u) continue;  // the CTA after this one begins the job
+      if (job0 + kStart < begin) cta0 = (uint32_t)div64(job0 + kStart, share);
+      if (cta0 != blockIdx.x || job0 + x.len > end) n_parts = (uint32_t)div64(job0 + x.len - 1u, share) - cta0 + 1u;
+    }
 
     const uint32_t r0 = tile * TR, n_rows = min((uint32_t)TR, (uint32_t)x.q.n_new * p.G - r0);
     const int32_t first_pos = x.q.start + (int32_t)div_g(p, r0), last_pos = x.q.start + (int32_t)div_g(p, r0 + n_rows - 1u);
@@ -796,9 +836,14 @@ int step_d(const C16Params& p, uint32_t ctas, void* stream) {
 
 // Two CTAs an SM (one for D = 256), fewer where the batch cannot have as many shares: host fields only, the device finds
 // how many steps there are.
-int launch_c16_attend(const C16Params& p, uint64_t jobs, uint64_t keys, void* stream) {
-  const uint64_t steps = jobs * (keys / (p.D >= 128u ? 16u : 32u) + 2u + kStart);
-  const uint32_t ctas = (uint32_t)std::min<uint64_t>(p.D == 256u ? kC8Sms : kC16Ctas, (steps + kLeast - 1u) / kLeast);
+int launch_c16_attend(const C16Params& params, uint64_t jobs, uint64_t keys, void* stream) {
+  C16Params p = params;
+  const uint64_t most = p.D == 256u ? kC8Sms : kC16Ctas, steps = keys / (p.D >= 128u ? 16u : 32u) + 2u;
+  // Up to half as many jobs as CTAs: even parts, one to a CTA, cost some CTAs at worst and no CTA two jobs (48 sequences with one KV
+  // head, 96 jobs: 24.3 us with shares).
+  p.even = 2u * jobs <= most ? 1u : 0u;
+  const uint32_t ctas = (uint32_t)std::min<uint64_t>(
+      most, p.even ? jobs * ((steps + kLeast - kStart - 1u) / (kLeast - kStart) + 1u) : (jobs * (steps + kStart) + kLeast - 1u) / kLeast);
   KVC_C8_DISPATCH(step_d, p, ctas, stream);
 }
 

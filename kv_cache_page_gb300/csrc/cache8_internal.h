@@ -76,6 +76,7 @@ struct AppendParams : C8Params {
 // Attention over 16-bit pages (strides in bytes, scales NULL).
 struct C16Params : C8Params {
   uint32_t tile_rows;           // rows of a tile: 8 where one token's query heads fit, else 16
+  uint32_t even;                // the jobs may be few enough to split each into even parts
   uint32_t g_magic, g_shift;    // n / G = (umulhi(g_magic, n) + n) >> g_shift, n < 2^31
 };
 
