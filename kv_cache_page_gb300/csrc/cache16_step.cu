@@ -128,7 +128,7 @@ __device__ __forceinline__ float2 ld_join2(const float* ptr) {
   return __ldcg(reinterpret_cast<const float2*>(ptr));
 }
 
-// Warps of a CTA, two of which share an SM (one for D = 256): the start of a job and the joins of one hide behind
+// Warps of a CTA, two of which share an SM: the start of a job and the joins of one hide behind
 // the other.  CTAs of 8 warps, one an SM: 64 uneven sequences 103 us against 101, 48 with one KV head 27 against 25.
 constexpr int kWarps = 4, kThreads16 = 32 * kWarps;
 // What a job costs its CTA besides its steps (its first copies, the joins), in steps: some 5 us.  Shares that did not
@@ -146,12 +146,14 @@ struct Shape16 {
   static constexpr int RPI = 32 / C;               // rows that a warp's copy instruction covers
   // Rows lie an odd number of chunks apart: 8 rows' chunks of one column are in 8 different bank groups.
   static constexpr int kPitch = D * 2 + 16;
-  static constexpr int kStage = 2 * TS * kPitch;   // K's rows, then V's
-  static constexpr int NS = D == 32 ? 4 : 3;
+  static constexpr int kSlot = TS * kPitch;        // K's rows of a step, or V's
+  // Steps that copies are ahead; a warp's slots hold these, K and V one after the other, and the K or V in use.
+  static constexpr int kAhead = D == 256 ? 1 : D == 32 ? 3 : 2;
+  static constexpr int NS = 2 * kAhead + 1;
   static constexpr int kQ = 16 * kPitch;
   static constexpr int kSmall = 1024;
   static constexpr int kOut = D + 4;               // floats of a row in the join of the warps
-  static constexpr int kSmem = kQ + kSmall + kWarps * NS * kStage;
+  static constexpr int kSmem = kQ + kSmall + kWarps * NS * kSlot;
 };
 // n / G for n < 2^31
 __device__ __forceinline__ uint32_t div_g(const C16Params& p, uint32_t n) {
@@ -207,7 +209,7 @@ __device__ __forceinline__ Seq16 seq16(const C16Params& p, uint32_t s, uint32_t 
 template <int DT, int D, bool PAGED16, int NT>
 __global__ void __launch_bounds__(kThreads16) c16_step_kernel(const __grid_constant__ C16Params p) {
   using S = Shape16<D>;
-  constexpr int NS = S::NS, TS = S::TS, HT = S::HT, TR = 8 * NT, KS = D / 16;
+  constexpr int NS = S::NS, kAhead = S::kAhead, TS = S::TS, HT = S::HT, TR = 8 * NT, KS = D / 16;
   constexpr uint32_t kFull = TS == 32 ? 0xffffffffu : 0xffffu;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t tid = threadIdx.x, lane = tid & 31u, warp = tid >> 5;
@@ -223,8 +225,8 @@ __global__ void __launch_bounds__(kThreads16) c16_step_kernel(const __grid_const
   uint8_t* slots = smem + S::kQ + S::kSmall;
   float* s_o = reinterpret_cast<float*>(slots);                    // [warp][TR][kOut], over the slots
   float2* s_ml = reinterpret_cast<float2*>(slots);                 // [partial][TR], over the slots
-  static_assert((int)kC16Ctas * 16 * 8 <= kWarps * S::NS * S::kStage && 16 * S::kOut * 4 <= S::NS * S::kStage, "");
-  const uint32_t my_slots = sm_q + S::kQ + S::kSmall + warp * (NS * S::kStage);
+  static_assert((int)kC16Ctas * 16 * 8 <= kWarps * S::NS * S::kSlot && 16 * S::kOut * 4 <= S::NS * S::kSlot, "");
+  const uint32_t my_slots = sm_q + S::kQ + S::kSmall + warp * (NS * S::kSlot);
 
   // ---- this CTA's share
   // All jobs one after the other.  Few jobs: each is split into even parts of `most` steps at most, a part to a CTA.  Else
@@ -300,7 +302,7 @@ __global__ void __launch_bounds__(kThreads16) c16_step_kernel(const __grid_const
   const uint32_t c_row = lane / S::C, c_chunk = lane % S::C;
   const uint32_t c_dst = my_slots + c_row * S::kPitch + c_chunk * 16;
   const uint32_t k_at = my_slots + (lane & 15u) * S::kPitch + ((lane >> 4) << 4);
-  const uint32_t v_at = my_slots + (TS + (lane & 7u) + ((lane >> 4) << 3)) * S::kPitch + (((lane >> 3) & 1u) << 4);
+  const uint32_t v_at = my_slots + ((lane & 7u) + ((lane >> 4) << 3)) * S::kPitch + (((lane >> 3) & 1u) << 4);
 
   Seq16 x = seq16<D, PAGED16, TR>(p, s, most);
   const uint64_t begin = at;
@@ -356,28 +358,28 @@ __global__ void __launch_bounds__(kThreads16) c16_step_kernel(const __grid_const
     };
     const uint8_t* k_src = p.k + (int64_t)head * p.sh + c_chunk * 16 + (PAGED16 ? (int64_t)c_row * p.st : 0);
     const uint8_t* v_src = p.v + (int64_t)head * p.sh + c_chunk * 16 + (PAGED16 ? (int64_t)c_row * p.st : 0);
-    // Start the copies of step t.  Tokens that no row sees, and those without a page, become zeros.  Returns the
-    // tokens that are there, a bit each.
-    auto issue = [&](int32_t t, int stage, int32_t entry) -> uint32_t {
-      const uint32_t dst = c_dst + stage * S::kStage;
+    // Where the lane's token of step t lies; returns the tokens that are there, a bit each.
+    auto place = [&](int32_t t, int32_t entry, int64_t& off) -> uint32_t {
       const int32_t tok = x.lo + TS * t + (int32_t)(lane % TS);
       const bool in = tok >= t_lo && tok < t_hi, page = (uint32_t)entry < p.num_blocks;
       bad |= in && !page;
-      const uint32_t there = __ballot_sync(0xffffffffu, in && page) & kFull;
       const uint32_t in_page = (uint32_t)tok - c8_div_t(p, (uint32_t)tok) * p.T;
-      const int64_t off = (int64_t)entry * p.sb + (int64_t)in_page * p.st;
+      off = (int64_t)entry * p.sb + (int64_t)in_page * p.st;
+      return __ballot_sync(0xffffffffu, in && page) & kFull;
+    };
+    // Start the copies of a step's K or V.  Tokens that no row sees, and those without a page, become zeros.
+    auto issue = [&](const uint8_t* src, int slot, uint32_t there, int64_t off) {
+      const uint32_t dst = c_dst + slot * S::kSlot;
 #pragma unroll
       for (int h = 0; h < HT; ++h) {
         const uint32_t bits = HT == 1 ? there : (there >> (16 * h)) & 0xffffu;
         const int64_t tile_off = __shfl_sync(0xffffffffu, off, 16 * h);
         if (PAGED16 && bits == 0xffffu) {
-          const uint8_t *ks = k_src + tile_off, *vs = v_src + tile_off;
+          const uint8_t* at = src + tile_off;
 #pragma unroll
           for (int i = 0; i < 16 / S::RPI; ++i) {
-            cp16(dst + (16 * h + i * S::RPI) * S::kPitch, ks);
-            cp16(dst + (TS + 16 * h + i * S::RPI) * S::kPitch, vs);
-            ks += S::RPI * p.st;
-            vs += S::RPI * p.st;
+            cp16(dst + (16 * h + i * S::RPI) * S::kPitch, at);
+            at += S::RPI * p.st;
           }
         } else {
 #pragma unroll 4
@@ -385,22 +387,20 @@ __global__ void __launch_bounds__(kThreads16) c16_step_kernel(const __grid_const
             const uint32_t row = c_row + S::RPI * i;
             const bool ok = (bits >> row) & 1u;
             const int64_t o = PAGED16 ? tile_off + (int64_t)(S::RPI * i) * p.st : __shfl_sync(0xffffffffu, off, 16 * h + row);
-            cp16z(dst + (16 * h + i * S::RPI) * S::kPitch, ok ? k_src + o : p.k, ok);
-            cp16z(dst + (TS + 16 * h + i * S::RPI) * S::kPitch, ok ? v_src + o : p.v, ok);
+            cp16z(dst + (16 * h + i * S::RPI) * S::kPitch, ok ? src + o : p.k, ok);
           }
         }
       }
-      return there;
     };
 
     cta_sync();  // the job before is done with shared memory
-    uint32_t there[NS];  // of the stages in flight, the oldest first
+    uint32_t there[kAhead + 1];  // of the steps in flight, the oldest first
     int32_t entry;
     {
-      int32_t e[NS - 1];
+      int32_t e[kAhead];
 #pragma unroll
-      for (int i = 0; i < NS - 1; ++i) e[i] = entry_of(x_lo + (int32_t)(warp + i * W));
-      entry = entry_of(x_lo + (int32_t)(warp + (NS - 1) * W));
+      for (int i = 0; i < kAhead; ++i) e[i] = entry_of(x_lo + (int32_t)(warp + i * W));
+      entry = entry_of(x_lo + (int32_t)(warp + kAhead * W));
       for (uint32_t i = tid; i < TR * (D / 8); i += threads) {
         const uint32_t r = i / (D / 8), c = i % (D / 8), rr = r0 + min(r, n_rows - 1u), tok = div_g(p, rr);
         const uint16_t* src = p.a + ((int64_t)x.q.row + tok) * p.a_row + (int64_t)(head * p.G + rr - tok * p.G) * p.a_head + c * 8;
@@ -408,13 +408,22 @@ __global__ void __launch_bounds__(kThreads16) c16_step_kernel(const __grid_const
       }
       cp_commit();
 #pragma unroll
-      for (int i = 0; i < NS - 1; ++i) {
+      for (int i = 0; i < kAhead; ++i) {
         const int32_t t = x_lo + (int32_t)(warp + i * W);
-        there[i] = t < x_hi ? issue(t, i, e[i]) : 0u;
+        there[i] = 0u;
+        if (t < x_hi) {
+          int64_t off;
+          there[i] = place(t, e[i], off);
+          issue(k_src, 2 * i, there[i], off);
+          cp_commit();
+          issue(v_src, 2 * i + 1, there[i], off);
+        } else {
+          cp_commit();
+        }
         cp_commit();
       }
     }
-    cp_wait<NS - 1>();  // the queries
+    cp_wait<2 * kAhead>();  // the queries
     cta_sync();
     // the queries' fragments: in registers, or (where the sums leave no room) read again at each step
     constexpr bool kHeld = D < 256;
@@ -439,26 +448,26 @@ __global__ void __launch_bounds__(kThreads16) c16_step_kernel(const __grid_const
 #pragma unroll
     for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = kNegInf, l[n][0] = l[n][1] = 0.0f;
 
-    int stage = 0;
+    int slot = 0;  // of K; V's is the next one
     for (int32_t t = x_lo + (int32_t)warp; t < x_hi; t += (int32_t)W) {
-      {
-        const int32_t tn = t + (int32_t)((NS - 1) * W);
-        __syncwarp();  // every lane is done with the stage that is refilled
-        there[NS - 1] = 0u;
-        if (tn < x_hi) {
-          const int32_t e = entry;
-          entry = entry_of(tn + (int32_t)W);
-          there[NS - 1] = issue(tn, stage == 0 ? NS - 1 : stage - 1, e);
-        }
-        cp_commit();
-        cp_wait<NS - 1>();
-        __syncwarp();  // the other lanes' copies
+      const int32_t tn = t + (int32_t)(kAhead * W);
+      int64_t off = 0;
+      __syncwarp();  // every lane is done with the slot that is refilled
+      there[kAhead] = 0u;
+      if (tn < x_hi) {
+        there[kAhead] = place(tn, entry, off);
+        entry = entry_of(tn + (int32_t)W);
+        issue(k_src, slot == 0 ? NS - 1 : slot - 1, there[kAhead], off);
       }
-      const uint32_t bits = there[0];
-      const uint32_t sk = k_at + stage * S::kStage, sv = v_at + stage * S::kStage;
+      cp_commit();
+      cp_wait<2 * kAhead>();
+      __syncwarp();  // the other lanes' copies
+      const uint32_t bits = there[0], more = there[kAhead];
+      const uint32_t sk = k_at + slot * S::kSlot, sv = v_at + (slot == NS - 1 ? 0 : slot + 1) * S::kSlot;
+      const int k_slot = slot;
 #pragma unroll
-      for (int i = 0; i < NS - 1; ++i) there[i] = there[i + 1];
-      stage = stage == NS - 1 ? 0 : stage + 1;
+      for (int i = 0; i < kAhead; ++i) there[i] = there[i + 1];
+      slot = slot >= NS - 2 ? slot + 2 - NS : slot + 2;
       const int32_t tok0 = x.lo + TS * t;
 
       // scores of tokens 16 h + g, + 8 and rows 8 n + 2 qd, + 1
@@ -494,6 +503,9 @@ __global__ void __launch_bounds__(kThreads16) c16_step_kernel(const __grid_const
 #pragma unroll
           for (int e = 0; e < 4; ++e) z[h][n][e] = (Z == 2 ? y[0][n][e] + y[Z - 1][n][e] : y[0][n][e]) * p.scale_log2;
       }
+      __syncwarp();  // K's slot is read
+      if (tn < x_hi) issue(v_src, k_slot, more, off);
+      cp_commit();
       const bool by_row = tok0 + TS > full_hi || tok0 < full_lo;
       if (by_row || bits != kFull) {
 #pragma unroll
@@ -565,6 +577,8 @@ __global__ void __launch_bounds__(kThreads16) c16_step_kernel(const __grid_const
             wl[h][n][e] = transpose8(pack2<DT>(p0 - lo_f32<DT>(w), p1 - hi_f32<DT>(w)));
           }
       }
+      cp_wait<2 * kAhead>();
+      __syncwarp();  // the other lanes' copies of V
       // V: dims 16 i + g, + 8 of tokens 2 qd, + 1, + 8, + 9
       constexpr uint32_t E = DT == 0 ? 0x7c00u : 0x7f80u, one = DT == 0 ? 0x3c00u : 0x3f80u;
       bool odd = false;
@@ -834,11 +848,11 @@ int step_d(const C16Params& p, uint32_t ctas, void* stream) {
 
 }  // namespace
 
-// Two CTAs an SM (one for D = 256), fewer where the batch cannot have as many shares: host fields only, the device finds
+// Two CTAs an SM, fewer where the batch cannot have as many shares: host fields only, the device finds
 // how many steps there are.
 int launch_c16_attend(const C16Params& params, uint64_t jobs, uint64_t keys, void* stream) {
   C16Params p = params;
-  const uint64_t most = p.D == 256u ? kC8Sms : kC16Ctas, steps = keys / (p.D >= 128u ? 16u : 32u) + 2u;
+  const uint64_t most = kC16Ctas, steps = keys / (p.D >= 128u ? 16u : 32u) + 2u;
   // Up to half as many jobs as CTAs: even parts, one to a CTA, cost some CTAs at worst and no CTA two jobs (48 sequences with one KV
   // head, 96 jobs: 24.3 us with shares).
   p.even = 2u * jobs <= most ? 1u : 0u;
