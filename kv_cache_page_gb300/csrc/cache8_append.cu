@@ -20,7 +20,7 @@ constexpr uint32_t kQueries = 8;  // iterations of a queries' warp: 256 bytes of
 
 struct Append8 : AppendParams {
   RowMap qm;
-  uint32_t page_blocks;
+  uint64_t q_share;  // of the blocks, times 2^32, rounded up: floor(b q_share / 2^32) of the first b blocks turn queries
 };
 
 #ifdef KVC_BOUNDS_CHECK
@@ -39,11 +39,13 @@ __device__ __forceinline__ void prefetch_line(const void* ptr) {
 template <int DT, int D>
 __global__ void __launch_bounds__(kWarps * 32, 2) c8_append_kernel(const __grid_constant__ Append8 p) {
   constexpr int LPR = D / 16, RPI = 32 / LPR, R = 4;  // lanes of a token's row, rows a warp holds at once, times R
-  if (blockIdx.x >= p.page_blocks)
-    return append_queries<DT, D, kQueries>(p, p.qm, (blockIdx.x - p.page_blocks) * kWarps + (threadIdx.x >> 5));
+  // blocks of pages and of queries alternate in proportion: the ones wait for instructions, the others for memory
+  const uint32_t qb = (uint32_t)((blockIdx.x * p.q_share) >> 32);
+  if ((uint32_t)(((blockIdx.x + 1ull) * p.q_share) >> 32) != qb)
+    return append_queries<DT, D, kQueries>(p, p.qm, qb * kWarps + (threadIdx.x >> 5));
   const uint32_t lane = threadIdx.x & 31u;
   PageJob j;
-  if (!page_find(p, blockIdx.x * kWarps + (threadIdx.x >> 5), j) || j.t0 >= j.t1) return;
+  if (!page_find(p, (blockIdx.x - qb) * kWarps + (threadIdx.x >> 5), j) || j.t0 >= j.t1) return;
   j.id = c8_page(p, j.q.s, (uint32_t)j.page);  // (not looked at before the new values have been asked for)
   const int sub = lane / LPR, first = j.t0 + sub;
   const int32_t pos0 = j.page * (int32_t)p.T;
@@ -157,9 +159,9 @@ int append_d(const AppendParams& p, void* stream) {
   const uint64_t warps = (a.both_roles ? 1ull : 2ull) * p.H * p.n_units;
   a.qm = row_map(p.q ? p.n_new : 0u, p.HQ * (D / 16), kQueries);
   const uint64_t pages = (warps + kWarps - 1u) / kWarps;
-  const uint64_t grid = pages + (a.qm.warps + (uint64_t)kWarps - 1u) / kWarps;
+  const uint64_t queries = (a.qm.warps + (uint64_t)kWarps - 1u) / kWarps, grid = pages + queries;
   if (a.qm.warps == 0xffffffffu || grid > 0x7fffffffull || warps > 0xffffffffull) return KV_ERR_INVALID_ARG;
-  a.page_blocks = (uint32_t)pages;
+  a.q_share = ((queries << 32) + grid - 1u) / grid;
   return dbg_launch(
       stream,
       [&] {
