@@ -58,7 +58,9 @@ int kv_cache16_destroy(kv_cache16_t cache);
 /* The batch's new tokens into their pages: keys turned by their positions (rotation NULL:
  * as they are), values as they are; a turned value is rounded once, to nearest even.  q and
  * q_out as for kv_cache8_append.  A token whose page is none, or whose position is
- * negative, is not written (its queries are turned all the same, or become 0). */
+ * negative, is not written (its queries are turned all the same, or become 0).  No two
+ * new tokens of a call may lie in the same place of a page (a shared prefix ends before
+ * them), and k, v and q lie outside the pages. */
 int kv_cache16_append(kv_cache16_t cache, const kv_cache16_layer* layer, const kv_cache8_batch* batch,
                       const kv_cache8_rows* k, const kv_cache8_rows* v, const kv_cache8_rotation* rotation,
                       const kv_cache8_rows* q, const kv_cache8_rows* q_out, void* stream);

@@ -273,6 +273,43 @@ def test_one_workspace_for_every_batch_and_for_the_8_bit_cache():
                 assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
 
 
+@pytest.mark.parametrize("new", [None, [9, 1, 4]])
+def test_hints_that_are_too_small_cost_time_alone(new):
+    """max_new and max_len below what the arrays hold: every row is served all the same."""
+    lens = [2100, 40, 700]
+    su = R.Setup(D=64, H=1, T=16, lens=lens, dtype="bf16", seed=4)
+    su.fill()
+    n = sum(new) if new else 3
+    c, layer, full = su.cache(cache16, 4), su.device_layer(cache16), su.batch(cache8, new)
+    b = cache8.Batch(full.tables, full.lens, full.cu_new, n_new=n, max_new=1, max_len=1)
+    q = su.values(n, 4)
+    out, lse = torch.empty(n, 4, 64, dtype=su.dtype, device=DEV), torch.empty(n, 4, device=DEV)
+    c.attend(layer, b, q.to(DEV), out, lse=lse, workspace=torch.zeros(c.attend_workspace(b), dtype=torch.uint8, device=DEV))
+    _check(su, lens, new, q, out.cpu().double(), lse.cpu().double())
+
+
+def test_pages_shared_between_sequences():
+    """A common prefix of whole pages in several tables."""
+    lens = [100, 100, 70, 64]
+    su = R.Setup(D=128, H=1, T=16, lens=lens, dtype="fp16", seed=4)
+    su.fill()
+    su.tables[1:, :4] = su.tables[0, :4]
+    q, out, lse = _attend(su, lens, None, 8)
+    _check(su, lens, None, q, out, lse)
+
+
+@pytest.mark.parametrize("window", [0, 33, 90])
+def test_tables_that_end_before_the_window(window):
+    """Lengths past the table: what lies in it is seen where the window reaches it, and rows may see nothing at all."""
+    lens = [200, 90, 50]
+    su = R.Setup(D=64, H=2, T=16, lens=[48, 48, 48], dtype="bf16", seed=3)
+    su.fill()
+    errors = torch.zeros(3, dtype=torch.int32, device=DEV)
+    q, out, lse = _attend(su, lens, None, 4, window=window, errors=errors)
+    _check(su, lens, None, q, out, lse, window=window)
+    assert errors.tolist() == [1, 1, 1]
+
+
 def test_strided_queries_and_outputs():
     lens = [90, 17]
     su = R.Setup(D=64, H=2, T=16, lens=lens, dtype="bf16", seed=4)
