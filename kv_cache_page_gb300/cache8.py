@@ -53,6 +53,11 @@ class _Rows(C.Structure):
     _fields_ = [("data", C.c_void_p), ("stride_row", C.c_int64), ("stride_head", C.c_int64)]
 
 
+# two and four of these side by side in one array (0.3 us less a call than as many structures)
+_Rows2, _Rows4 = C.c_int64 * 6, C.c_int64 * 12
+assert C.sizeof(_Rows) == 24
+
+
 class _Rotation(C.Structure):
     _fields_ = [("struct_size", C.c_uint32), ("dim", C.c_uint32), ("positions", C.c_uint32), ("flags", C.c_uint32),
                 ("cos", C.c_void_p), ("sin", C.c_void_p), ("stride", C.c_int64)]
@@ -187,17 +192,18 @@ class Rotation:
 class _Cache:
     """What the 8-bit and the 16-bit cache share: rows, and the calls that take them."""
 
-    def _rows(self, t, batch, heads, name):
-        if t.dtype is not self.dtype or not t.is_cuda or t.get_device() != batch.device:
+    def _row(self, t, batch, heads, name):
+        """Pointer and strides of rows [n_new, heads, head_dim], as _Rows has them."""
+        if t.dtype is not self.dtype or t.get_device() != batch.device:  # (a tensor of the CPU is on device -1)
             raise ValueError(f"{name} must be a {self.dtype} CUDA tensor on the batch's device")
-        row, head, one = t.stride() if t.dim() == 3 else (0, 0, 0)
-        if one != 1 or t.shape != (batch.n_new, heads, self.head_dim):
+        stride = t.stride()
+        if t.shape != (batch.n_new, heads, self.head_dim) or stride[2] != 1:
             raise ValueError(f"{name} must be [{batch.n_new}, {heads}, {self.head_dim}] with values side by side")
-        return _Rows(t.data_ptr(), row, head)
+        return t.data_ptr(), stride[0], stride[1]
 
     def _append_call(self, call, what, layer, batch, k, v, rotation, q, q_out, stream):
-        kr, vr = self._rows(k, batch, self.num_kv_heads, "k"), self._rows(v, batch, self.num_kv_heads, "v")
-        qr = qo = turn = None
+        rows = self._row(k, batch, self.num_kv_heads, "k") + self._row(v, batch, self.num_kv_heads, "v")
+        turn = None
         if rotation is not None:
             if rotation.device != batch.device:
                 raise ValueError("the rotation must be on the batch's device")
@@ -205,14 +211,20 @@ class _Cache:
         if (q is None) != (q_out is None) or (q is not None and turn is None):
             raise ValueError("q and q_out go together, and with a rotation")
         if q is not None:
-            qr, qo = self._rows(q, batch, self.num_q_heads, "q"), self._rows(q_out, batch, self.num_q_heads, "q_out")
-        rc = call(self._h, self._layer(layer, batch), batch._ref, C.addressof(kr), C.addressof(vr), turn,
-                  qr and C.addressof(qr), qo and C.addressof(qo), _stream(stream, batch.device))
+            rows = _Rows4(*rows, *self._row(q, batch, self.num_q_heads, "q"), *self._row(q_out, batch, self.num_q_heads, "q_out"))
+            at = C.addressof(rows)
+            rc = call(self._h, self._layer(layer, batch), batch._ref, at, at + 24, turn, at + 48, at + 72,
+                      _stream(stream, batch.device))
+        else:
+            rows = _Rows2(*rows)
+            at = C.addressof(rows)
+            rc = call(self._h, self._layer(layer, batch), batch._ref, at, at + 24, turn, None, None,
+                      _stream(stream, batch.device))
         if rc:
             _codec._check(rc, what)
 
     def _attend_call(self, call, what, layer, batch, q, out, lse, scale, causal, window, workspace, stream):
-        qr, outr = self._rows(q, batch, self.num_q_heads, "q"), self._rows(out, batch, self.num_q_heads, "out")
+        rows = _Rows2(*self._row(q, batch, self.num_q_heads, "q"), *self._row(out, batch, self.num_q_heads, "out"))
         at = None
         if lse is not None:
             if lse.dtype is not torch.float32 or not lse.is_cuda or lse.shape != (batch.n_new, self.num_q_heads) or \
@@ -232,8 +244,9 @@ class _Cache:
             if not workspace.is_cuda or not workspace.is_contiguous() or workspace.get_device() != batch.device:
                 raise ValueError("workspace must be a contiguous CUDA tensor on the batch's device")
             ws, nb = workspace.data_ptr(), workspace.nbytes
-        rc = call(self._h, self._layer(layer, batch), batch._ref, C.addressof(qr), C.addressof(outr), at, scale,
-                  window, CAUSAL if causal else 0, ws, nb, _stream(stream, batch.device))
+        first = C.addressof(rows)
+        rc = call(self._h, self._layer(layer, batch), batch._ref, first, first + 24, at, scale, window,
+                  CAUSAL if causal else 0, ws, nb, _stream(stream, batch.device))
         if rc:
             _codec._check(rc, what)
 
@@ -293,9 +306,9 @@ class Cache8(_Cache):
         """Quantise the batch's new tokens (k, v: [n_new, num_kv_heads, head_dim]) into
         their pages; a page's scale grows where the new values need it, and its earlier
         codes are rewritten under the grown scale."""
-        kr, vr = self._rows(k, batch, self.num_kv_heads, "k"), self._rows(v, batch, self.num_kv_heads, "v")
-        rc = self._write(self._h, self._layer(layer, batch), batch._ref, C.addressof(kr), C.addressof(vr),
-                         _stream(stream, batch.device))
+        rows = _Rows2(*self._row(k, batch, self.num_kv_heads, "k"), *self._row(v, batch, self.num_kv_heads, "v"))
+        at = C.addressof(rows)
+        rc = self._write(self._h, self._layer(layer, batch), batch._ref, at, at + 24, _stream(stream, batch.device))
         if rc:
             _codec._check(rc, "kv_cache8_write")
 
@@ -308,9 +321,9 @@ class Cache8(_Cache):
 
     def read(self, layer: Layer, batch: Batch, k, v, stream=None):
         """The batch's new tokens back in 16 bits, into k and v."""
-        kr, vr = self._rows(k, batch, self.num_kv_heads, "k"), self._rows(v, batch, self.num_kv_heads, "v")
-        rc = self._read(self._h, self._layer(layer, batch), batch._ref, C.addressof(kr), C.addressof(vr),
-                        _stream(stream, batch.device))
+        rows = _Rows2(*self._row(k, batch, self.num_kv_heads, "k"), *self._row(v, batch, self.num_kv_heads, "v"))
+        at = C.addressof(rows)
+        rc = self._read(self._h, self._layer(layer, batch), batch._ref, at, at + 24, _stream(stream, batch.device))
         if rc:
             _codec._check(rc, "kv_cache8_read")
 
