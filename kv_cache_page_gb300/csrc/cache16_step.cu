@@ -139,7 +139,9 @@ constexpr int kWarps = 4, kThreads16 = 32 * kWarps;
 // one KV head 26.6, 26.5, 24.6, 24.6, 24.6 us, 64 uneven ones 102, 100, 101, 102, 102.
 constexpr uint32_t kStart = 16;
 constexpr uint32_t kLeast = kStart + 4;  // of a share
-constexpr uint32_t kFlat = 12;  // partials that are joined at once
+// Partials that are joined at once; more are joined in groups.  One sequence of 131072, 4 heads, 76 partials: at once 64 us, in
+// groups of nine 58; 65536, 8 heads, 38 partials: 59 and 57; between 12 and 24 it makes no difference.
+constexpr uint32_t kFlat = 12;
 
 template <int D>
 struct Shape16 {
