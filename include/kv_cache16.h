@@ -72,8 +72,8 @@ int kv_cache16_append(kv_cache16_t cache, const kv_cache16_layer* layer, const k
  * GPU by the lengths found on the device; parts of a row are joined in a fixed order, so the
  * result does not depend on timing.
  * Products accumulate in FP32; maxima, sums and joins are FP32.  The weights of V go into
- * the product as two 16-bit terms, which together hold them to 2^-16 (BF16) or 2^-22 (FP16;
- * to 2^-36 of the row's largest weight at worst).  What a row does not see, or what lies in
+ * the product as 16-bit terms, three of BF16 or two of FP16, which together hold them to
+ * 2^-24 (BF16) or 2^-22 (FP16; to 2^-36 of the row's largest weight at worst).  What a row does not see, or what lies in
  * a page past its sequence's length, does not reach it, NaN and infinities included; a row
  * that sees an infinity or a NaN has outputs that are not finite. */
 int kv_cache16_attend(kv_cache16_t cache, const kv_cache16_layer* layer, const kv_cache8_batch* batch,

@@ -18,9 +18,9 @@
 //
 // Both products have the tokens (scores) and the dims (outputs) as their 16 rows and 8 query
 // rows as their columns: K's tile is the operand as it lies, V's as ldmatrix transposes it,
-// and the weights pass through a transposition in registers.  A weight is split into two
-// 16-bit terms (the second product is made twice, for 0 to 3 % of the time): with one, BF16
-// weights alone would be as coarse as the output's rounding.
+// and the weights pass through a transposition in registers.  A weight is split into 16-bit
+// terms, two of FP16 or three of BF16, with a product for each, so that it keeps what FP32
+// arithmetic gave it (two BF16 terms were 0 to 1 % faster with 8 query rows, 2 to 8 with 16).
 //
 // Measured on a GB300, 8 heads of 128: 64 sequences of 100 to 8192 tokens 99 us (5.7 TB/s; a plain
 // copy 6.8), one of 131072 with 4 heads 57 us (4.7; the walk 36 to 41 us of it, 4 to start, 8 to join).
@@ -53,10 +53,16 @@ namespace {
 constexpr float kNegInf = -INFINITY;
 // m may lag the true maximum by kLag (fewer rescalings of the sums).
 constexpr float kLag = 4.0f;
-// Weights are held as 2^(z - m + bias).  FP16: largest 2^11 .. 2^15, so that 2^-25, half of the smallest FP16, is 2^-36 of the
-// largest.  BF16: 2^-24 .. 2^-20, so that sums over 2^20 keys of V next to 2^128 stay in FP32's range.
+// A weight 2^(z - m) enters V's product times this.  FP16: the largest are 2^11 .. 2^15, so that 2^-25, half of the smallest
+// FP16, is 2^-36 of the largest.  BF16: 2^-24 .. 2^-20, so that sums over 2^20 keys of V next to 2^128 stay in FP32's range.
+// (A factor is exact; added to the exponent it would cost the score bits: 24 holds 2^-19 of it.)
 template <int DT>
-constexpr float kBias = DT == 0 ? 11.0f : -24.0f;
+constexpr float kHold = DT == 0 ? 0x1p11f : 0x1p-24f;
+// It enters as this many 16-bit terms, each the nearest to what the earlier ones leave: 24 bits in three BF16 terms, 22 in two of
+// FP16, as fine as ex2.approx (2^-22).  One BF16 term would be as coarse as the output's rounding; two (2^-18) showed in outputs
+// whose values nearly cancel.
+template <int DT>
+constexpr int kTerms = DT == 0 ? 2 : 3;
 
 // A barrier of the CTA that counts threads, whether or not their warp is converged.
 __device__ __forceinline__ void cta_sync() { asm volatile("barrier.sync 0;" ::: "memory"); }
@@ -564,22 +570,25 @@ __global__ void __launch_bounds__(kThreads16) c16_step_kernel(const __grid_const
             }
           }
       }
-      // weights, split in two terms and transposed: row g, tokens 2 qd, + 1 (+ 8 e)
-      uint32_t wh[HT][NT][2], wl[HT][NT][2];
+      // weights, split in terms and transposed: row g, tokens 2 qd, + 1 (+ 8 e)
+      uint32_t w[kTerms<DT>][HT][NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const float b0 = m[n][0] == kNegInf ? 0.0f : m[n][0] - kBias<DT>;
-        const float b1 = m[n][1] == kNegInf ? 0.0f : m[n][1] - kBias<DT>;
+        const float b0 = m[n][0] == kNegInf ? 0.0f : m[n][0], b1 = m[n][1] == kNegInf ? 0.0f : m[n][1];
 #pragma unroll
         for (int h = 0; h < HT; ++h)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float p0 = ex2(z[h][n][2 * e] - b0), p1 = ex2(z[h][n][2 * e + 1] - b1);
+            float p0 = ex2(z[h][n][2 * e] - b0), p1 = ex2(z[h][n][2 * e + 1] - b1);
             l[n][0] += p0;
             l[n][1] += p1;
-            const uint32_t w = pack2<DT>(p0, p1);
-            wh[h][n][e] = transpose8(w);
-            wl[h][n][e] = transpose8(pack2<DT>(p0 - lo_f32<DT>(w), p1 - hi_f32<DT>(w)));
+            p0 *= kHold<DT>, p1 *= kHold<DT>;
+#pragma unroll
+            for (int i = 0; i < kTerms<DT>; ++i) {
+              const uint32_t x = pack2<DT>(p0, p1);
+              w[i][h][n][e] = transpose8(x);
+              p0 -= lo_f32<DT>(x), p1 -= hi_f32<DT>(x);
+            }
           }
       }
       cp_wait<2 * kAhead>();
@@ -606,10 +615,9 @@ __global__ void __launch_bounds__(kThreads16) c16_step_kernel(const __grid_const
             uint32_t a[4];
             ldsm4_t(a, sv + h * 16 * S::kPitch + i * 32);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma16816<DT>(o[i][n], a, wh[h][n][0], wh[h][n][1]);
-              mma16816<DT>(o[i][n], a, wl[h][n][0], wl[h][n][1]);
-            }
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int t = 0; t < kTerms<DT>; ++t) mma16816<DT>(o[i][n], a, w[t][h][n][0], w[t][h][n][1]);
           }
       } else {
         // such values become 0, and NaN is put where they are seen: rows x dims with one, counted by the same product
@@ -633,8 +641,8 @@ __global__ void __launch_bounds__(kThreads16) c16_step_kernel(const __grid_const
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              mma16816<DT>(o[i][n], a, wh[h][n][0], wh[h][n][1]);
-              mma16816<DT>(o[i][n], a, wl[h][n][0], wl[h][n][1]);
+#pragma unroll
+              for (int t = 0; t < kTerms<DT>; ++t) mma16816<DT>(o[i][n], a, w[t][h][n][0], w[t][h][n][1]);
               float cnt[4] = {0.f, 0.f, 0.f, 0.f};
               mma16816<DT>(cnt, b, seen[n][0], seen[n][1]);
 #pragma unroll
@@ -688,11 +696,11 @@ __global__ void __launch_bounds__(kThreads16) c16_step_kernel(const __grid_const
     float* mine = part_of(blockIdx.x - cta0);
     // a row's maximum and sum: the factor of its outputs, and lse
     auto finish_row = [&](uint32_t row, float mx, float ls) {
-      s_fin[row] = make_float2(mx, ls == 0.0f ? 0.0f : 1.0f / ls);
+      s_fin[row] = make_float2(mx, ls == 0.0f ? 0.0f : (1.0f / kHold<DT>) / ls);
       if (p.lse && row < n_rows) {
         const uint32_t rr = r0 + row, tok = div_g(p, rr), hd = head * p.G + rr - tok * p.G;
         st4(p.lse + ((int64_t)x.q.row + tok) * p.HQ + hd,
-            __float_as_uint(ls == 0.0f ? kNegInf : (mx - kBias<DT> + log2f(ls)) * 0.693147180559945309f));
+            __float_as_uint(ls == 0.0f ? kNegInf : (mx + log2f(ls)) * 0.693147180559945309f));
       }
     };
     auto finish_out = [&](uint32_t r, uint32_t d4, float4 y) {
