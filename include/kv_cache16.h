@@ -73,9 +73,12 @@ int kv_cache16_append(kv_cache16_t cache, const kv_cache16_layer* layer, const k
  * result does not depend on timing.
  * Products accumulate in FP32; maxima, sums and joins are FP32.  The weights of V go into
  * the product as 16-bit terms, three of BF16 or two of FP16, which together hold them to
- * 2^-24 (BF16) or 2^-22 (FP16; to 2^-36 of the row's largest weight at worst).  What a row does not see, or what lies in
- * a page past its sequence's length, does not reach it, NaN and infinities included; a row
- * that sees an infinity or a NaN has outputs that are not finite. */
+ * 2^-24 (BF16) or 2^-22 (FP16; to 2^-36 of the row's largest weight at worst).
+ * What a row does not see, or what lies in a page past its sequence's length, does not reach
+ * it, NaN and infinities included.  What it sees does: a NaN or +inf among its scores leaves
+ * it no finite output, an infinity or NaN in V none of that dim.  A key whose score is -inf
+ * weighs 0 (times an infinity or NaN of its value: NaN); a row whose scores are all -inf gets
+ * what a row that sees no key gets. */
 int kv_cache16_attend(kv_cache16_t cache, const kv_cache16_layer* layer, const kv_cache8_batch* batch,
                       const kv_cache8_rows* q, const kv_cache8_rows* out, float* lse, float scale,
                       uint32_t window, uint32_t flags, void* workspace, uint64_t workspace_bytes,

@@ -20,7 +20,7 @@
 // rows as their columns: K's tile is the operand as it lies, V's as ldmatrix transposes it,
 // and the weights pass through a transposition in registers.  A weight is split into 16-bit
 // terms, two of FP16 or three of BF16, with a product for each, so that it keeps what FP32
-// arithmetic gave it (two BF16 terms were 0 to 1 % faster with 8 query rows, 2 to 8 with 16).
+// arithmetic gave it (two BF16 terms were 0 to 3 % faster with 8 query rows, 3 to 7 with 16).
 //
 // Measured on a GB300, 8 heads of 128: 64 sequences of 100 to 8192 tokens 99 us (5.7 TB/s; a plain
 // copy 6.8), one of 131072 with 4 heads 57 us (4.7; the walk 36 to 41 us of it, 4 to start, 8 to join).
@@ -518,27 +518,26 @@ __global__ void __launch_bounds__(kThreads16) c16_step_kernel(const __grid_const
       if (tn < x_hi) issue(v_src, k_slot, more, off);
       cp_commit();
       const bool by_row = tok0 + TS > full_hi || tok0 < full_lo;
+      // which of the step's tokens row 8 n + 2 qd + r sees, a bit each
+      auto sees = [&](int n, int r) -> uint32_t {
+        if (!by_row) return bits;
+        const int32_t pos = x.q.start + (int32_t)div_g(p, r0 + 8u * n + 2u * qd + r);
+        // the first token that it sees no more, and the first that it sees, from the step's first on
+        const int32_t hi = pos < 0 ? 0 : p.causal ? min(max(pos + 1 - tok0, 0), TS) : TS;
+        const int32_t lo = p.window ? (int32_t)min(max((int64_t)pos - p.window + 1 - tok0, (int64_t)0), (int64_t)TS) : 0;
+        return bits & (uint32_t)((1ull << hi) - 1ull) & ~(uint32_t)((1ull << lo) - 1ull);
+      };
       if (by_row || bits != kFull) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            // keys that the row sees
-            int32_t hi = 0x7fffffff, lo = 0;
-            if (by_row) {
-              const int32_t pos = x.q.start + (int32_t)div_g(p, r0 + 8u * n + 2u * qd + r);
-              if (p.causal) hi = pos + 1;
-              if (p.window) lo = (int32_t)max((int64_t)0, (int64_t)pos - p.window + 1);
-              if (pos < 0) hi = 0;
-            }
+            const uint32_t seen = sees(n, r) >> g;
 #pragma unroll
             for (int h = 0; h < HT; ++h)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint32_t i = 16u * h + 8u * e + g;
-                const int32_t tok = tok0 + (int32_t)i;
-                if (!((bits >> i) & 1u) || tok >= hi || tok < lo) z[h][n][2 * e + r] = kNegInf;
-              }
+              for (int e = 0; e < 2; ++e)
+                if (!((seen >> (16 * h + 8 * e)) & 1u)) z[h][n][2 * e + r] = kNegInf;
           }
       }
       // running maxima; the sums are rescaled only where a maximum grew by more than kLag
@@ -620,15 +619,18 @@ __global__ void __launch_bounds__(kThreads16) c16_step_kernel(const __grid_const
               for (int t = 0; t < kTerms<DT>; ++t) mma16816<DT>(o[i][n], a, w[t][h][n][0], w[t][h][n][1]);
           }
       } else {
-        // such values become 0, and NaN is put where they are seen: rows x dims with one, counted by the same product
+        // Such values become 0, and NaN is put where they are seen: rows x dims with one, counted by the same product.  (Seen by
+        // the mask: a score of -inf weighs 0, and 0 times such a value is no number.)
 #pragma unroll
         for (int h = 0; h < HT; ++h) {
           uint32_t seen[NT][2];
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int n = 0; n < NT; ++n) {
+            const uint32_t s0 = sees(n, 0) >> (g + 16u * h), s1 = sees(n, 1) >> (g + 16u * h);
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              seen[n][e] = transpose8((z[h][n][2 * e] == kNegInf ? 0u : one) | (z[h][n][2 * e + 1] == kNegInf ? 0u : one << 16));
+              seen[n][e] = transpose8((((s0 >> (8 * e)) & 1u) ? one : 0u) | (((s1 >> (8 * e)) & 1u) ? one << 16 : 0u));
+          }
 #pragma unroll
           for (int i = 0; i < KS; ++i) {
             uint32_t a[4], b[4];
