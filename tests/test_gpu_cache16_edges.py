@@ -114,3 +114,91 @@ def test_rows_whose_scores_are_all_minus_infinity(new):
     q[..., 7] = 1.0
     _, out, lse = _attend(su, lens, new, 4, q=q)
     assert not out.any() and bool((lse == -math.inf).all())
+
+
+# ---------------------------------------------------------------- every key once
+def _counted(lens, new, *, D, H, T, G, dtype, layout="nhd", causal=True, window=0, seed=0):
+    """All scores 0 and V 1 in one dim, another every 16 tokens: lse is the logarithm of the number of keys, and out how often
+    each dim came up among them.  FP32 holds every sum exactly, so a lost or doubled step of any part shows."""
+    su = R.Setup(D=D, H=H, T=T, lens=lens, dtype=dtype, layout=layout, seed=seed)
+    top = max(lens)
+    for s, n in enumerate(lens):
+        j = torch.arange(n)
+        page, slot = su.tables[s].long()[j // T], j % T
+        su.pool[0][page, slot] = 0.0
+        for h in range(H):
+            one = torch.zeros(n, D, dtype=su.dtype)
+            one[j, (j // 16 + s + 3 * h) % D] = 1.0
+            su.pool[1][page, slot, h] = one
+    q, out, lse = _attend(su, lens, new, H * G, causal, window)
+    before = torch.zeros(top + 1, D, dtype=torch.int32)  # [j]: how often each dim came up in tokens below j of sequence 0, head 0
+    before[torch.arange(top) + 1, torch.arange(top) // 16 % D] = 1
+    before = before.cumsum(0).double()
+    half, least = torch.finfo(su.dtype).eps / 2, torch.finfo(su.dtype).tiny * torch.finfo(su.dtype).eps
+    row = 0
+    for s, c in enumerate(new if new is not None else [1] * len(lens)):
+        n, at = lens[s], torch.arange(lens[s] - c, lens[s])
+        hi = torch.where(at >= 0, at + 1 if causal else torch.full_like(at, n), 0)
+        lo = torch.minimum((at - window + 1).clamp(min=0), hi) if window else torch.zeros_like(at)
+        keys = (hi - lo).double()
+        got = lse[row:row + c]
+        want = torch.log(keys)[:, None].expand(c, H * G)
+        # log2f within two units of its last place, one rounding after it
+        assert torch.equal(torch.isneginf(got), torch.isneginf(want)), s
+        f = torch.isfinite(want)
+        assert bool(((got - want).abs()[f] <= want[f] * 2.0 ** -21 + 2.0 ** -22).all()), (s, float((got - want).abs()[f].max()))
+        for h in range(H):
+            o = out[row:row + c, h * G:h * G + G]
+            x = ((before[hi] - before[lo]) / keys.clamp(min=1)[:, None]).roll((s + 3 * h) % D, 1)[:, None]
+            # two FP32 roundings, one to the type
+            assert bool(((o - x).abs() <= x * (half + 2.0 ** -22) + least).all()), (s, h, float((o - x).abs().max()))
+        row += c
+
+
+@pytest.mark.parametrize("D,T,H,G,dtype,layout", [(32, 16, 3, 1, "fp16", "nhd"), (64, 5, 1, 16, "bf16", "hnd"),
+                                                  (128, 16, 2, 4, "bf16", "packed"), (256, 32, 1, 4, "fp16", "nhd")])
+def test_every_key_once_in_equal_shares(D, T, H, G, dtype, layout):
+    """More jobs than half the CTAs: shares that begin and end inside long jobs and go over many short ones."""
+    lens = [20000, 3, 0, 1, 900, 0, 0, 4097] + [1 + (7 * i) % 90 for i in range(200)] + [0, 15000]
+    for window in (0, 4000):
+        _counted(lens, None, D=D, H=H, T=T, G=G, dtype=dtype, layout=layout, window=window)
+
+
+@pytest.mark.parametrize("D,T,H,G,dtype", [(32, 16, 1, 8, "bf16"), (64, 24, 2, 2, "fp16"), (128, 16, 1, 20, "bf16"),
+                                           (256, 5, 2, 4, "fp16")])
+@pytest.mark.parametrize("lens", [[40001], [9000, 17, 0, 30000], [700, 20, 650, 81], [1000] * 36])
+def test_every_key_once_in_even_parts(D, T, H, G, dtype, lens):
+    _counted(lens, None, D=D, H=H, T=T, G=G, dtype=dtype)
+
+
+@pytest.mark.parametrize("D,T,H,G,dtype", [(32, 16, 2, 4, "bf16"), (64, 24, 1, 5, "fp16"), (128, 16, 1, 2, "fp16"),
+                                           (256, 16, 1, 16, "bf16")])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 333), (False, 0)])
+def test_every_key_once_for_drafts(D, T, H, G, dtype, causal, window):
+    lens, new = [9000, 5, 0, 3000, 777, 12], [4, 7, 2, 1, 40, 12]
+    _counted(lens, new, D=D, H=H, T=T, G=G, dtype=dtype, causal=causal, window=window)
+
+
+@pytest.mark.parametrize("D,T,H,G,dtype,layout", [(64, 16, 1, 8, "bf16", "packed"), (128, 16, 2, 4, "fp16", "nhd"),
+                                                  (32, 5, 1, 3, "fp16", "hnd"), (256, 16, 1, 2, "bf16", "packed")])
+@pytest.mark.parametrize("window", [0, 500])
+def test_every_key_once_for_prompts(D, T, H, G, dtype, layout, window):
+    """Prompts of thousands of tokens, one continued, next to a single token: thousands of tiles."""
+    _counted([3001, 1, 2500, 1777], [3001, 1, 2500, 600], D=D, H=H, T=T, G=G, dtype=dtype, layout=layout, window=window)
+
+
+@pytest.mark.parametrize("D,H,G,dtype", [(128, 2, 4, "bf16"), (64, 1, 7, "fp16")])
+def test_prompts_of_real_length(D, H, G, dtype):
+    """Values of every kind: rows at the ends of tiles and pages, and some between, against the definition."""
+    lens, new = [2600, 40, 1900], [2600, 40, 700]
+    su = R.Setup(D=D, H=H, T=16, lens=lens, dtype=dtype, seed=6, layout="packed")
+    su.fill()
+    q, out, lse = _attend(su, lens, new, H * G)
+    row = 0
+    for s, c in enumerate(new):
+        start = lens[s] - c
+        for i in sorted({0, 1, c - 1, c - 2} | {i for i in range(c) if (start + i) % 16 in (15, 0) and (start + i) % 400 < 32} |
+                        set(range(7, c, 331))):
+            want, wl, eo, el = su.attend(s, start + i + 1, q[row + i:row + i + 1])
+            assert bool(((out[row + i] - want[0]).abs() <= eo[0]).all()) and bool(((lse[row + i] - wl[0]).abs() <= el[0]).all()), (s, i)
+        row += c

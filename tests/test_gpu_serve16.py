@@ -41,6 +41,28 @@ def test_the_example_serves_offloads_and_goes_on():
     assert torch.equal(R.turn(r["prompt_q"].cpu().float(), pos, *tab, False).to(torch.bfloat16), r["prompt_turned"].cpu())
 
 
+def test_the_example_s_prompts_and_drafts(monkeypatch):
+    """What the example's calls outside its graph give, the prompts' and the drafts', is the attention over the pages as
+    they lie at that time."""
+    calls, attend = [], cache16.Cache16.attend
+
+    def kept(self, layer, batch, q, out, **kw):
+        attend(self, layer, batch, q, out, **kw)
+        if not torch.cuda.is_current_stream_capturing():
+            calls.append([x.cpu() for x in (batch.tables, batch.lens, batch.cu_new, q, out, layer.k, layer.v)])
+
+    monkeypatch.setattr(cache16.Cache16, "attend", kept)
+    _example().serve(3, 90, 20)
+    assert [c[3].shape[0] for c in calls] == [90 + 73 + 56, 3 * 4]
+    for tables, lens, cu, q, out, k, v in calls:
+        su = R.Setup(D=128, H=8, T=16, lens=lens.tolist(), dtype="bf16")
+        su.pool, su.tables, su.pages = [k.transpose(1, 2), v.transpose(1, 2)], tables, k.shape[0]
+        for s in range(3):
+            rows = slice(int(cu[s]), int(cu[s + 1]))
+            want, _, eo, _ = su.attend(s, int(lens[s]), q[rows])
+            assert bool(((out[rows].double() - want).abs() <= eo).all()), s
+
+
 def test_one_batch_serves_16_bit_and_8_bit_layers():
     """A model with layers of both kinds: one batch, one rotation and one workspace; prompts, then single tokens."""
     lens = [70, 33, 5]
