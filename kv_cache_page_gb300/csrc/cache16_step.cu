@@ -140,13 +140,16 @@ __device__ __forceinline__ float2 ld_join2(const float* ptr) {
 // Warps of a CTA, two of which share an SM: the start of a job and the joins of one hide behind
 // the other.  CTAs of 8 warps, one an SM: 64 uneven sequences 103 us against 101, 48 with one KV head 27 against 25.
 constexpr int kWarps = 4, kThreads16 = 32 * kWarps;
-// What a job costs its CTA besides its steps (its first copies, the joins), in steps: some 5 us.  Shares that did not
-// count it left CTAs with many short jobs three times as long as the others.  Of 8, 12, 16, 20, 24: 48 sequences with
-// one KV head 26.6, 26.5, 24.6, 24.6, 24.6 us, 64 uneven ones 102, 100, 101, 102, 102.
-constexpr uint32_t kStart = 16;
+// What a job costs its CTA besides its steps (its first copies, the joins), in steps; equal shares count it (even parts do not).
+// Shares that did not count it left CTAs with many short jobs three times as long as the others.  200 sequences of 10 to
+// 6000 tokens, 4 KV heads, with 4, 8, 12, 16, 20 and 24: head_dim 32 49, 41, 39, 41, 42, 44 us; 64 57, 47, 48, 50, 52, 55;
+// 128 89, 79, 79, 79, 80, 81; 256 154, 146, 148, 149, 151, 152.  So one number does for all; with 64 sequences of 100 to 8192
+// tokens or 256 of 200 to 1500 it makes 4 % at most from 8 to 16.
+constexpr uint32_t kStart = 12;
 constexpr uint32_t kLeast = kStart + 4;  // of a share
-// Partials that are joined at once; more are joined in groups.  One sequence of 131072, 4 heads, 76 partials: at once 64 us, in
-// groups of nine 58; 65536, 8 heads, 38 partials: 59 and 57; between 12 and 24 it makes no difference.
+// Partials that are joined at once; more are joined in groups.  One sequence of 131072 with 2 heads, 152 partials, at once and
+// in groups: head_dim 32 27 and 19 us, 64 33 and 25, 128 51 and 37, 256 96 and 63; with 4 heads, 76 partials: 31 and 28, 38 and
+// 35, 62 and 57, 116 and 102.  6, 12 or 24 makes no difference for any head_dim.
 constexpr uint32_t kFlat = 12;
 
 template <int D>
