@@ -60,8 +60,8 @@ extern "C" {
 #define KV_CACHE8_STALLED 2u  /* a wait inside the attention kernel ran out (of a sequence whose output is then
                                  unspecified; untold where errors is NULL); never seen in a sound run */
 
-#define KV_CACHE8_BAD_POSITION 4u /* append: a token's position is past the rotation's table; its key and its
-                                     queries are NaN */
+#define KV_CACHE8_BAD_POSITION 4u /* append: a token's position is past the rotation's table; the turned channels of
+                                     its key and its queries are NaN, the others as they were */
 
 /* Registered once per cache.  Strides are in bytes (= codes), the value stride
  * is 1, and every stride is a multiple of 16. */

@@ -116,7 +116,7 @@ class Cache16(_cache8._Cache):
         """The batch's new tokens (k, v: [n_new, num_kv_heads, head_dim]) into their pages, the keys turned by their
         positions (rotation None: as they are).  q, q_out ([n_new, num_q_heads, head_dim], both or neither): the tokens'
         queries, turned; q_out may be q itself.  Rows without a position get q_out = 0; those past the rotation's table
-        get NaN keys and queries, and BAD_POSITION; a token without a page is not written, and BAD_PAGE."""
+        get NaN in the turned channels of keys and queries, and BAD_POSITION; a token without a page is not written, and BAD_PAGE."""
         self._append_call(self._append, "kv_cache16_append", layer, batch, k, v, rotation, q, q_out, stream)
 
     def attend_workspace(self, batch: Batch) -> int:

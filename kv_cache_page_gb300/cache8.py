@@ -315,8 +315,8 @@ class Cache8(_Cache):
     def append(self, layer: Layer, batch: Batch, k, v, *, rotation: Optional[Rotation], q=None, q_out=None, stream=None):
         """``write`` with the keys turned by their positions on the way, quantised from float32 (rotation None: as they
         are).  q, q_out ([n_new, num_q_heads, head_dim], both or neither): the tokens' queries, turned and rounded to the
-        dtype; q_out may be q itself.  Rows without a position get q_out = 0; those past the rotation's table get NaN
-        keys and queries, and BAD_POSITION."""
+        dtype; q_out may be q itself.  Rows without a position get q_out = 0; those past the rotation's table get NaN in
+        the turned channels of keys and queries, and BAD_POSITION."""
         self._append_call(self._append, "kv_cache8_append", layer, batch, k, v, rotation, q, q_out, stream)
 
     def read(self, layer: Layer, batch: Batch, k, v, stream=None):

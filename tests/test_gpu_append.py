@@ -159,6 +159,20 @@ def test_positions_past_the_table_and_bad_pages(eight):
     assert errors.tolist() == [4, 4, 5, 0]
 
 
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("neighbours", [False, True])
+def test_positions_past_the_table_keep_what_is_not_turned(eight, neighbours):
+    """NaN in the turned channels alone."""
+    lens, new = [60, 55], [60, 5]
+    errors = torch.zeros(2, dtype=torch.int32, device=DEV)
+    tab, rotation = _rotation(48, neighbours, positions=50)
+    module, append = (R8, _append8) if eight else (R, _append16)
+    su = module.Setup(D=64, H=2, T=16, lens=lens, dtype="bf16", seed=2)
+    su.fill([0, 50])
+    append(su, lens, new, 4, 48, neighbours, tab=tab, rotation=rotation, errors=errors)
+    assert errors.tolist() == [4, 4]
+
+
 def test_signed_zeros_and_what_is_no_number():
     """Infinities and NaN stay in their pair and row; channels that are not turned keep their bits."""
     su = R.Setup(D=64, H=1, T=16, lens=[16], dtype="fp16")
