@@ -7,7 +7,7 @@
 // row's values first, and finds the row's sequence, position and page (three dependent
 // trips to memory) while these are on their way.  K, V and queries are one launch.
 // Measured on a GB300, 4 x 8192 tokens with 8 KV heads and 32 query heads of 128 in FP16: 125 us,
-// 6.5 TB/s (a plain copy 6.8).
+// 6.5 TB/s (a plain copy 6.7).
 #include "rotate.cuh"
 
 namespace kvc {

@@ -22,8 +22,8 @@
 // terms, two of FP16 or three of BF16, with a product for each, so that it keeps what FP32
 // arithmetic gave it (two BF16 terms were 0 to 3 % faster with 8 query rows, 3 to 7 with 16).
 //
-// Measured on a GB300, 8 heads of 128: 64 sequences of 100 to 8192 tokens 99 us (5.7 TB/s; a plain
-// copy 6.8), one of 131072 with 4 heads 57 us (4.7; the walk 36 to 41 us of it, 4 to start, 8 to join).
+// Measured on a GB300, 8 heads of 128: 64 sequences of 100 to 8192 tokens 99 to 103 us (5.7 TB/s; a
+// plain copy 6.7), one of 131072 with 4 heads 57 us (4.7; the walk 36 to 41 us of it, 4 to start, 8 to join).
 #include <algorithm>
 
 #include "cache8_common.cuh"

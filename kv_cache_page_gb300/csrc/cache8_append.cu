@@ -9,7 +9,7 @@
 // from L2.
 //
 // Bound by memory for whole prompts: 3 bytes a value of K and V, 4 of queries.  Measured on a GB300,
-// 4 x 8192 tokens with 8 KV heads and 32 query heads of 128 in BF16: 125 us, 5.9 TB/s (a plain copy 6.8).
+// 4 x 8192 tokens with 8 KV heads and 32 query heads of 128 in BF16: 125 to 127 us, 5.9 TB/s (a plain copy 6.7).
 #include "cache8_page.cuh"
 #include "rotate.cuh"
 
