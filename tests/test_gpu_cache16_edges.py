@@ -6,7 +6,6 @@ import torch
 
 import cache16_ref as R
 from cache16_cancel import PERIOD, SCALE, Cancel
-from kv_cache_page_gb300 import cache8, cache16
 from test_gpu_cache16 import _attend
 
 pytestmark = pytest.mark.gpu
